@@ -15,6 +15,9 @@ Formats (pages cited by title and section):
     16-point random Hadamard transform (transcript, cue 8).
   * Fused SwiGLU epilogue: SiLU(gate) * up -> row FWHT -> MXFP4 in one kernel
     ("Sub-4-Bit Microscaling", section 3, the online SiLU_and_Mul rotation).
+  * Paged key/value cache in NVFP4 or MXFP4: quantizing new tokens into it,
+    reading it back, attention over it (section 3, the rotated
+    NVFP4 KV cache).
 """
 from collections import namedtuple
 
@@ -22,9 +25,11 @@ import torch
 
 from . import _lib
 from ._lib import Fp4qError, load  # noqa: F401
+from ._kv import KvCache, kv_cache, kv_cache_attention, kv_cache_read, kv_cache_write
 
 __all__ = [
     "quantize_mxfp4", "quantize_nvfp4", "silu_mul_fwht_mxfp4", "fwht", "dequantize", "mxfp4_gemm",
+    "KvCache", "kv_cache", "kv_cache_write", "kv_cache_read", "kv_cache_attention",
     "workspace_bytes",
     "check_counters", "version", "MxResult", "NvResult", "Fp4qError",
 ]

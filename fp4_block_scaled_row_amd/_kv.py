@@ -1,0 +1,267 @@
+"""The paged key/value cache in 4 bits: quantizing new tokens into it, reading
+it back, and attention over it (the binding of fp4q_kv_* of include/fp4q.h).
+
+A cache is four uint8 planes of pages, [pages, kv_heads, page_size, bytes] in
+any memory order (a cache kept [pages, page_size, kv_heads, bytes] is passed
+as its .transpose(1, 2)): packed E2M1 codes, head_dim / 2 bytes a row, and
+block scales, head_dim / 16 E4M3 bytes for "nvfp4" or head_dim / 32 E8M0 bytes
+for "mxfp4".  NVFP4 keys and values each have one fp32 tensor scale g, fixed
+before the first token is written (quantize_nvfp4 of a calibration tensor
+returns one as global_scale).
+"""
+import torch
+
+from . import _lib
+
+__all__ = ["KvCache", "kv_cache", "kv_cache_write", "kv_cache_read", "kv_cache_attention"]
+
+_FORMATS = {"nvfp4": (_lib.FP4Q_NVFP4, 16), "mxfp4": (_lib.FP4Q_MXFP4, 32)}
+_DTYPES = {torch.float32: _lib.FP4Q_F32, torch.bfloat16: _lib.FP4Q_BF16}
+_ROTATIONS = {None: _lib.FP4Q_ROT_NONE, "none": _lib.FP4Q_ROT_NONE, "fwht128": _lib.FP4Q_ROT_FWHT128}
+
+
+class KvCache:
+    """A cache over planes that the caller owns.  Checked once, here; the
+    calls below take it as it is."""
+
+    def __init__(self, format, k_codes, k_scales, v_codes, v_scales, k_global=None, v_global=None):
+        if format not in _FORMATS:
+            raise ValueError("fp4q: a cache's format is 'nvfp4' or 'mxfp4', got %r" % (format,))
+        code, block = _FORMATS[format]
+        planes = (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales))
+        for what, t in planes:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError("fp4q: %s must be a GPU tensor" % what)
+            if t.dtype != torch.uint8 or t.dim() != 4:
+                raise ValueError("fp4q: %s must be uint8 [pages, kv_heads, page_size, bytes]" % what)
+            if t.device != k_codes.device:
+                raise ValueError("fp4q: the planes of a cache must be on one device")
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError("fp4q: rows of %s must be contiguous (stride(3) == 1)" % what)
+        pages, heads, page, half = k_codes.shape
+        scales = (pages, heads, page, half * 2 // block)
+        if half * 2 % 32 or v_codes.shape != k_codes.shape or tuple(k_scales.shape) != scales \
+                or v_scales.shape != k_scales.shape:
+            raise ValueError("fp4q: inconsistent cache planes: codes %s and %s, scales %s and %s" %
+                             tuple(tuple(t.shape) for t in (k_codes, v_codes, k_scales, v_scales)))
+        if k_codes.stride() != v_codes.stride() or k_scales.stride() != v_scales.stride():
+            raise ValueError("fp4q: key and value planes must have the same strides")
+        if format == "nvfp4":
+            for what, t in (("k_global", k_global), ("v_global", v_global)):
+                if not isinstance(t, torch.Tensor) or t.device != k_codes.device or t.dtype != torch.float32 \
+                        or t.numel() != 1:
+                    raise ValueError("fp4q: %s must be one float32 on the cache's device" % what)
+        else:
+            k_global = v_global = None
+        self.format, self.head_dim, self.kv_heads, self.page_size, self.num_pages = format, half * 2, heads, page, pages
+        self.device = k_codes.device
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_global, self.v_global = k_global, v_global
+        a = _lib.KvCacheArgs()
+        a.format, a.kv_heads, a.head_dim, a.page_size, a.num_pages = code, heads, half * 2, page, pages
+        for what, t in planes:
+            setattr(a, what, t.data_ptr())
+        if k_global is not None:
+            a.k_global, a.v_global = k_global.data_ptr(), v_global.data_ptr()
+        a.code_stride[:] = k_codes.stride()[:3]
+        a.scale_stride[:] = k_scales.stride()[:3]
+        self._args = a
+
+
+def kv_cache(num_pages, page_size, kv_heads, head_dim, *, format="nvfp4", k_global=1.0, v_global=1.0, device="cuda"):
+    """A zeroed cache, [pages, kv_heads, page_size, bytes] dense.  k_global,
+    v_global: the NVFP4 tensor scales, floats or one-element float32 tensors."""
+    if format not in _FORMATS:
+        raise ValueError("fp4q: a cache's format is 'nvfp4' or 'mxfp4', got %r" % (format,))
+    if head_dim % 32:
+        raise ValueError("fp4q: head_dim must be a multiple of 32, got %d" % head_dim)
+    block = _FORMATS[format][1]
+    widths = (head_dim // 2, head_dim // block) * 2
+    planes = [torch.zeros((num_pages, kv_heads, page_size, w), dtype=torch.uint8, device=device) for w in widths]
+    if format == "mxfp4":
+        return KvCache(format, *planes)
+    scales = [g if isinstance(g, torch.Tensor) else torch.full((1,), float(g), device=device)
+              for g in (k_global, v_global)]
+    return KvCache(format, *planes, *scales)
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _rotation(rotation):
+    try:
+        return _ROTATIONS[rotation]
+    except KeyError:
+        raise ValueError("fp4q: a cache's rotation is None or 'fwht128', got %r" % (rotation,)) from None
+
+
+def _rows(t, what, cache, heads):
+    """A [tokens, heads, head_dim] tensor of fp32 or bf16 on the cache's device."""
+    if not isinstance(t, torch.Tensor) or t.device != cache.device:
+        raise ValueError("fp4q: %s must be a tensor on the cache's device" % what)
+    if t.dtype not in _DTYPES:
+        raise TypeError("fp4q: %s must be float32 or bfloat16, got %s" % (what, t.dtype))
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads and t.shape[1] != heads):
+        raise ValueError("fp4q: %s must be [tokens, %s, %d], got %s" %
+                         (what, heads or "heads", cache.head_dim, tuple(t.shape)))
+    if t.stride(2) != 1:
+        raise ValueError("fp4q: rows of %s must be contiguous (stride(2) == 1)" % what)
+
+
+def _index(t, what, cache, dtype, dims):
+    if not isinstance(t, torch.Tensor) or t.device != cache.device or t.dtype != dtype or t.dim() != dims:
+        raise ValueError("fp4q: %s must be a %d-D %s tensor on the cache's device" % (what, dims, dtype))
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("fp4q: %s must be contiguous along its last dimension" % what)
+
+
+def kv_cache_write(cache, k, v, slots, *, rotation=None):
+    """Quantize new tokens' keys and values, [tokens, kv_heads, head_dim] fp32
+    or bf16 (any 16-byte aligned token and head strides, e.g. slices of a
+    projection), into the cache.
+
+    slots: int64 [tokens], page * page_size + offset of each token; a token
+    whose slot lies outside the cache (a negative one, say) is skipped, and no
+    two tokens of a call share a slot.  rotation "fwht128" stores the keys in
+    the basis of the normalised Hadamard transform of each 128 elements
+    (head_dim a multiple of 128); pass the same to kv_cache_attention and
+    kv_cache_read.  The bytes are those of quantize_nvfp4 / quantize_mxfp4."""
+    _rows(k, "k", cache, cache.kv_heads)
+    _rows(v, "v", cache, cache.kv_heads)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("fp4q: k and v must have the same shape and dtype")
+    _index(slots, "slots", cache, torch.int64, 1)
+    if slots.shape[0] != k.shape[0]:
+        raise ValueError("fp4q: slots must have one entry a token")
+    a = _lib.KvWriteArgs()
+    a.tokens = k.shape[0]
+    a.k, a.v, a.slots = k.data_ptr(), v.data_ptr(), slots.data_ptr()
+    a.k_stride[0], a.k_stride[1], _ = k.stride()
+    a.v_stride[0], a.v_stride[1], _ = v.stride()
+    a.in_dtype, a.rotation = _DTYPES[k.dtype], _rotation(rotation)
+    with torch.cuda.device(cache.device):
+        _lib.check(_lib.load().fp4q_kv_write(cache._args, a, _stream(cache.device)), "fp4q_kv_write")
+
+
+def kv_cache_read(cache, page_table, cu, *, total, starts=None, rotation=None, out_dtype=torch.bfloat16, out=None):
+    """The values that the cache holds of runs of tokens: (k, v), each [total,
+    kv_heads, head_dim] in out_dtype.
+
+    page_table: int32 [seqs, pages]; cu: int32 [seqs + 1], output rows cu[b]
+    to cu[b + 1] - 1 are tokens starts[b] (0 without starts, int32 [seqs])
+    onwards of sequence b; total: rows of the output.  Keys written with a
+    rotation come back in their original basis when it is given here.  out: a
+    pair of buffers to write, either of them None to leave it out."""
+    _index(page_table, "page_table", cache, torch.int32, 2)
+    _index(cu, "cu", cache, torch.int32, 1)
+    seqs = page_table.shape[0]
+    if cu.shape[0] != seqs + 1:
+        raise ValueError("fp4q: cu must have one entry more than page_table has rows")
+    if starts is not None:
+        _index(starts, "starts", cache, torch.int32, 1)
+        if starts.shape[0] != seqs:
+            raise ValueError("fp4q: starts must have one entry a sequence")
+    if out_dtype not in _DTYPES:
+        raise TypeError("fp4q: out_dtype must be float32 or bfloat16, got %s" % out_dtype)
+    shape = (int(total), cache.kv_heads, cache.head_dim)
+    if out is None:
+        out = (torch.empty(shape, dtype=out_dtype, device=cache.device),
+               torch.empty(shape, dtype=out_dtype, device=cache.device))
+    else:
+        for t in out:
+            if t is not None and (t.device != cache.device or t.dtype != out_dtype or tuple(t.shape) != shape
+                                  or not t.is_contiguous()):
+                raise ValueError("fp4q: out must be contiguous %s tensors of shape %s" % (out_dtype, shape))
+    a = _lib.KvReadArgs()
+    a.page_table, a.table_stride = page_table.data_ptr(), page_table.stride(0)
+    a.table_cols, a.seqs, a.cu, a.total = page_table.shape[1], seqs, cu.data_ptr(), shape[0]
+    if seqs <= 1:
+        a.table_stride = max(a.table_stride, a.table_cols)
+    a.starts = None if starts is None else starts.data_ptr()
+    a.k_out, a.v_out = (None if t is None else t.data_ptr() for t in out)
+    a.out_dtype, a.rotation = _DTYPES[out_dtype], _rotation(rotation)
+    with torch.cuda.device(cache.device):
+        _lib.check(_lib.load().fp4q_kv_read(cache._args, a, _stream(cache.device)), "fp4q_kv_read")
+    return out
+
+
+# One workspace per (device, stream), grown as calls need it: calls on one
+# stream are ordered, and a call leaves nothing in it.
+_workspaces = {}
+
+
+def _workspace(device, stream, need):
+    ws = _workspaces.get((device, stream))
+    if ws is None or ws.numel() < need:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("fp4q: the workspace of this stream is missing or too small; pass workspace= or make "
+                               "one call of this size on the stream before capturing it")
+        ws = _workspaces[(device, stream)] = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws
+
+
+def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None, scale=None, causal=True, window=0,
+                       rotation=None, out=None, return_lse=False, workspace=None):
+    """softmax(scale q k^T) v over the cache: q [total, q_heads, head_dim],
+    fp32 or bf16, q_heads a multiple of the cache's heads (consecutive query
+    heads share one); head_dim 64, 96, 128 or 256.
+
+    page_table: int32 [seqs, pages]; seq_lens: int32 [seqs], the tokens in the
+    cache, new ones among them.  Without cu_q each sequence has one query;
+    with cu_q (int32 [seqs + 1]) sequence b's are rows cu_q[b] to
+    cu_q[b + 1] - 1, at most max_q (default: all rows) in any.  causal: query
+    i of m sees token j <= n - m + i of the n; window > 0: only the last
+    `window` of them.  scale: 1 / sqrt(head_dim) by default.  rotation: as the
+    keys were written.
+
+    Returns out [total, q_heads, head_dim] in q's dtype, or (out, lse) with
+    the fp32 log-sum-exps [total, q_heads].  A query that sees no token gives
+    zeros and -inf.  Nothing waits for the GPU: lengths and tables are read
+    there, so a captured call may be replayed with others in place."""
+    _rows(q, "q", cache, 0)
+    _index(page_table, "page_table", cache, torch.int32, 2)
+    _index(seq_lens, "seq_lens", cache, torch.int32, 1)
+    seqs, total, q_heads = page_table.shape[0], q.shape[0], q.shape[1]
+    if seq_lens.shape[0] != seqs:
+        raise ValueError("fp4q: seq_lens must have one entry a sequence")
+    if cu_q is None:
+        if total != seqs:
+            raise ValueError("fp4q: without cu_q, q must have one row a sequence")
+    else:
+        _index(cu_q, "cu_q", cache, torch.int32, 1)
+        if cu_q.shape[0] != seqs + 1:
+            raise ValueError("fp4q: cu_q must have one entry more than there are sequences")
+    if out is None:
+        out = torch.empty((total, q_heads, cache.head_dim), dtype=q.dtype, device=cache.device)
+    elif out.device != cache.device or out.dtype != q.dtype or tuple(out.shape) != tuple(q.shape) \
+            or not out.is_contiguous():
+        raise ValueError("fp4q: out must be a contiguous %s tensor of shape %s" % (q.dtype, tuple(q.shape)))
+    a = _lib.KvAttentionArgs()
+    a.q, a.out, a.total_q, a.q_heads, a.dtype = q.data_ptr(), out.data_ptr(), total, q_heads, _DTYPES[q.dtype]
+    a.q_stride[0], a.q_stride[1], _ = q.stride()
+    lse = None
+    if return_lse:
+        lse = torch.empty((total, q_heads), dtype=torch.float32, device=cache.device)
+        a.lse = lse.data_ptr()
+    if cu_q is not None:
+        a.cu_q = cu_q.data_ptr()
+        a.max_q = total if max_q is None else int(max_q)
+    a.seq_lens, a.page_table, a.table_stride = seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0)
+    a.table_cols, a.seqs = page_table.shape[1], seqs
+    if seqs <= 1:
+        a.table_stride = max(a.table_stride, a.table_cols)
+    a.causal, a.window, a.rotation = int(bool(causal)), int(window), _rotation(rotation)
+    a.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    lib = _lib.load()
+    with torch.cuda.device(cache.device):
+        stream = _stream(cache.device)
+        if workspace is None:
+            need = lib.fp4q_kv_attention_workspace_bytes(cache._args, a)
+            workspace = _workspace(cache.device, stream, need) if need else None
+        elif not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("fp4q: the workspace must be a contiguous GPU tensor")
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _lib.check(lib.fp4q_kv_attention(cache._args, a, None if workspace is None else workspace.data_ptr(), size,
+                                         stream), "fp4q_kv_attention")
+    return (out, lse) if return_lse else out

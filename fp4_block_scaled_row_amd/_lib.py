@@ -23,7 +23,9 @@ FP4Q_ROT_NONE, FP4Q_ROT_FWHT_ROW, FP4Q_ROT_RHT16, FP4Q_ROT_FWHT128 = 0, 1, 2, 3
 EXPORTED = [
     "fp4q_workspace_bytes", "fp4q_quantize_mxfp4", "fp4q_quantize_nvfp4", "fp4q_quantize_nvfp4_noalloc",
     "fp4q_silu_mul_fwht_mxfp4", "fp4q_fwht",
-    "fp4q_dequantize", "fp4q_mxfp4_gemm", "fp4q_check_counters", "fp4q_status_string", "fp4q_version",
+    "fp4q_dequantize", "fp4q_mxfp4_gemm",
+    "fp4q_kv_write", "fp4q_kv_read", "fp4q_kv_attention", "fp4q_kv_attention_workspace_bytes",
+    "fp4q_check_counters", "fp4q_status_string", "fp4q_version",
 ]
 
 
@@ -40,6 +42,42 @@ class Outputs(C.Structure):
     _fields_ = [
         ("codes", C.c_void_p), ("scales", C.c_void_p), ("global_scale", C.c_void_p),
         ("choice_bits", C.c_void_p), ("rotated", C.c_void_p), ("counters", C.c_void_p),
+    ]
+
+
+class KvCacheArgs(C.Structure):
+    _fields_ = [
+        ("format", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32),
+        ("num_pages", C.c_int64),
+        ("k_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_codes", C.c_void_p), ("v_scales", C.c_void_p),
+        ("k_global", C.c_void_p), ("v_global", C.c_void_p),
+        ("code_stride", C.c_int64 * 3), ("scale_stride", C.c_int64 * 3),
+    ]
+
+
+class KvWriteArgs(C.Structure):
+    _fields_ = [
+        ("tokens", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p),
+        ("k_stride", C.c_int64 * 2), ("v_stride", C.c_int64 * 2), ("slots", C.c_void_p),
+        ("in_dtype", C.c_int32), ("rotation", C.c_int32),
+    ]
+
+
+class KvReadArgs(C.Structure):
+    _fields_ = [
+        ("page_table", C.c_void_p), ("table_stride", C.c_int64), ("table_cols", C.c_int32), ("seqs", C.c_int32),
+        ("cu", C.c_void_p), ("starts", C.c_void_p), ("total", C.c_int64),
+        ("k_out", C.c_void_p), ("v_out", C.c_void_p), ("out_dtype", C.c_int32), ("rotation", C.c_int32),
+    ]
+
+
+class KvAttentionArgs(C.Structure):
+    _fields_ = [
+        ("q", C.c_void_p), ("q_stride", C.c_int64 * 2), ("out", C.c_void_p), ("lse", C.c_void_p),
+        ("cu_q", C.c_void_p), ("seq_lens", C.c_void_p), ("page_table", C.c_void_p), ("table_stride", C.c_int64),
+        ("total_q", C.c_int64), ("table_cols", C.c_int32), ("seqs", C.c_int32), ("max_q", C.c_int32),
+        ("q_heads", C.c_int32), ("dtype", C.c_int32), ("causal", C.c_int32), ("window", C.c_int32),
+        ("rotation", C.c_int32), ("scale", C.c_float),
     ]
 
 
@@ -80,6 +118,15 @@ def load():
         lib.fp4q_dequantize.restype = C.c_int
         lib.fp4q_mxfp4_gemm.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, vp, vp]
         lib.fp4q_mxfp4_gemm.restype = C.c_int
+        kvp = C.POINTER(KvCacheArgs)
+        lib.fp4q_kv_write.argtypes = [kvp, C.POINTER(KvWriteArgs), vp]
+        lib.fp4q_kv_write.restype = C.c_int
+        lib.fp4q_kv_read.argtypes = [kvp, C.POINTER(KvReadArgs), vp]
+        lib.fp4q_kv_read.restype = C.c_int
+        lib.fp4q_kv_attention_workspace_bytes.argtypes = [kvp, C.POINTER(KvAttentionArgs)]
+        lib.fp4q_kv_attention_workspace_bytes.restype = C.c_size_t
+        lib.fp4q_kv_attention.argtypes = [kvp, C.POINTER(KvAttentionArgs), vp, C.c_size_t, vp]
+        lib.fp4q_kv_attention.restype = C.c_int
         lib.fp4q_check_counters.argtypes = [vp]
         lib.fp4q_check_counters.restype = C.c_int
         lib.fp4q_status_string.argtypes = [C.c_int]

@@ -1,0 +1,647 @@
+// fp4q_kv_attend.h -- attention over the paged 4-bit cache: what its kernels
+// share.
+//
+//   o_i = sum_j softmax_j(scale q_i . k_j) v_j over the tokens j that query i
+// of a sequence with n cached tokens and m queries sees: j < n, and causal:
+// j <= n - m + i, with a window also j > n - m + i - window.
+//
+// Types.  NVFP4 values (E2M1 times E4M3, 6 significant bits, 2^-10 to 2688)
+// and MXFP4 values (E2M1 times a power of two) are exact in fp16 and bf16, so
+// the cache enters the matrix instructions without any rounding: NVFP4 in
+// fp16 (one packed product per two values), MXFP4 in bf16 (the conversion
+// applies the scale).  The tensor scales are applied in fp32, the keys' to
+// the scores and the values' to the output.
+//   The queries enter as a sum of kQ pieces in that type, each the rounding of
+// what the ones before left: a bf16 query is exact in one piece, a rotated one
+// keeps 16 (bf16) or 22 (fp16) bits in two, an fp32 one 22 to 24.  fp16 pieces
+// are scaled by a power of two per row that puts the row's largest value in
+// [2^8, 2^9).  The softmax weights enter in kP pieces: one (2^-12 in fp16,
+// 2^-9 in bf16 relative to the weight, below the bf16 output's own rounding)
+// for bf16 outputs, two for fp32 outputs.  Scores, maxima, weights' sums and
+// outputs are held in fp32.
+//
+// Layout in the matrix instructions.  Scores are formed transposed, keys as
+// the left operand and queries as the right one, so that a lane ends up with
+// the weights of one query row for tokens that are also the ones it has to
+// supply to the second product: weights go from one instruction to the other
+// in registers.  The order of head elements inside the first contraction is
+// free; it is chosen so that a lane's codes are contiguous bytes.  The values
+// go through LDS, whose transposing read gives a lane 4 tokens of one element.
+//
+// Running maximum.  A row's maximum is raised only when a score exceeds it by
+// more than 8 (in powers of two); until then weights are at most 2^8, which
+// fp32 and the pieces' types hold.  So the common step has no exchange between
+// lanes and no rescaling.  Sums of weights stay in their lanes to the end.
+#pragma once
+
+#include "fp4q_kv.h"
+
+namespace fp4q {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -0x1p126f;       // a maximum before any score
+constexpr float kRaise = 8.0f;            // slack of the running maximum
+
+// The element type of a format's matrix products: fp16 for NVFP4 (FMT 1),
+// bf16 for MXFP4 (FMT 0).  Weights carry a factor 2^kUp that makes use of
+// fp16's range (at most 2^(kUp + kRaise) = 2^15; down to 2^-31 of the maximum).
+template <int FMT>
+struct KvType;
+template <>
+struct KvType<0> {
+  static constexpr float kUp = 0.0f;
+  static __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const bf16x2_t p = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, p);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return bf_lo(w); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return bf_hi(w); }
+};
+template <>
+struct KvType<1> {
+  static constexpr float kUp = 7.0f;
+  static __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+  }
+  static __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const f16x2_t p = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, p);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(f16x2_t, w)[0]; }
+  static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(f16x2_t, w)[1]; }
+};
+
+// Pieces of a pair of fp32 values: out[0] their rounding, out[1] the rounding
+// of the rest, and so on.
+template <int FMT, int N>
+__device__ __forceinline__ void pieces(float a, float b, uint32_t out[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    out[i] = KvType<FMT>::pack(a, b);
+    if (i + 1 < N) {
+      a -= KvType<FMT>::lo(out[i]);
+      b -= KvType<FMT>::hi(out[i]);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
+// What a lane reads of one plane row.  The lanes of group g = lane / 16 hold
+// the elements e(c, g) .. + 7 of every 32-element chunk c: with head_dim 64
+// or a multiple of 128 they are one run of head_dim / 4 elements (kRun), so
+// that the codes are one wide load and the scales one load too; with others
+// 8 elements of each chunk.
+template <int FMT, int D>
+struct KvLane {
+  static constexpr int kChunks = D / 32;
+  static constexpr bool kRun = D == 64 || D % 128 == 0;
+  static constexpr int kBlock = FMT == 0 ? 32 : 16;
+  // scale bytes of a lane: its run's blocks, or one byte a chunk
+  static constexpr int kScales = kRun ? (D / 4 >= kBlock ? D / 4 / kBlock : 1) : kChunks;
+  static __device__ __forceinline__ int element(int c, int g) { return kRun ? g * (D / 4) + 8 * c : 32 * c + 8 * g; }
+
+  uint32_t codes[kChunks];
+  uint32_t scales;                         // kScales bytes (at most 4)
+
+  __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* srow, int g) {
+    if constexpr (kRun) {
+      const uint8_t* p = row + g * (D / 8);
+      if constexpr (kChunks == 2) {
+        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+        codes[0] = w.x;
+        codes[1] = w.y;
+      } else {
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 4) {
+          const u32x4_t w = *reinterpret_cast<const u32x4_t*>(p + 4 * c);
+          codes[c] = w.x;
+          codes[c + 1] = w.y;
+          codes[c + 2] = w.z;
+          codes[c + 3] = w.w;
+        }
+      }
+      const uint8_t* q = srow + (g * (D / 4)) / kBlock;
+      if constexpr (kScales == 1) scales = *q;
+      else if constexpr (kScales == 2) scales = *reinterpret_cast<const uint16_t*>(q);
+      else scales = *reinterpret_cast<const uint32_t*>(q);
+    } else {
+      scales = 0u;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        codes[c] = *reinterpret_cast<const uint32_t*>(row + 16 * c + 4 * g);
+        scales |= (uint32_t)srow[FMT == 0 ? c : 2 * c + (g >> 1)] << (8 * c);
+      }
+    }
+  }
+  // Which of the scale bytes chunk c takes.
+  static __device__ __forceinline__ constexpr int scale_of(int c) { return kRun ? (8 * c) / kBlock : c; }
+
+  // Scale bytes of blocks that are no finite numbers: NVFP4's NaN code; for
+  // MXFP4 253 and more, which no finite input is stored with (its largest
+  // exponent less 2 is 252) and whose values pass bf16's range.
+  static __device__ __forceinline__ bool not_finite(uint32_t b) { return FMT == 0 ? b >= 253u : (b & 0x7Fu) == 0x7Fu; }
+  // Makes such blocks zero and says whether there were any.
+  __device__ __forceinline__ bool drop_not_finite() {
+    uint32_t keep = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) keep &= not_finite((scales >> (8 * i)) & 0xFFu) ? ~(0xFFu << (8 * i)) : 0xFFFFFFFFu;
+    scales &= keep;
+    if constexpr (FMT == 0) {      // (scale byte 0 is 2^-127, not 0)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) codes[c] = (keep >> (8 * scale_of(c))) & 1u ? codes[c] : 0u;
+    }
+    return keep != 0xFFFFFFFFu;
+  }
+  // Zeros in place of what was loaded (a token that is not there).
+  __device__ __forceinline__ void keep_if(bool there) {
+    scales = there ? scales : 0u;
+    if constexpr (FMT == 0) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) codes[c] = there ? codes[c] : 0u;
+    }
+  }
+  // All scale bytes prepared for values(): NVFP4's as fp16 pairs.
+  struct Scales {
+    uint32_t h[FMT == 0 ? 1 : (kScales + 1) / 2];
+  };
+  __device__ __forceinline__ Scales prepare() const {
+    Scales s;
+    if constexpr (FMT == 0) {
+      s.h[0] = scales;
+    } else {
+      const int b = (int)(scales & 0x7F7F7F7Fu);   // (bit 7 means nothing in an NVFP4 scale)
+      s.h[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false));
+      if constexpr (kScales > 2)
+        s.h[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true));
+    }
+    return s;
+  }
+  // The 8 values of chunk c in the products' type, low elements first.
+  __device__ __forceinline__ u32x4_t values(int c, const Scales& s) const {
+    const int i = scale_of(c);
+    u32x4_t o;
+    if constexpr (FMT == 0) {
+      const uint32_t b = (s.h[0] >> (8 * i)) & 0xFFu;
+      const float sc = e8m0_operand(b);
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[c], sc, 0));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[c], sc, 1));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[c], sc, 2));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[c], sc, 3));
+      if (not_finite(b)) o = u32x4_t{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+    } else {
+      const f16x2_t pair = __builtin_bit_cast(f16x2_t, s.h[i / 2]);
+      const _Float16 one = pair[i % 2];
+      const f16x2_t sc = {one, one};
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], 1.0f, 0) * sc);
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], 1.0f, 1) * sc);
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], 1.0f, 2) * sc);
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], 1.0f, 3) * sc);
+    }
+    return o;
+  }
+};
+
+// Where the rows of a token are, in the planes of one cache head (the lane's
+// own part of a row included): a lane's token is found by its page number and
+// offset with two 64-bit multiply-adds a plane pair.
+struct KvHead {
+  const uint8_t *kc, *ks, *vc, *vs;
+};
+__device__ __forceinline__ KvHead kv_head(const KvPlanes& p, int head) {
+  KvHead h;
+  const uint64_t c = (uint64_t)head * p.code_stride[1], s = (uint64_t)head * p.scale_stride[1];
+  h.kc = p.kc + c;
+  h.vc = p.vc + c;
+  h.ks = p.ks + s;
+  h.vs = p.vs + s;
+  return h;
+}
+struct KvAt {
+  uint64_t code, scale;
+};
+__device__ __forceinline__ KvAt kv_at(const KvPlanes& p, uint32_t page, uint32_t offset) {
+  KvAt a;
+  a.code = (uint64_t)page * p.code_stride[0] + (uint64_t)offset * p.code_stride[2];
+  a.scale = (uint64_t)page * p.scale_stride[0] + (uint64_t)offset * p.scale_stride[2];
+  return a;
+}
+
+// Four tokens of one element a lane: lane l of each 16 gives the address of
+// tokens' row l / 4, elements 4 (l % 4) .. + 3, and gets element l of rows 0-3.
+__device__ __forceinline__ u32x2_t read_transposed(const uint16_t* p) {
+  const s16x4_t r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4_t*)(__attribute__((address_space(3))) void*)p);
+  return __builtin_bit_cast(u32x2_t, r);
+}
+
+// ----------------------------------------------------------------------------
+// The schedule.  A unit is one block of kRows query rows (row r of a sequence:
+// query r / group, head r % group of its cache head) of one sequence and cache
+// head; it has to go through the groups of kTokens tokens that any of its rows
+// sees.  The groups of all units are numbered through, (sequence, block)
+// first, then cache head, and workgroup w of W takes the w-th stretch of equal
+// length: whatever the lengths are, all have the same to do.  Blocks are found
+// by numbers too: block k of sequence b has the number cu[b] group / kRows + b
+// + k (rounded down), which leaves room for each sequence's blocks and skips
+// at most one number a sequence, so that a thread finds a number's sequence by
+// bisection and no list has to be built.
+struct KvUnit {
+  int b, block, blocks;   // sequence, block of its query rows, its blocks
+  int head;               // cache head
+  int row0;               // first query row
+  int q0, m, n;           // first row of q, queries, cached tokens
+  int lo, hi;             // tokens that some row of the block sees
+  int groups;             // at least 1: rows without tokens are written too
+};
+
+// Row of q of sequence b's first query (never past the rows there are).
+__device__ __forceinline__ int kv_first_query(const KvAttendLaunch& a, int b) {
+  const int q = a.cu_q ? a.cu_q[b] : b;
+  return q < 0 ? 0 : (q > (int)a.total_q ? (int)a.total_q : q);
+}
+
+template <int kRows>
+__device__ __forceinline__ int64_t kv_block_number(const KvAttendLaunch& a, int b) {
+  return (int64_t)kv_first_query(a, b) * a.group / kRows + b;
+}
+
+template <int kRows, int kTokens>
+__device__ __forceinline__ void kv_sequence(const KvAttendLaunch& a, int b, KvUnit& u) {
+  u.b = b;
+  u.q0 = kv_first_query(a, b);
+  u.m = kv_first_query(a, b + 1) - u.q0;
+  const int len = a.lens[b];
+  u.n = len < 0 ? 0 : (len > a.most_tokens ? (int)a.most_tokens : len);
+  u.blocks = u.m > 0 ? (int)(((int64_t)u.m * a.group + kRows - 1) / kRows) : 0;
+}
+
+template <int kRows, int kTokens>
+__device__ __forceinline__ void kv_block(const KvAttendLaunch& a, int block, KvUnit& u) {
+  u.block = block;
+  u.row0 = block * kRows;
+  const int i0 = (int)quotient((uint32_t)u.row0, a.group_div);
+  const int i1 = min((int)quotient((uint32_t)(u.row0 + kRows - 1), a.group_div), u.m - 1);
+  const int64_t past = (int64_t)u.n - u.m;    // tokens before the first query's (may be negative)
+  const int64_t hi = a.causal ? past + i1 + 1 : u.n;
+  const int64_t lo = a.window > 0 ? past + i0 + 1 - a.window : 0;
+  u.hi = (int)(hi < 0 ? 0 : hi);
+  u.lo = (int)(lo < 0 ? 0 : (lo > u.hi ? u.hi : lo));
+  u.groups = max(1, (u.hi - u.lo + kTokens - 1) / kTokens);
+}
+
+// Block number -> sequence and block; false: a skipped number.
+template <int kRows, int kTokens>
+__device__ __forceinline__ bool kv_numbered(const KvAttendLaunch& a, int64_t number, KvUnit& u) {
+  int lo = 0, hi = a.seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (kv_block_number<kRows>(a, mid) <= number) lo = mid;
+    else hi = mid;
+  }
+  kv_sequence<kRows, kTokens>(a, lo, u);
+  const int64_t block = number - kv_block_number<kRows>(a, lo);
+  if (block < 0 || block >= u.blocks) return false;
+  kv_block<kRows, kTokens>(a, (int)block, u);
+  return true;
+}
+
+// A workgroup's stretch: `left` groups from group `group` of unit `u` on.
+struct KvStretch {
+  KvUnit u;
+  int group;
+  int64_t left;
+};
+
+// Every thread of the workgroup calls it, with all query block numbers below
+// `numbers`; scratch: 8 + 2 waves words of LDS.  False: nothing to do.
+template <int kRows, int kTokens, int kThreadsWg>
+__device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numbers, KvStretch& st, long long* scratch) {
+  constexpr int kW = kThreadsWg / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t each = (numbers + kThreadsWg - 1) / kThreadsWg;
+  const int64_t x0 = tid * each, x1 = x0 + each < numbers ? x0 + each : numbers;
+  long long mine = 0;
+  for (int64_t x = x0; x < x1; ++x) {
+    KvUnit u;
+    if (kv_numbered<kRows, kTokens>(a, x, u)) mine += (long long)u.groups * a.p.heads;
+  }
+  long long upto = mine;     // inclusive scan over the workgroup
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const long long x = __shfl_up(upto, o, 64);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 63) scratch[wave] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    if (w < wave) upto += scratch[w];
+    total += scratch[w];
+  }
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long begin = share * blockIdx.x;
+  if (begin >= total) return false;
+  long long before = upto - mine;
+  if (begin >= before && begin < upto) {
+    KvUnit u;
+    for (int64_t x = x0; x < x1; ++x) {
+      if (!kv_numbered<kRows, kTokens>(a, x, u)) continue;
+      const long long here = (long long)u.groups * a.p.heads;
+      if (begin < before + here) break;
+      before += here;
+    }
+    scratch[kW] = u.b;
+    scratch[kW + 1] = u.block;
+    scratch[kW + 2] = begin - before;
+  }
+  __syncthreads();
+  const int b = __builtin_amdgcn_readfirstlane((int)scratch[kW]);
+  const int block = __builtin_amdgcn_readfirstlane((int)scratch[kW + 1]);
+  const int64_t in_block = scratch[kW + 2];
+  kv_sequence<kRows, kTokens>(a, b, st.u);
+  kv_block<kRows, kTokens>(a, block, st.u);
+  st.u.head = __builtin_amdgcn_readfirstlane((int)(in_block / st.u.groups));
+  st.group = __builtin_amdgcn_readfirstlane((int)(in_block - (int64_t)st.u.head * st.u.groups));
+  st.left = total - begin < share ? total - begin : share;
+  return true;
+}
+
+// The next unit (there is one while groups are left).
+template <int kRows, int kTokens>
+__device__ __forceinline__ void kv_next(const KvAttendLaunch& a, KvUnit& u) {
+  if (++u.head < a.p.heads) return;
+  u.head = 0;
+  int block = u.block + 1;
+  while (block >= u.blocks && u.b + 1 < a.seqs) {
+    kv_sequence<kRows, kTokens>(a, u.b + 1, u);
+    block = 0;
+  }
+  kv_block<kRows, kTokens>(a, block, u);
+}
+
+// Numbers of all query blocks lie below this.
+template <int kRows>
+inline int64_t kv_block_numbers(const KvAttendLaunch& a) {
+  return a.total_q * a.group / kRows + a.seqs;
+}
+
+// What a workgroup leaves in the workspace: a header saying which units it
+// shares with its neighbours, and for either end of its stretch the partial
+// result of that unit: kRows x D weighted values, kRows maxima, kRows sums.
+//   first: 0 none, 1 a piece of a unit that began before, 2 its last piece
+//   last:  1 the first piece of a unit that goes on in the next workgroup
+struct KvShared {
+  int32_t first, last, b, head, row0, pad0, pad1, pad2;
+};
+__device__ __forceinline__ KvShared* kv_shared(const KvAttendLaunch& a) {
+  return reinterpret_cast<KvShared*>(a.ws);
+}
+template <int D, int kRows>
+__device__ __forceinline__ float* kv_partial(const KvAttendLaunch& a, int64_t workgroups, int64_t workgroup, bool last) {
+  return reinterpret_cast<float*>(a.ws + workgroups * sizeof(KvShared)) +
+         (2 * workgroup + (last ? 1 : 0)) * (int64_t)kRows * (D + 2);
+}
+inline size_t kv_partial_bytes(int64_t workgroups, int64_t rows, int64_t head_dim) {
+  return (size_t)workgroups * (sizeof(KvShared) + 2 * rows * (head_dim + 2) * sizeof(float));
+}
+
+// Query head and row of q of row rr of a sequence; false: past its queries.
+struct KvOutRow {
+  int64_t at;     // row of out and lse, [total_q][q_heads]
+};
+__device__ __forceinline__ bool kv_out_row(const KvAttendLaunch& a, int q0, int m, int head, int rr, KvOutRow& o) {
+  const int i = (int)quotient((uint32_t)rr, a.group_div);
+  o.at = ((int64_t)q0 + i) * ((int64_t)a.p.heads * a.group) + (int64_t)head * a.group + (rr - i * a.group);
+  return i < m;
+}
+
+// Joins the pieces of the unit that begins in workgroup blockIdx.x's last
+// piece: each wave takes one of its rows.
+template <int FMT, int D, int kRows>
+__global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttendLaunch a, int workgroups) {
+  const int lane = threadIdx.x & 63, row = blockIdx.y * kWaves + (threadIdx.x >> 6);
+  const int w0 = blockIdx.x;
+  const KvShared h = kv_shared(a)[w0];
+  if (!h.last) return;
+  int pieces = 0;          // of the workgroups after w0, up to the one that ends the unit
+  for (int w = w0 + 1; w < workgroups; w += 64) {
+    const bool ends = w + lane < workgroups && kv_shared(a)[w + lane].first == 2;
+    const unsigned long long found = __ballot(ends);
+    if (found) {
+      pieces += __ffsll((long long)found);
+      break;
+    }
+    pieces += 64;
+  }
+  KvOutRow o;
+  const int q0 = kv_first_query(a, h.b), m = kv_first_query(a, h.b + 1) - q0;
+  if (row >= kRows || !kv_out_row(a, q0, m, h.head, h.row0 + row, o)) return;
+  float top = kNoMax;
+  for (int i = lane; i <= pieces; i += 64)
+    top = fmaxf(top, kv_partial<D, kRows>(a, workgroups, w0 + i, i == 0)[(int64_t)kRows * D + row]);
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+  constexpr int kEach = (D + 63) / 64;
+  float sum[kEach], all = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) sum[k] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i <= pieces; ++i) {
+    const float* part = kv_partial<D, kRows>(a, workgroups, w0 + i, i == 0);
+    const float f = __builtin_amdgcn_exp2f(part[(int64_t)kRows * D + row] - top);
+    all += f * part[(int64_t)kRows * (D + 1) + row];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (lane + 64 * k < D) sum[k] += f * part[(int64_t)row * D + lane + 64 * k];
+  }
+  const float inv = all == 0.0f ? 0.0f : (FMT == 1 ? *a.p.vg : 1.0f) / all;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int d = lane + 64 * k;
+    if (d >= D) continue;
+    const float x = all == 0.0f ? 0.0f : sum[k] * inv;
+    if (a.dtype == kF32) static_cast<float*>(a.out)[o.at * D + d] = x;
+    else static_cast<uint16_t*>(a.out)[o.at * D + d] = (uint16_t)KvType<0>::pack(x, x);
+  }
+  if (a.lse && lane == 0)
+    a.lse[o.at] = all == 0.0f ? -INFINITY : (top - KvType<FMT>::kUp + __builtin_amdgcn_logf(all)) * kLn2;
+}
+
+template <int FMT, int kQ>
+constexpr bool kv_scaled_rows() { return FMT == 1; }
+
+// 8 elements of q, widened and rotated; rows past the last are zero.
+__device__ __forceinline__ void load_q8(const KvAttendLaunch& a, const KvUnit& u, int row, int at, float v[8]) {
+  const uint32_t i = quotient((uint32_t)row, a.group_div);
+  if ((int)i < u.m) {
+    const int64_t off = (u.q0 + (int64_t)i) * a.q_stride[0] +
+                        ((int64_t)u.head * a.group + (row - (int)i * a.group)) * a.q_stride[1] + 8 * at;
+    if (a.dtype == kF32) {
+      SlotRaw<kF32> r;
+      const float* p = static_cast<const float*>(a.q) + off;
+      const u32x4_t x = load16<false>(p), y = load16<false>(p + 4);
+      r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+      r.w[4] = y.x; r.w[5] = y.y; r.w[6] = y.z; r.w[7] = y.w;
+      widen_slot<kF32>(r, v);
+    } else {
+      SlotRaw<kBF16> r;
+      const u32x4_t x = load16<false>(static_cast<const uint16_t*>(a.q) + off);
+      r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+      widen_slot<kBF16>(r, v);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+  }
+}
+
+// Stages ROWS query rows as kQ pieces in LDS, rows of D + 8 halves, pieces
+// ROWS rows apart, and each row's factor from raw score to exponent of two in
+// factor[].  Every thread of the workgroup calls it; it ends synchronised.
+// most[]: ROWS words of scratch.
+template <int FMT, int D, int kQ, int ROWS>
+__device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, const KvUnit& u, uint16_t* sq, float* factor,
+                                              uint32_t* most) {
+  constexpr int kPer = D / 8, kItems = ROWS * kPer;
+  constexpr int kEach = (kItems + kThreads - 1) / kThreads;
+  const int tid = threadIdx.x;
+  float v[kEach][8];
+  if constexpr (kv_scaled_rows<FMT, kQ>()) {
+    for (int i = tid; i < ROWS; i += kThreads) most[i] = 0u;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int item = tid + k * kThreads;
+    if (item < kItems) {      // (whole waves: kItems is a multiple of 64)
+      const int row = item / kPer, at = item % kPer;
+      load_q8(a, u, u.row0 + row, at, v[k]);
+      if constexpr (D % 128 == 0) {
+        if (a.rotate) fwht128_lanes(v[k], tid & 15, a.rot_scale);
+      }
+      if constexpr (kv_scaled_rows<FMT, kQ>()) atomicMax(most + row, abs_max_bits8(v[k]));
+    }
+  }
+  __syncthreads();
+  const float base = a.scale * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f);
+  for (int i = tid; i < ROWS; i += kThreads) {
+    float f = base;
+    if constexpr (kv_scaled_rows<FMT, kQ>()) {
+      const uint32_t e = min(max(most[i] >> 23, 9u), 254u);
+      f = base * as_f((e - 8u) << 23);
+    }
+    factor[i] = f;
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int item = tid + k * kThreads;
+    if (item < kItems) {
+      const int row = item / kPer, at = item % kPer;
+      if constexpr (kv_scaled_rows<FMT, kQ>()) {
+        const uint32_t e = min(max(most[row] >> 23, 9u), 254u);
+        const float f = as_f((262u - e) << 23);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] *= f;
+      }
+      uint32_t w[4][kQ];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pieces<FMT, kQ>(v[k][2 * j], v[k][2 * j + 1], w[j]);
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        *reinterpret_cast<u32x4_t*>(sq + ((size_t)q * ROWS + row) * (D + 8) + 8 * at) =
+            u32x4_t{w[0][q], w[1][q], w[2][q], w[3][q]};
+    }
+  }
+  __syncthreads();
+}
+
+// Tokens [from, from + count) that row rr of a unit's sequence sees.
+__device__ __forceinline__ void kv_sees(const KvAttendLaunch& a, const KvUnit& u, int rr, int& from, uint32_t& count) {
+  const int i = (int)quotient((uint32_t)rr, a.group_div);
+  const int64_t pos = (int64_t)u.n - u.m + i;     // the query's own token
+  const int64_t to = a.causal ? min(pos + 1, (int64_t)u.n) : u.n;
+  const int64_t lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
+  from = (int)min(lo, (int64_t)u.n);
+  count = i < u.m && to > lo ? (uint32_t)(to - lo) : 0u;
+}
+
+// Tokens [from, to) that every row of the block sees.
+template <int kRows>
+__device__ __forceinline__ void kv_all_see(const KvAttendLaunch& a, const KvUnit& u, int& from, int& to) {
+  const int i0 = (int)quotient((uint32_t)u.row0, a.group_div);
+  const int i1 = min((int)quotient((uint32_t)(u.row0 + kRows - 1), a.group_div), u.m - 1);
+  const int64_t past = (int64_t)u.n - u.m;
+  to = (int)max((int64_t)0, a.causal ? min((int64_t)u.n, past + i0 + 1) : (int64_t)u.n);
+  from = a.window > 0 ? (int)max((int64_t)0, past + i1 - a.window + 1) : 0;
+}
+
+// Values that are no finite numbers, in a tile that some rows see only in
+// part, enter the products as zeros: 0 times NaN must not reach the rows that
+// do not see them.  Where that happened the rows that do see one are made NaN
+// here, element d .. d + 3 of row rr at a time, by going through the scale
+// bytes of tokens [t0, t1) again.
+template <int FMT, int D>
+__device__ __forceinline__ bool kv_sees_nan(const KvAttendLaunch& a, const KvUnit& u, int rr, int d, int t0, int t1) {
+  int from;
+  uint32_t count;
+  kv_sees(a, u, rr, from, count);
+  const KvHead planes = kv_head(a.p, u.head);
+  const int32_t* table = a.table + u.b * a.table_stride;
+  bool nan = false;
+  for (int t = max(t0, from); t < t1 && (uint32_t)(t - from) < count; ++t) {
+    const uint32_t col = quotient((uint32_t)t, a.p.page);
+    const int32_t page = table[col];
+    if ((uint32_t)page >= (uint32_t)a.p.num_pages) continue;
+    const KvAt at = kv_at(a.p, (uint32_t)page, (uint32_t)t - col * a.p.page.d);
+    nan |= KvLane<FMT, D>::not_finite(planes.vs[at.scale + d / KvLane<FMT, D>::kBlock]);
+  }
+  return nan;
+}
+
+// Stores 4 consecutive elements of an output row.
+__device__ __forceinline__ void store_out4(const KvAttendLaunch& a, int64_t o, f32x4_t v) {
+  if (a.dtype == kF32) {
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + o) = v;
+  } else {
+    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + o) =
+        u32x2_t{KvType<0>::pack(v.x, v.y), KvType<0>::pack(v.z, v.w)};
+  }
+}
+
+// Elements d .. d + 3 of a finished row rr: the sum of weighted values over
+// the sum of weights, and with element 0 the row's log-sum-exp.
+template <int FMT, int D>
+__device__ __forceinline__ void kv_finish4(const KvAttendLaunch& a, const KvUnit& u, int rr, int d, f32x4_t sum,
+                                           float top, float total) {
+  KvOutRow out;
+  if (!kv_out_row(a, u.q0, u.m, u.head, rr, out)) return;
+  const float inv = total == 0.0f ? 0.0f : (FMT == 1 ? *a.p.vg : 1.0f) / total;
+  store_out4(a, out.at * D + d, total == 0.0f ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : sum * inv);
+  if (a.lse && d == 0)
+    a.lse[out.at] = total == 0.0f ? -INFINITY : (top - KvType<FMT>::kUp + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+}  // namespace fp4q

@@ -1,0 +1,286 @@
+// fp4q_kv_cache.hip -- writing keys and values into the paged 4-bit cache and
+// reading them back.
+//
+// A lane holds 8 consecutive elements of one (token, head) vector, so a
+// 16-block is a lane pair, a 32-block a lane quad and a 128-point transform
+// 16 lanes, as in the library's other quantizers, whose bytes these match.
+#include "fp4q_kv.h"
+#include "fp4q_nv_common.h"
+
+namespace fp4q {
+namespace {
+
+// ----------------------------------------------------------------------------
+// NVFP4 encoding against a given tensor scale g, one block's factors computed
+// where they are used: the calls that matter most write a few rows, where a
+// table of every scale's factors would take longer than the rows.
+//   s = RNE_E4M3(bamax / (6 g)) and codes RNE_E2M1(x / (s g)) are decided on
+//   the exact quotients: fp32 products with the reciprocal off by -+2^-21
+//   bracket each quotient (product, reciprocal and bracket round by 2^-24
+//   each), brackets that disagree are resolved by the sign of an exact FMA
+//   residual, and tensor scales outside [2^-100, 2^100] take fp64 quotients.
+__device__ __noinline__ uint32_t nv_encode_wide(const float v[8], float bamax, float g, uint32_t& scale) {
+  const double mg = 6.0 * (double)g;
+  scale = e4m3_encode_exact(bamax, (double)bamax / mg, mg);
+  const double den = (double)e4m3_value(scale) * (double)g;
+  uint32_t codes = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t mag = scale ? e2m1_rne_mag_f64(fabs((double)v[i]) / den) : 0u;
+    codes |= (mag | ((as_u(v[i]) >> 31) << 3)) << (4 * i);
+  }
+  return codes;
+}
+
+__device__ __forceinline__ uint32_t nv_encode_block(const float v[8], float bamax, float g, uint32_t& scale) {
+  if (!(g >= 0x1p-100f && g <= 0x1p100f)) return nv_encode_wide(v, bamax, g, scale);
+  constexpr float kBelow = 1.0f - 0x1p-21f, kAbove = 1.0f + 0x1p-21f;
+  const float inv6 = 1.0f / (6.0f * g);
+  const uint32_t c = nv_scale_code(bamax, inv6 * kBelow, inv6 * kAbove, 0.0, 0.0, false, 6.0f, g);
+  const float sd = e4m3_value(c);
+  const float inv = c ? 1.0f / (sd * g) : 0.0f;
+  const float lo = inv * kBelow, hi = inv * kAbove, one = e8m0_operand(127u);
+  uint32_t a = 0u, b = 0u;
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[0] * lo, v[1] * lo, one, 0);
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[2] * lo, v[3] * lo, one, 1);
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[4] * lo, v[5] * lo, one, 2);
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[6] * lo, v[7] * lo, one, 3);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[0] * hi, v[1] * hi, one, 0);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[2] * hi, v[3] * hi, one, 1);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[4] * hi, v[5] * hi, one, 2);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[6] * hi, v[7] * hi, one, 3);
+  uint32_t d = (a ^ b) & 0x77777777u;
+  if (d != 0u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((d >> (4 * i)) & 7u) {
+        const uint32_t mag = e2m1_rne_mag_exact(fabsf(v[i]), (a >> (4 * i)) & 7u, sd, g);
+        a = (a & ~(7u << (4 * i))) | (mag << (4 * i));
+      }
+    }
+  }
+  scale = c;
+  return a;
+}
+
+__device__ __forceinline__ uint32_t mx_encode_block(const float v[8], uint32_t amax, uint32_t& scale) {
+  const int e = (amax == 0u) ? 0 : max((int)(amax >> 23) - 129, -127);
+  scale = (uint32_t)(e + 127);
+  const float sc = e8m0_operand(scale);
+  uint32_t codes = 0u;
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[0], v[1], sc, 0);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2], v[3], sc, 1);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[4], v[5], sc, 2);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[6], v[7], sc, 3);
+  return codes;
+}
+
+template <int FMT, int IN>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteLaunch w, float rot_scale, FastDiv row_slots,
+                                                            FastDiv heads, uint32_t nslots) {
+  const bool values = blockIdx.y != 0;
+  const uint32_t s = blockIdx.x * kThreads + threadIdx.x;
+  const bool in_range = s < nslots;
+  const uint32_t row = quotient(in_range ? s : 0u, row_slots), at = (in_range ? s : 0u) - row * row_slots.d;
+  const uint32_t token = quotient(row, heads), head = row - token * heads.d;
+  const int64_t slot = w.slots[token];
+  const bool active = in_range && slot >= 0 && slot < (int64_t)w.p.num_pages * w.p.page.d;
+  SlotRaw<IN> r;
+#pragma unroll
+  for (int i = 0; i < (IN == kF32 ? 8 : 4); ++i) r.w[i] = 0u;
+  if (active) {
+    const int64_t off = values ? token * w.v_stride[0] + head * w.v_stride[1] : token * w.k_stride[0] + head * w.k_stride[1];
+    const void* x = values ? w.v : w.k;
+    if constexpr (IN == kF32) {
+      const float* p = static_cast<const float*>(x) + off + 8 * at;
+      const u32x4_t a = load16<true>(p), b = load16<true>(p + 4);
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+      r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+    } else {
+      const u32x4_t a = load16<true>(static_cast<const uint16_t*>(x) + off + 8 * at);
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    }
+  }
+  float v[8];
+  widen_slot<IN>(r, v);
+  // (head_dim is a multiple of 128 here, so 16 consecutive lanes hold one chunk)
+  if (w.rotate && !values) fwht128_lanes(v, threadIdx.x & 15, rot_scale);
+  uint32_t amax = abs_max_bits8(v);
+  amax = max(amax, dpp_u32<kQuadXor1>(amax));
+  if constexpr (FMT == 0) amax = max(amax, dpp_u32<kQuadXor2>(amax));
+  uint32_t scale, codes;
+  if constexpr (FMT == 0) codes = mx_encode_block(v, amax, scale);
+  else codes = nv_encode_block(v, as_f(amax), *(values ? w.p.vg : w.p.kg), scale);
+  if (amax >= 0x7F800000u) {   // a block with an infinity or NaN: the NaN scale code
+    codes = 0u;
+    scale = FMT == 0 ? 0xFFu : 0x7Fu;
+  }
+  if (!active) return;
+  // (slot < 2^31 * 2^31: 64-bit division only where it does not fit 32 bits)
+  const int64_t page = slot <= 0x7FFFFFFF ? (int64_t)quotient((uint32_t)slot, w.p.page) : slot / w.p.page.d;
+  const int64_t offset = slot - page * w.p.page.d;
+  uint8_t* cp = (values ? w.p.vc : w.p.kc) + page * w.p.code_stride[0] + (int64_t)head * w.p.code_stride[1] +
+                offset * w.p.code_stride[2];
+  *reinterpret_cast<uint32_t*>(cp + 4 * at) = codes;
+  constexpr uint32_t per = FMT == 0 ? 4u : 2u;   // lanes of one block
+  if ((at & (per - 1)) == 0) {
+    uint8_t* sp = (values ? w.p.vs : w.p.ks) + page * w.p.scale_stride[0] + (int64_t)head * w.p.scale_stride[1] +
+                  offset * w.p.scale_stride[2];
+    sp[at / per] = (uint8_t)scale;
+  }
+}
+
+template <int FMT>
+hipError_t launch_write_t(const KvWriteLaunch& w, int64_t first, int64_t count, hipStream_t st) {
+  KvWriteLaunch part = w;
+  const size_t esz = w.in_dtype == kF32 ? 4 : 2;
+  part.k = static_cast<const char*>(w.k) + first * w.k_stride[0] * esz;
+  part.v = static_cast<const char*>(w.v) + first * w.v_stride[0] * esz;
+  part.slots = w.slots + first;
+  const uint32_t per = (uint32_t)w.head_dim / 8, nslots = (uint32_t)(count * w.p.heads * per);
+  const dim3 grid((nslots + kThreads - 1) / kThreads, 2);
+  const float c = (float)(1.0 / sqrt(128.0));
+  if (w.in_dtype == kF32)
+    hipLaunchKernelGGL((kv_write_kernel<FMT, kF32>), grid, dim3(kThreads), 0, st, part, c, fast_div(per),
+                       fast_div((uint32_t)w.p.heads), nslots);
+  else
+    hipLaunchKernelGGL((kv_write_kernel<FMT, kBF16>), grid, dim3(kThreads), 0, st, part, c, fast_div(per),
+                       fast_div((uint32_t)w.p.heads), nslots);
+  return hipGetLastError();
+}
+
+// ----------------------------------------------------------------------------
+// Last index b with cu[b] <= t, of a cumulative array cu[0..n] (cu[0] = 0).
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int64_t t) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <int FMT, int OUT>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float rot_scale, FastDiv row_slots,
+                                                           FastDiv heads, uint32_t nslots, int64_t first) {
+  const bool values = r.k_out == nullptr || blockIdx.y != 0;
+  const uint32_t s = blockIdx.x * kThreads + threadIdx.x;
+  const bool in_range = s < nslots;
+  const uint32_t row = quotient(in_range ? s : 0u, row_slots), at = (in_range ? s : 0u) - row * row_slots.d;
+  const uint32_t token = quotient(row, heads), head = row - token * heads.d;
+  const int64_t t = first + token;
+  const int b = sequence_of(r.cu, r.seqs, t);
+  const int64_t pos = t - r.cu[b] + (r.starts ? r.starts[b] : 0);
+  const bool there = t < r.cu[b + 1] && pos >= 0 && pos < (int64_t)r.table_cols * r.p.page.d;
+  uint32_t cw = 0u, sb = FMT == 0 ? 127u : 0u;
+  if (there && in_range) {
+    const int64_t col = pos <= 0x7FFFFFFF ? (int64_t)quotient((uint32_t)pos, r.p.page) : pos / r.p.page.d;
+    const int64_t offset = pos - col * r.p.page.d;
+    const int32_t page = r.table[b * r.table_stride + col];
+    if (page >= 0 && page < r.p.num_pages) {
+      const uint8_t* cp = (values ? r.p.vc : r.p.kc) + (int64_t)page * r.p.code_stride[0] + (int64_t)head * r.p.code_stride[1] +
+                          offset * r.p.code_stride[2];
+      const uint8_t* sp = (values ? r.p.vs : r.p.ks) + (int64_t)page * r.p.scale_stride[0] + (int64_t)head * r.p.scale_stride[1] +
+                          offset * r.p.scale_stride[2];
+      cw = *reinterpret_cast<const uint32_t*>(cp + 4 * at);
+      sb = sp[FMT == 0 ? at >> 2 : at >> 1];
+    }
+  }
+  const bool rotate = r.rotate && !values;
+  const float g = FMT == 0 ? 1.0f : *(values ? r.p.vg : r.p.kg);
+  float v[8], sd = 1.0f;
+  const float sc = FMT == 0 ? e8m0_operand(sb) : e8m0_operand(127u);
+  float2_t p;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 0); v[0] = p.x; v[1] = p.y;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 1); v[2] = p.x; v[3] = p.y;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 2); v[4] = p.x; v[5] = p.y;
+  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 3); v[6] = p.x; v[7] = p.y;
+  bool nan = FMT == 0 ? sb == 255u : (sb & 0x7Fu) == 0x7Fu;
+  if constexpr (FMT != 0) {
+    sd = e4m3_value(sb & 0x7Fu);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= sd;   // exact: 2 and 4 significant bits
+  }
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = as_f(0x7FC00000u);
+  }
+  if (rotate) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= g;
+    fwht128_lanes(v, threadIdx.x & 15, rot_scale);
+  }
+  if (!in_range) return;
+  const int64_t o = ((t * heads.d + head) * row_slots.d + at) * 8;
+  void* out = values ? r.v_out : r.k_out;
+  if constexpr (OUT == kF32) {
+    if (!rotate) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= g;
+    }
+    u32x4_t* dst = reinterpret_cast<u32x4_t*>(static_cast<float*>(out) + o);
+    __builtin_nontemporal_store(u32x4_t{as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])}, dst);
+    __builtin_nontemporal_store(u32x4_t{as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])}, dst + 1);
+  } else {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = rotate ? v[2 * i] : v[2 * i] * g, c = rotate ? v[2 * i + 1] : v[2 * i + 1] * g;
+      const bf16x2_t pk = {(__bf16)a, (__bf16)c};
+      h[i] = __builtin_bit_cast(uint32_t, pk);
+      // v s g is rounded once: where its fp32 product sits on a bf16 midpoint
+      // the exact product decides (the rotated values are sums, rounded twice)
+      if (FMT != 0 && !rotate) {
+        if ((as_u(a) & 0xFFFFu) == 0x8000u) h[i] = (h[i] & 0xFFFF0000u) | bf16_of_product(v[2 * i], g);
+        if ((as_u(c) & 0xFFFFu) == 0x8000u) h[i] = (h[i] & 0xFFFFu) | (bf16_of_product(v[2 * i + 1], g) << 16);
+      }
+    }
+    __builtin_nontemporal_store(u32x4_t{h[0], h[1], h[2], h[3]},
+                                reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + o));
+  }
+}
+
+template <int FMT>
+hipError_t launch_read_t(const KvReadLaunch& r, int64_t first, int64_t count, hipStream_t st) {
+  const uint32_t per = (uint32_t)r.head_dim / 8, nslots = (uint32_t)(count * r.p.heads * per);
+  const dim3 grid((nslots + kThreads - 1) / kThreads, r.k_out && r.v_out ? 2 : 1);
+  const float c = (float)(1.0 / sqrt(128.0));
+  if (r.out_dtype == kF32)
+    hipLaunchKernelGGL((kv_read_kernel<FMT, kF32>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
+                       fast_div((uint32_t)r.p.heads), nslots, first);
+  else
+    hipLaunchKernelGGL((kv_read_kernel<FMT, kBF16>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
+                       fast_div((uint32_t)r.p.heads), nslots, first);
+  return hipGetLastError();
+}
+
+// Slots of one launch fit 31 bits; longer calls run as several launches.
+int64_t tokens_per_launch(int heads, int head_dim) {
+  const int64_t n = ((int64_t)1 << 30) / ((int64_t)heads * (head_dim / 8));
+  return n < 1 ? 1 : n;
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const KvWriteLaunch& w, hipStream_t st) {
+  const int64_t step = tokens_per_launch(w.p.heads, w.head_dim);
+  for (int64_t at = 0; at < w.tokens; at += step) {
+    const int64_t n = w.tokens - at < step ? w.tokens - at : step;
+    const hipError_t e = w.format == 0 ? launch_write_t<0>(w, at, n, st) : launch_write_t<1>(w, at, n, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_kv_read(const KvReadLaunch& r, hipStream_t st) {
+  const int64_t step = tokens_per_launch(r.p.heads, r.head_dim);
+  for (int64_t at = 0; at < r.total; at += step) {
+    const int64_t n = r.total - at < step ? r.total - at : step;
+    const hipError_t e = r.format == 0 ? launch_read_t<0>(r, at, n, st) : launch_read_t<1>(r, at, n, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp4q

@@ -1,0 +1,344 @@
+// fp4q_kv_decode.h -- attention over the 4-bit cache for few query rows.
+//
+// One read of the cache is what such a call costs; its groups of 128 tokens
+// are shared out evenly (the schedule of fp4q_kv_attend.h), lengths being read
+// on the device, so that a captured launch follows them.  A unit inside one
+// stretch is finished there; the others leave partial results that a second
+// kernel joins.
+//
+// In a workgroup each of the 4 waves works on 32 tokens of a group by itself:
+// keys from memory into the left operand of 16x16x32 products (16 tokens x 16
+// rows), values through the wave's own LDS rows.  Codes of the next group are
+// in flight while one is worked on.  Bound by HBM.
+#pragma once
+
+#include "fp4q_kv_attend.h"
+
+namespace fp4q {
+
+constexpr int kGroupTokens = 128;
+
+template <int FMT, int D, int kTiles, int kQ, int kP>
+struct DecodeShape {
+  static constexpr int kRows = 16 * kTiles;
+  static constexpr int kChunks = D / 32;
+  // query pieces stay in registers up to 64 of them, in LDS beyond
+  static constexpr bool kQRegs = kTiles * kQ * kChunks * 4 <= 64;
+  static constexpr int kVStride = D + 16;                        // halves: rows 8 banks apart
+  static constexpr int kVBytes = kWaves * 32 * kVStride * 2;
+  static constexpr int kOStride = D + 4;                         // floats
+  static constexpr int kOBytes = kWaves * 16 * kOStride * 4;
+  static constexpr int kQBytes = kQ * kRows * (D + 8) * 2;
+  static constexpr int kMax1 = kVBytes > kOBytes ? kVBytes : kOBytes;
+  static constexpr int kMain = kQRegs && kQBytes > kMax1 ? kQBytes : kMax1;
+  static constexpr int kShared = kMain + (kQRegs ? 0 : kQBytes);
+  static constexpr int kWavesPerSimd = D > 128 ? 1 : (kTiles == 2 ? 2 : 3);
+};
+
+template <int FMT, int D, int kTiles, int kQ, int kP>
+__global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd)) void kv_decode_kernel(
+    KvAttendLaunch a, int64_t numbers) {
+  using Shape = DecodeShape<FMT, D, kTiles, kQ, kP>;
+  using T = KvType<FMT>;
+  using Lane = KvLane<FMT, D>;
+  constexpr int kChunks = Shape::kChunks, kRows = Shape::kRows;
+  __shared__ __align__(16) uint8_t s_main[Shape::kShared];
+  __shared__ float s_factor[kRows];
+  __shared__ uint32_t s_most[kRows];
+  __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
+  __shared__ int s_bad[kWaves];
+  __shared__ long long s_scan[kWaves + 3];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  uint16_t* sv = reinterpret_cast<uint16_t*>(s_main) + wave * 32 * Shape::kVStride;
+  float* so = reinterpret_cast<float*>(s_main);
+  uint16_t* sq = reinterpret_cast<uint16_t*>(s_main + (Shape::kQRegs ? 0 : Shape::kMain));
+
+  KvStretch st;
+  if (!kv_stretch<kRows, kGroupTokens, kThreads>(a, numbers, st, s_scan)) {
+    if (tid == 0) kv_shared(a)[blockIdx.x] = KvShared{0, 0, 0, 0, 0, 0, 0, 0};
+    return;
+  }
+  int shared_first = 0, shared_last = 0, shared_b = 0, shared_head = 0, shared_row0 = 0;
+  KvUnit u = st.u;
+  int group = st.group;
+  int64_t left = st.left;
+  for (;;) {
+    // the unit's groups [group, last) are this workgroup's
+    const int last = (int)min((int64_t)u.groups, group + left);
+    stage_queries<FMT, D, kQ, kRows>(a, u, sq, s_factor, s_most);
+
+    u32x4_t qf[Shape::kQRegs ? kTiles : 1][Shape::kQRegs ? kQ : 1][Shape::kQRegs ? kChunks : 1];
+    float factor[kTiles];
+    int sees_from[kTiles];                      // the lane's row sees `sees` tokens from here
+    uint32_t sees[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      factor[t] = s_factor[16 * t + r];
+      kv_sees(a, u, u.row0 + 16 * t + r, sees_from[t], sees[t]);
+      if constexpr (Shape::kQRegs) {
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            qf[t][q][c] = *reinterpret_cast<const u32x4_t*>(sq + (q * kRows + 16 * t + r) * (D + 8) + Lane::element(c, g));
+      }
+    }
+    if constexpr (Shape::kQRegs) __syncthreads();     // the values' rows overlie the queries
+    int all_from, all_to;
+    kv_all_see<kRows>(a, u, all_from, all_to);
+
+    f32x4_t o[kTiles][D / 16];
+    float m[kTiles], l[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      m[t] = kNoMax;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[t][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    const int32_t* table = a.table + u.b * a.table_stride;
+    const KvHead planes = kv_head(a.p, u.head);
+    const int first = u.lo + 32 * wave, n = u.hi;
+    // Codes of 2 x 16 tokens a lane, those of the next group in flight, and
+    // the page numbers of the group after that.  No branches: tokens past the
+    // end are looked for at the last one's place, pages that are none at page
+    // 0, and then zeroed.
+    Lane kl[2], vl[2];
+    int32_t pages[2];
+    bool there[2];
+    auto find = [&](int grp) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = min(first + grp * kGroupTokens + 16 * x + r, n - 1);
+        pages[x] = table[quotient((uint32_t)t, a.p.page)];
+      }
+    };
+    auto fetch = [&](int grp) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = first + grp * kGroupTokens + 16 * x + r;
+        const uint32_t tt = (uint32_t)min(t, n - 1);
+        const bool page = (uint32_t)pages[x] < (uint32_t)a.p.num_pages;
+        const KvAt at = kv_at(a.p, page ? (uint32_t)pages[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
+        kl[x].load(planes.kc + at.code, planes.ks + at.scale, g);
+        vl[x].load(planes.vc + at.code, planes.vs + at.scale, g);
+        there[x] = page && t < n;
+      }
+    };
+    bool bad = false;       // a value that is no finite number was left out
+    if (n > 0) {
+      find(group);
+      fetch(group);
+      find(group + 1);
+    }
+    for (int grp = group; grp < last; ++grp) {
+      const int t0 = first + grp * kGroupTokens;
+      if (t0 >= n) break;
+      const bool edge = t0 + 32 > all_to || t0 < all_from;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        kl[x].keep_if(there[x]);
+        vl[x].keep_if(there[x]);
+      }
+      if (edge) {
+        const bool left_out = vl[0].drop_not_finite() | vl[1].drop_not_finite();
+        bad |= __any(left_out) != 0;
+      }
+      // scores of 32 tokens x 16 rows, transposed: token 16 x + 4 g + i, row r
+      f32x4_t s[kTiles][2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const typename Lane::Scales sc = kl[x].prepare();
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) s[t][x] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const u32x4_t kf = kl[x].values(c, sc);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+              if constexpr (Shape::kQRegs) {
+                s[t][x] = T::mfma16(kf, qf[t][q][c], s[t][x]);
+              } else {
+                const u32x4_t w = *reinterpret_cast<const u32x4_t*>(sq + (q * kRows + 16 * t + r) * (D + 8) +
+                                                                    Lane::element(c, g));
+                s[t][x] = T::mfma16(kf, w, s[t][x]);
+              }
+            }
+        }
+      }
+      // values into the wave's LDS rows
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const typename Lane::Scales sc = vl[x].prepare();
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          *reinterpret_cast<u32x4_t*>(sv + (16 * x + r) * Shape::kVStride + Lane::element(c, g)) = vl[x].values(c, sc);
+      }
+      fetch(grp + 1);
+      find(grp + 2);
+
+      // (scalars and selects throughout: hipcc 7.2 moves the wrong elements of
+      // a vector when one is replaced under a lane's condition)
+      float y[kTiles][8];
+      bool raise = false;
+      float most[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[t][k] = s[t][k >> 2][k & 3] * factor[t];
+        if (edge) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t j = (uint32_t)(t0 + 16 * (k >> 2) + 4 * g + (k & 3) - sees_from[t]);
+            y[t][k] = j < sees[t] ? y[t][k] : -INFINITY;
+          }
+        }
+        most[t] = fmaxf(fmaxf(fmaxf(y[t][0], y[t][1]), fmaxf(y[t][2], y[t][3])),
+                        fmaxf(fmaxf(y[t][4], y[t][5]), fmaxf(y[t][6], y[t][7])));
+        raise |= most[t] > m[t] + kRaise;
+      }
+      // raise the maxima where a score exceeds them by more than the slack
+      if (__any(raise)) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          float x = fmaxf(most[t], __shfl_xor(most[t], 16, 64));
+          x = fmaxf(x, __shfl_xor(x, 32, 64));
+          x = fmaxf(x, m[t]);
+          const float f = __builtin_amdgcn_exp2f(m[t] - x);
+          m[t] = x;
+          l[t] *= f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) o[t][c] *= f;
+        }
+      }
+      u32x4_t w[kTiles][kP];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const float top = m[t] - T::kUp;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          y[t][k] = __builtin_amdgcn_exp2f(y[t][k] - top);
+          l[t] += y[t][k];
+        }
+        uint32_t h[4][kP];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pieces<FMT, kP>(y[t][2 * j], y[t][2 * j + 1], h[j]);
+#pragma unroll
+        for (int q = 0; q < kP; ++q) w[t][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
+      }
+      // weighted values: element 16 c + 4 g + i, row r
+      const uint16_t* vp = sv + (4 * g + (r >> 2)) * Shape::kVStride + 4 * (r & 3);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const u32x2_t x0 = read_transposed(vp + 16 * c), x1 = read_transposed(vp + 16 * Shape::kVStride + 16 * c);
+        const u32x4_t vf = {x0.x, x0.y, x1.x, x1.y};
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int q = 0; q < kP; ++q) o[t][c] = T::mfma16(vf, w[t][q], o[t][c]);
+      }
+    }
+
+    // join the four waves: maxima and sums of every row, then the values
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      l[t] += __shfl_xor(l[t], 16, 64);
+      l[t] += __shfl_xor(l[t], 32, 64);
+      if (g == 0) {
+        s_m[wave][16 * t + r] = m[t];
+        s_l[wave][16 * t + r] = l[t];
+      }
+    }
+    if (lane == 0) s_bad[wave] = bad;
+    const bool whole = group == 0 && last == u.groups;
+    float* part = kv_partial<D, kRows>(a, gridDim.x, blockIdx.x, group == 0);
+    if (!whole) {
+      if (group == 0) {
+        shared_last = 1;
+        shared_b = u.b;
+        shared_head = u.head;
+        shared_row0 = u.row0;
+      } else {
+        shared_first = last == u.groups ? 2 : 1;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      __syncthreads();
+      const float top = fmaxf(fmaxf(s_m[0][16 * t + r], s_m[1][16 * t + r]), fmaxf(s_m[2][16 * t + r], s_m[3][16 * t + r]));
+      const float f = __builtin_amdgcn_exp2f(m[t] - top);
+      float* dst = so + (wave * 16 + r) * Shape::kOStride + 4 * g;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) *reinterpret_cast<f32x4_t*>(dst + 16 * c) = o[t][c] * f;
+      __syncthreads();
+      for (int item = tid; item < 16 * (D / 4); item += kThreads) {
+        const int row = item / (D / 4), d = 4 * (item % (D / 4));
+        const int rr = 16 * t + row;
+        f32x4_t sum = *reinterpret_cast<const f32x4_t*>(so + row * Shape::kOStride + d);
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4_t*>(so + (w * 16 + row) * Shape::kOStride + d);
+        if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) {
+          const int t1 = min(u.hi, u.lo + last * kGroupTokens);
+          if (kv_sees_nan<FMT, D>(a, u, u.row0 + rr, d, u.lo + group * kGroupTokens, t1)) sum *= as_f(0x7FC00000u);
+        }
+        const float mx = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
+        float total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) total += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mx);
+        if (whole) {
+          kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, mx, total);
+        } else {
+          *reinterpret_cast<f32x4_t*>(part + (int64_t)rr * D + d) = sum;
+          if (d == 0) {
+            part[(int64_t)kRows * D + rr] = mx;
+            part[(int64_t)kRows * (D + 1) + rr] = total;
+          }
+        }
+      }
+    }
+    __syncthreads();
+
+    left -= last - group;
+    if (left <= 0) break;
+    group = 0;
+    kv_next<kRows, kGroupTokens>(a, u);
+  }
+  if (tid == 0)
+    kv_shared(a)[blockIdx.x] = KvShared{shared_first, shared_last, shared_b, shared_head, shared_row0, 0, 0, 0};
+}
+
+template <int FMT, int D, int kTiles, int kQ, int kP>
+hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
+  constexpr int kRows = 16 * kTiles;
+  const int64_t numbers = kv_block_numbers<kRows>(a);
+  const int64_t groups = (a.most_tokens + kGroupTokens - 1) / kGroupTokens;
+  const int64_t most = numbers * a.p.heads * (groups < 1 ? 1 : groups);
+  const int64_t resident = (int64_t)cus * DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd;
+  const int grid = (int)(most < resident ? most : resident);
+  hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP>), dim3(grid), dim3(kThreads), 0, st, a, numbers);
+  hipError_t e = hipGetLastError();
+  // (a stretch is at least a group, and a unit of one group is never shared)
+  if (e != hipSuccess || groups <= 1) return e;
+  hipLaunchKernelGGL((kv_join_kernel<FMT, D, kRows>), dim3(grid, kRows / kWaves), dim3(kThreads), 0, st, a, grid);
+  return hipGetLastError();
+}
+
+// The choice of pieces (see fp4q_kv_attend.h): fp32, bf16 rotated, bf16.
+template <int FMT, int D, int kTiles>
+hipError_t launch_decode_pieces(const KvAttendLaunch& a, int cus, hipStream_t st) {
+  if (a.dtype == kF32) return launch_decode_t<FMT, D, kTiles, FMT == 1 ? 2 : 3, 2>(a, cus, st);
+  if (a.rotate) return launch_decode_t<FMT, D, kTiles, 2, 1>(a, cus, st);
+  return launch_decode_t<FMT, D, kTiles, 1, 1>(a, cus, st);
+}
+
+template <int D, int FMT>
+hipError_t launch_decode_d(const KvAttendLaunch& a, int tiles, int cus, hipStream_t st) {
+  return tiles == 1 ? launch_decode_pieces<FMT, D, 1>(a, cus, st) : launch_decode_pieces<FMT, D, 2>(a, cus, st);
+}
+
+}  // namespace fp4q

@@ -259,6 +259,118 @@ fp4q_status fp4q_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *a_co
                             const uint8_t *b_codes, const uint8_t *b_scales, int32_t out_dtype, void *c,
                             void *hip_stream);
 
+/* The paged key/value cache in 4 bits ("Sub-4-Bit Microscaling", section 3:
+ * the rotated NVFP4 KV cache).
+ *
+ * Keys and values of num_pages pages of page_size tokens, kv_heads heads of
+ * head_dim elements.  The row of (page p, head h, token offset o) starts at
+ * byte p stride[0] + h stride[1] + o stride[2] of its plane: head_dim / 2
+ * bytes of codes (element 2k in the low nibble of byte k) or head_dim / block
+ * scale bytes.  Any order of pages, heads and tokens is a matter of strides;
+ * keys and values share theirs.  Format FP4Q_NVFP4 (16-blocks, E4M3 scales,
+ * k_global and v_global: device pointers to the tensor scales g, positive and
+ * finite) or FP4Q_MXFP4 (32-blocks, E8M0 scales); IF4 is UNSUPPORTED.
+ * head_dim: a multiple of 32 up to 1024; page_size: any.  Code planes and
+ * code strides are 16-byte aligned, scale planes and strides to the scale
+ * bytes of a quarter row where head_dim is a multiple of 128 (else
+ * FP4Q_ERR_UNSUPPORTED).  A dense [pages][heads][tokens] or
+ * [pages][tokens][heads] cache is.
+ *
+ * Token t of sequence b lies in page page_table[b * table_stride + t /
+ * page_size] at offset t % page_size.  A page id outside [0, num_pages) is
+ * never followed: its tokens read as zeros. */
+typedef struct {
+  int32_t format;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int64_t num_pages;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const float *k_global, *v_global;   /* NVFP4 only */
+  int64_t code_stride[3];             /* bytes between pages, heads, tokens */
+  int64_t scale_stride[3];
+} fp4q_kv_cache;
+
+typedef struct {
+  int64_t tokens;
+  const void *k, *v;       /* element e of head h of token t: t stride[0] + h stride[1] + e */
+  int64_t k_stride[2];     /* elements; in bytes multiples of 16 */
+  int64_t v_stride[2];
+  const int64_t *slots;    /* [tokens]: page * page_size + offset of each token */
+  int32_t in_dtype;        /* FP4Q_F32 or FP4Q_BF16 */
+  int32_t rotation;        /* FP4Q_ROT_NONE, or FP4Q_ROT_FWHT128: of the keys */
+} fp4q_kv_write_args;
+
+/* Quantizes keys and values of new tokens into their slots, in one launch:
+ * the bytes of fp4q_quantize_nvfp4 (policy NV_MAX6, round to nearest, with
+ * g = *k_global, *v_global) or fp4q_quantize_mxfp4 (OCP_MAX, round to
+ * nearest).  With FP4Q_ROT_FWHT128 (head_dim a multiple of 128) the keys are
+ * rotated first by the normalised Hadamard transform of each 128 elements;
+ * fp4q_kv_attention then rotates the queries alike, which leaves q . k as it
+ * is.  A slot outside the cache (any negative one, say) skips its token; slots
+ * of one call have to be distinct.  Non-finite inputs give their block the
+ * NaN scale code. */
+fp4q_status fp4q_kv_write(const fp4q_kv_cache *cache, const fp4q_kv_write_args *args, void *hip_stream);
+
+typedef struct {
+  const int32_t *page_table;   /* [seqs][table_stride] */
+  int64_t table_stride;
+  int32_t table_cols;          /* pages listed for a sequence */
+  int32_t seqs;
+  const int32_t *cu;           /* [seqs + 1] from 0: output rows of sequence b are cu[b] .. cu[b + 1] - 1 */
+  const int32_t *starts;       /* [seqs]: first token read of each sequence, or NULL for 0 */
+  int64_t total;               /* output rows */
+  void *k_out, *v_out;         /* [total][kv_heads][head_dim]; either may be NULL */
+  int32_t out_dtype;
+  int32_t rotation;            /* as the keys were written: they come back in their original basis */
+} fp4q_kv_read_args;
+
+/* The values that the cache holds of runs of tokens, gathered into dense
+ * rows: element * scale * g rounded once to the output type; rotated keys in
+ * fp32 through the transform (its own inverse), then rounded.  A NaN scale
+ * code gives NaN for its block (its 128-chunk, rotated back).  Rows without a
+ * token (beyond cu[seqs], beyond the table's pages) are zero. */
+fp4q_status fp4q_kv_read(const fp4q_kv_cache *cache, const fp4q_kv_read_args *args, void *hip_stream);
+
+typedef struct {
+  const void *q;               /* element e of head h of query t: t q_stride[0] + h q_stride[1] + e */
+  int64_t q_stride[2];         /* elements; in bytes multiples of 16 */
+  void *out;                   /* [total_q][q_heads][head_dim] of dtype */
+  float *lse;                  /* [total_q][q_heads] natural log-sum-exp of the scaled scores, or NULL */
+  const int32_t *cu_q;         /* [seqs + 1] from 0: queries of sequence b are cu_q[b] .. cu_q[b + 1] - 1; */
+                               /* NULL: one query each (total_q = seqs) */
+  const int32_t *seq_lens;     /* [seqs]: tokens in the cache, the new ones among them */
+  const int32_t *page_table;   /* [seqs][table_stride] */
+  int64_t table_stride;
+  int64_t total_q;
+  int32_t table_cols;
+  int32_t seqs;
+  int32_t max_q;               /* most queries of a sequence, at least (0 or 1 without cu_q) */
+  int32_t q_heads;             /* a multiple of kv_heads: head h reads cache head h / (q_heads / kv_heads) */
+  int32_t dtype;               /* FP4Q_F32 or FP4Q_BF16, of q and out */
+  int32_t causal;              /* query i of m sees token j <= n - m + i of n; 0: every token */
+  int32_t window;              /* > 0: of those only the last `window` (causal only) */
+  int32_t rotation;            /* as the keys were written: the queries are rotated in the call */
+  float scale;                 /* factor of q . k, finite */
+} fp4q_kv_attention_args;
+
+/* Bytes of device workspace an attention call uses (0 for arguments it would
+ * refuse), 16-byte aligned; it needs no clearing and keeps nothing between
+ * calls.  It depends on the shapes and max_q alone, not on the lengths. */
+size_t fp4q_kv_attention_workspace_bytes(const fp4q_kv_cache *cache, const fp4q_kv_attention_args *args);
+
+/* Attention of new queries over the cache: out = softmax(scale q k^T) v over
+ * the tokens each query sees, several query heads a cache head.  head_dim 64,
+ * 96, 128 or 256 (else UNSUPPORTED).  The lengths, cu_q and the page table
+ * are read on the device, so a captured call follows their values; a length
+ * counts at most table_cols * page_size tokens.  The cache's values enter
+ * exactly; sums, maxima and outputs are fp32, rounded once.  A query that
+ * sees no token, or only scores of minus infinity, gives zeros and a
+ * log-sum-exp of minus infinity.  Tokens that a query does not see never
+ * reach it, whatever their bytes stand for.  At most 65535 sequences. */
+fp4q_status fp4q_kv_attention(const fp4q_kv_cache *cache, const fp4q_kv_attention_args *args, void *workspace,
+                              size_t workspace_bytes, void *hip_stream);
+
 /* Host-side check of counters copied back from the device: FP4Q_ERR_NONFINITE
  * when counters[2] != 0, else FP4Q_OK (NULL -> FP4Q_ERR_INVALID_ARG). */
 fp4q_status fp4q_check_counters(const uint64_t *host_counters);
