@@ -22,9 +22,8 @@ ARCH = "gfx950"
 
 SOURCES = ["fp4q_api.hip", "fp4q_mx.hip", "fp4q_nv.hip", "fp4q_nv_resident.hip", "fp4q_fwht.hip", "fp4q_gemm.hip",
            "fp4q_dequant.hip", "fp4q_kv_api.hip", "fp4q_kv_cache.hip",
-           "fp4q_kv_decode_mx64.hip", "fp4q_kv_decode_mx96.hip", "fp4q_kv_decode_mx128.hip",
-           "fp4q_kv_decode_mx256.hip", "fp4q_kv_decode_nv64.hip", "fp4q_kv_decode_nv96.hip",
-           "fp4q_kv_decode_nv128.hip", "fp4q_kv_decode_nv256.hip"]
+           *["fp4q_kv_%s_%s%d.hip" % (kind, fmt, dim)
+             for dim in (256, 128, 96, 64) for kind in ("decode", "prefill") for fmt in ("mx", "nv")]]
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-fPIC", "-std=c++17",
     "-ffp-contract=off", "-fno-fast-math", "-fno-gpu-flush-denormals-to-zero",

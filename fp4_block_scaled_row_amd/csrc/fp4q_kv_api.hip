@@ -118,25 +118,44 @@ fp4q_status check_attention(const fp4q_kv_cache* cache, const fp4q_kv_attention_
   return FP4Q_OK;
 }
 
-// Blocks of 16 query rows that a workgroup of the few-row kernels takes.
-int decode_tiles(const KvAttendLaunch& a) { return (int64_t)a.max_q * a.group <= 16 ? 1 : 2; }
+// Which kernels: up to 32 query rows of a cache head the few-row ones with
+// blocks of 16 or 32 rows, above them the many-row ones with 32 rows a wave.
+struct Plan {
+  bool prefill;
+  int tiles, waves;
+};
+Plan attend_plan(const KvAttendLaunch& a) {
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  Plan p = {rows > 32, rows <= 16 ? 1 : 2, 4};
+  if (rows > 128 && a.head_dim <= 128 && a.dtype == kBF16) p.waves = 8;
+  return p;
+}
 
 }  // namespace
 
-// (at most 3 workgroups of the few-row kernels on a CU)
+// (at most 3 workgroups of the few-row kernels on a CU, 8 waves of the others)
 size_t kv_attend_workspace(const KvAttendLaunch& a) {
-  return kv_partial_bytes((int64_t)device_cu_count() * 3, 16 * decode_tiles(a), a.head_dim);
+  const Plan p = attend_plan(a);
+  const int64_t cus = device_cu_count();
+  if (p.prefill) return kv_partial_bytes(cus * 8 / p.waves, 32 * p.waves, a.head_dim);
+  return kv_partial_bytes(cus * 3, 16 * p.tiles, a.head_dim);
 }
 
 hipError_t launch_kv_attend(const KvAttendLaunch& a, hipStream_t s) {
-  const int tiles = decode_tiles(a), cus = device_cu_count();
-  const bool nv = a.format == 1;
+  const Plan p = attend_plan(a);
+  const int cus = device_cu_count();
+#define FP4Q_KV_LAUNCH(D)                                                                     \
+  case D:                                                                                     \
+    if (p.prefill)                                                                            \
+      return a.format == 1 ? launch_prefill_nv##D(a, p.waves, cus, s) : launch_prefill_mx##D(a, p.waves, cus, s); \
+    return a.format == 1 ? launch_decode_nv##D(a, p.tiles, cus, s) : launch_decode_mx##D(a, p.tiles, cus, s)
   switch (a.head_dim) {
-    case 64: return nv ? launch_decode_nv64(a, tiles, cus, s) : launch_decode_mx64(a, tiles, cus, s);
-    case 96: return nv ? launch_decode_nv96(a, tiles, cus, s) : launch_decode_mx96(a, tiles, cus, s);
-    case 128: return nv ? launch_decode_nv128(a, tiles, cus, s) : launch_decode_mx128(a, tiles, cus, s);
-    case 256: return nv ? launch_decode_nv256(a, tiles, cus, s) : launch_decode_mx256(a, tiles, cus, s);
+    FP4Q_KV_LAUNCH(64);
+    FP4Q_KV_LAUNCH(96);
+    FP4Q_KV_LAUNCH(128);
+    FP4Q_KV_LAUNCH(256);
   }
+#undef FP4Q_KV_LAUNCH
   return hipErrorInvalidValue;
 }
 

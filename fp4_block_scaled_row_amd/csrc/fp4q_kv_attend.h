@@ -298,9 +298,8 @@ __device__ __forceinline__ void kv_sequence(const KvAttendLaunch& a, int b, KvUn
 }
 
 template <int kRows, int kTokens>
-__device__ __forceinline__ void kv_block(const KvAttendLaunch& a, int block, KvUnit& u) {
-  u.block = block;
-  u.row0 = block * kRows;
+__device__ __forceinline__ void kv_block_at(const KvAttendLaunch& a, int row0, KvUnit& u) {
+  u.row0 = row0;
   const int i0 = (int)quotient((uint32_t)u.row0, a.group_div);
   const int i1 = min((int)quotient((uint32_t)(u.row0 + kRows - 1), a.group_div), u.m - 1);
   const int64_t past = (int64_t)u.n - u.m;    // tokens before the first query's (may be negative)
@@ -309,6 +308,11 @@ __device__ __forceinline__ void kv_block(const KvAttendLaunch& a, int block, KvU
   u.hi = (int)(hi < 0 ? 0 : hi);
   u.lo = (int)(lo < 0 ? 0 : (lo > u.hi ? u.hi : lo));
   u.groups = max(1, (u.hi - u.lo + kTokens - 1) / kTokens);
+}
+template <int kRows, int kTokens>
+__device__ __forceinline__ void kv_block(const KvAttendLaunch& a, int block, KvUnit& u) {
+  u.block = block;
+  kv_block_at<kRows, kTokens>(a, block * kRows, u);
 }
 
 // Block number -> sequence and block; false: a skipped number.

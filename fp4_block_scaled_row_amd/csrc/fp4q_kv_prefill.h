@@ -1,0 +1,368 @@
+// fp4q_kv_prefill.h -- attention over the 4-bit cache for many query rows.
+//
+// Bound by the matrix instructions and the exponentials.  A workgroup of kW
+// waves takes a block of 32 kW query rows; it goes through the tokens 64 at a
+// time, which its waves turn from codes into fp16 / bf16 in LDS once for all
+// (codes of the next 64 in flight, LDS in two halves, one barrier a step).
+// Each wave works on its own 32 rows: scores by 32x32x16 products with the
+// keys as the left operand, so that a lane holds one row's scores of 32
+// tokens, whose weights are then its part of the second product's right
+// operand, the left one being the values read transposed.
+#pragma once
+
+#include "fp4q_kv_attend.h"
+
+namespace fp4q {
+
+constexpr int kStepTokens = 64;
+
+template <int FMT, int D, int kW, int kQ, int kP>
+struct PrefillShape {
+  static constexpr int kRows = 32 * kW;
+  static constexpr int kThreadsWg = 64 * kW;
+  static constexpr int kKStride = D + 8;                     // halves: rows 4 banks apart
+  // transposed reads take 4 rows of 16 words at once: rows 16 or 48 banks apart
+  static constexpr int kVStride = D == 96 ? D : D + 32;
+  static constexpr int kHalf = kStepTokens * (kKStride + kVStride);
+  // two waves a SIMD where the registers allow it
+  static constexpr int kWavesPerSimd = D <= 128 && kQ <= 2 && kP == 1 ? 2 : 1;
+};
+
+// The wave's query rows as right operands: lane's row l % 32, elements
+// 16 c + 8 (l / 32) .. + 7 of chunk c; returns the factor from raw score to
+// exponent of two.
+template <int FMT, int D, int kQ>
+__device__ __forceinline__ float wave_queries(const KvAttendLaunch& a, const KvUnit& u, int row, int half,
+                                              u32x4_t qf[kQ][D / 16]) {
+  float v[D / 16][8];
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) load_q8(a, u, row, 2 * c + half, v[c]);
+  if constexpr (D % 128 == 0) {
+    if (a.rotate) {
+      // elements 1, 2, 4 apart in a lane's 8, 8 apart between the lanes' two
+      // halves, 16, 32 and 64 apart between its chunks
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+#pragma unroll
+        for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i & h) continue;
+            const float x = v[c][i], y = v[c][i + h];
+            v[c][i] = x + y;
+            v[c][i + h] = x - y;
+          }
+        const float sign = half ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i], sign, __shfl_xor(v[c][i], 32, 64));
+      }
+#pragma unroll
+      for (int k = 0; k < D / 16; k += 8)
+#pragma unroll
+        for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (c & h) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x = v[k + c][i], y = v[k + c + h][i];
+              v[k + c][i] = x + y;
+              v[k + c + h][i] = x - y;
+            }
+          }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= a.rot_scale;
+    }
+  }
+  float factor = a.scale * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f), up = 1.0f;
+  if constexpr (kv_scaled_rows<FMT, kQ>()) {
+    uint32_t most = 0u;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) most = max(most, abs_max_bits8(v[c]));
+    most = max(most, (uint32_t)__shfl_xor((int)most, 32, 64));
+    const uint32_t e = min(max(most >> 23, 9u), 254u);
+    up = as_f((262u - e) << 23);
+    factor *= as_f((e - 8u) << 23);
+  }
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t w[4][kQ];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) pieces<FMT, kQ>(v[c][2 * j] * up, v[c][2 * j + 1] * up, w[j]);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) qf[q][c] = u32x4_t{w[0][q], w[1][q], w[2][q], w[3][q]};
+  }
+  return factor;
+}
+
+template <int FMT, int D, int kW, int kQ, int kP>
+__global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesPerSimd)) void kv_prefill_kernel(
+    KvAttendLaunch a, int64_t numbers) {
+  using Shape = PrefillShape<FMT, D, kW, kQ, kP>;
+  using T = KvType<FMT>;
+  using Lane = KvLane<FMT, D>;
+  constexpr int kRows = Shape::kRows;
+  constexpr int kTasks = 8 / kW;       // 16 tokens' keys or values a task: 8 in a step
+  __shared__ __align__(16) uint16_t s_kv[2 * Shape::kHalf];
+  __shared__ long long s_scan[kW + 3];
+  __shared__ int s_bad;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4, col = lane & 31, half = lane >> 5;
+
+  KvStretch st;
+  if (!kv_stretch<kRows, kStepTokens, 64 * kW>(a, numbers, st, s_scan)) {
+    if (tid == 0) kv_shared(a)[blockIdx.x] = KvShared{0, 0, 0, 0, 0, 0, 0, 0};
+    return;
+  }
+  int shared_first = 0, shared_last = 0, shared_b = 0, shared_head = 0, shared_row0 = 0;
+  KvUnit u = st.u;
+  int group = st.group;
+  int64_t left = st.left;
+  for (;;) {
+    const int last = (int)min((int64_t)u.groups, group + left);
+    const int row0 = u.row0 + 32 * wave;
+    u32x4_t qf[kQ][D / 16];
+    const float factor = wave_queries<FMT, D, kQ>(a, u, row0 + col, half, qf);
+    int sees_from;
+    uint32_t sees;
+    kv_sees(a, u, row0 + col, sees_from, sees);
+    // tokens that all rows of the block, all of the wave, any of the wave see
+    int block_from, block_to, all_from, all_to;
+    kv_all_see<kRows>(a, u, block_from, block_to);
+    KvUnit wu = u;
+    kv_block_at<32, kStepTokens>(a, row0, wu);
+    kv_all_see<32>(a, wu, all_from, all_to);
+    const bool rows = (int)quotient((uint32_t)row0, a.group_div) < u.m;
+
+    f32x16_t o[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] = f32x16_t{};
+    float m = kNoMax, l = 0.0f;
+
+    const int32_t* table = a.table + u.b * a.table_stride;
+    const KvHead planes = kv_head(a.p, u.head);
+    const int n = u.hi;
+    // task x of this wave: tokens 16 (task / 2) .. + 15 of a step, their keys
+    // (even) or values (odd); see the few-row kernel for the loads
+    Lane in[kTasks];
+    int32_t pages[kTasks];
+    bool there[kTasks];
+    const int task0 = wave * kTasks;
+    auto find = [&](int grp) {
+#pragma unroll
+      for (int x = 0; x < kTasks; ++x) {
+        const int t = min(u.lo + grp * kStepTokens + 16 * ((task0 + x) >> 1) + r, n - 1);
+        pages[x] = table[quotient((uint32_t)t, a.p.page)];
+      }
+    };
+    auto fetch = [&](int grp) {
+#pragma unroll
+      for (int x = 0; x < kTasks; ++x) {
+        const int t = u.lo + grp * kStepTokens + 16 * ((task0 + x) >> 1) + r;
+        const uint32_t tt = (uint32_t)min(t, n - 1);
+        const bool page = (uint32_t)pages[x] < (uint32_t)a.p.num_pages;
+        const KvAt at = kv_at(a.p, page ? (uint32_t)pages[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
+        const bool values = (task0 + x) & 1;
+        in[x].load((values ? planes.vc : planes.kc) + at.code, (values ? planes.vs : planes.ks) + at.scale, g);
+        there[x] = page && t < n;
+      }
+    };
+    auto put = [&](int grp) {
+      const int t0 = u.lo + grp * kStepTokens;
+      const bool edge = t0 + kStepTokens > block_to || t0 < block_from;
+      uint16_t* base = s_kv + (grp & 1) * Shape::kHalf;
+#pragma unroll
+      for (int x = 0; x < kTasks; ++x) {
+        const bool values = (task0 + x) & 1;
+        in[x].keep_if(there[x]);
+        if (values && edge) {
+          const bool left_out = in[x].drop_not_finite();
+          if (__any(left_out)) s_bad = 1;
+        }
+        const typename Lane::Scales sc = in[x].prepare();
+        const int t = 16 * ((task0 + x) >> 1) + r;
+        uint16_t* dst = values ? base + kStepTokens * Shape::kKStride + t * Shape::kVStride : base + t * Shape::kKStride;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) *reinterpret_cast<u32x4_t*>(dst + Lane::element(c, g)) = in[x].values(c, sc);
+      }
+    };
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    if (n > 0) {
+      find(group);
+      fetch(group);
+      find(group + 1);
+      put(group);
+      fetch(group + 1);
+      find(group + 2);
+    }
+    __syncthreads();
+    for (int grp = group; grp < last; ++grp) {
+      const int t0 = u.lo + grp * kStepTokens;
+      if (t0 >= n) break;                       // (a unit without tokens)
+      if (rows && t0 < wu.hi && t0 + kStepTokens > wu.lo) {
+        const uint16_t* ks = s_kv + (grp & 1) * Shape::kHalf + col * Shape::kKStride + 8 * half;
+        f32x16_t s[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          s[x] = f32x16_t{};
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(ks + 32 * x * Shape::kKStride + 16 * c);
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) s[x] = T::mfma32(kf, qf[q][c], s[x]);
+          }
+        }
+        // token 32 x + 8 (i / 4) + 4 half + i % 4 of the step
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = s[i >> 4][i & 15] * factor;
+        if (t0 + kStepTokens > all_to || t0 < all_from) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t j = (uint32_t)(t0 + 8 * (i >> 2) + 4 * half + (i & 3) - sees_from);
+            y[i] = j < sees ? y[i] : -INFINITY;
+          }
+        }
+        float most = y[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) most = fmaxf(most, y[i]);
+        if (__any(most > m + kRaise)) {
+          const float x = fmaxf(fmaxf(most, __shfl_xor(most, 32, 64)), m);
+          const float f = __builtin_amdgcn_exp2f(m - x);
+          m = x;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) o[c] *= f;
+        }
+        const float top = m - T::kUp;
+        u32x4_t w[4][kP];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[4][kP];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p0 = __builtin_amdgcn_exp2f(y[8 * k + 2 * j] - top);
+            const float p1 = __builtin_amdgcn_exp2f(y[8 * k + 2 * j + 1] - top);
+            l += p0 + p1;
+            pieces<FMT, kP>(p0, p1, h[j]);
+          }
+#pragma unroll
+          for (int q = 0; q < kP; ++q) w[k][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
+        }
+        // weighted values: element 32 c + 8 (i / 4) + 4 half + i % 4 of the row
+        const uint16_t* vs = s_kv + (grp & 1) * Shape::kHalf + kStepTokens * Shape::kKStride +
+                             (4 * half + (r >> 2)) * Shape::kVStride + 16 * (g & 1) + 4 * (r & 3);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const u32x2_t x0 = read_transposed(vs + 16 * k * Shape::kVStride + 32 * c);
+            const u32x2_t x1 = read_transposed(vs + (16 * k + 8) * Shape::kVStride + 32 * c);
+            const u32x4_t vf = {x0.x, x0.y, x1.x, x1.y};
+#pragma unroll
+            for (int q = 0; q < kP; ++q) o[c] = T::mfma32(vf, w[k][q], o[c]);
+          }
+      }
+      if (grp + 1 < last) {
+        put(grp + 1);
+        fetch(grp + 2);
+        find(grp + 3);
+      }
+      __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    const bool whole = group == 0 && last == u.groups;
+    const int rr = 32 * wave + col;
+    if (s_bad) {
+      const int t1 = min(u.hi, u.lo + last * kStepTokens);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const int d = 32 * c + 2 * i + 4 * half;
+          const float f = kv_sees_nan<FMT, D>(a, u, u.row0 + rr, d, u.lo + group * kStepTokens, t1) ? as_f(0x7FC00000u) : 1.0f;
+          o[c] = f32x16_t{i == 0 ? o[c][0] * f : o[c][0],    i == 0 ? o[c][1] * f : o[c][1],
+                          i == 0 ? o[c][2] * f : o[c][2],    i == 0 ? o[c][3] * f : o[c][3],
+                          i == 4 ? o[c][4] * f : o[c][4],    i == 4 ? o[c][5] * f : o[c][5],
+                          i == 4 ? o[c][6] * f : o[c][6],    i == 4 ? o[c][7] * f : o[c][7],
+                          i == 8 ? o[c][8] * f : o[c][8],    i == 8 ? o[c][9] * f : o[c][9],
+                          i == 8 ? o[c][10] * f : o[c][10],  i == 8 ? o[c][11] * f : o[c][11],
+                          i == 12 ? o[c][12] * f : o[c][12], i == 12 ? o[c][13] * f : o[c][13],
+                          i == 12 ? o[c][14] * f : o[c][14], i == 12 ? o[c][15] * f : o[c][15]};
+        }
+    }
+    if (whole) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          kv_finish4<FMT, D>(a, u, u.row0 + rr, 32 * c + 2 * i + 4 * half,
+                             f32x4_t{o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]}, m, l);
+    } else {
+      if (group == 0) {
+        shared_last = 1;
+        shared_b = u.b;
+        shared_head = u.head;
+        shared_row0 = u.row0;
+      } else {
+        shared_first = last == u.groups ? 2 : 1;
+      }
+      float* part = kv_partial<D, kRows>(a, gridDim.x, blockIdx.x, group == 0);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f32x4_t*>(part + (int64_t)rr * D + 32 * c + 2 * i + 4 * half) =
+              f32x4_t{o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]};
+      if (half == 0) {
+        part[(int64_t)kRows * D + rr] = m;
+        part[(int64_t)kRows * (D + 1) + rr] = l;
+      }
+    }
+    left -= last - group;
+    if (left <= 0) break;
+    group = 0;
+    kv_next<kRows, kStepTokens>(a, u);
+    __syncthreads();      // (everyone has read s_bad)
+  }
+  if (tid == 0)
+    kv_shared(a)[blockIdx.x] = KvShared{shared_first, shared_last, shared_b, shared_head, shared_row0, 0, 0, 0};
+}
+
+template <int FMT, int D, int kW, int kQ, int kP>
+hipError_t launch_prefill_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
+  using Shape = PrefillShape<FMT, D, kW, kQ, kP>;
+  constexpr int kRows = Shape::kRows;
+  const int64_t numbers = kv_block_numbers<kRows>(a);
+  const int64_t groups = (a.most_tokens + kStepTokens - 1) / kStepTokens;
+  const int64_t most = numbers * a.p.heads * (groups < 1 ? 1 : groups);
+  const int64_t resident = (int64_t)cus * (4 * Shape::kWavesPerSimd / kW);
+  const int grid = (int)(most < resident ? most : resident);
+  hipLaunchKernelGGL((kv_prefill_kernel<FMT, D, kW, kQ, kP>), dim3(grid), dim3(64 * kW), 0, st, a, numbers);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || groups <= 1) return e;
+  hipLaunchKernelGGL((kv_join_kernel<FMT, D, kRows>), dim3(grid, kRows / kWaves), dim3(kThreads), 0, st, a, grid);
+  return hipGetLastError();
+}
+
+// Waves: 8 where two of them fit a SIMD, for blocks of 256 rows; 4 elsewhere
+// and where sequences have at most 128 rows.
+template <int D, int FMT>
+hipError_t launch_prefill_d(const KvAttendLaunch& a, int waves, int cus, hipStream_t st) {
+  if (a.dtype == kF32) return launch_prefill_t<FMT, D, 4, FMT == 1 ? 2 : 3, 2>(a, cus, st);
+  if constexpr (D <= 128) {
+    if (waves == 8) {
+      if (a.rotate) return launch_prefill_t<FMT, D, 8, 2, 1>(a, cus, st);
+      return launch_prefill_t<FMT, D, 8, 1, 1>(a, cus, st);
+    }
+  }
+  if (a.rotate) return launch_prefill_t<FMT, D, 4, 2, 1>(a, cus, st);
+  return launch_prefill_t<FMT, D, 4, 1, 1>(a, cus, st);
+}
+
+}  // namespace fp4q
