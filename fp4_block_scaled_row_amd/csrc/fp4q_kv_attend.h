@@ -262,7 +262,10 @@ __device__ __forceinline__ u32x2_t read_transposed(const uint16_t* p) {
 // head; it has to go through the groups of kTokens tokens that any of its rows
 // sees.  The groups of all units are numbered through, (sequence, block)
 // first, then cache head, and workgroup w of W takes the w-th stretch of equal
-// length: whatever the lengths are, all have the same to do.  Blocks are found
+// length: whatever the lengths are, all have the same to do.  A unit counts
+// kCost groups more than it has, for what it takes to begin and end it (without
+// that the workgroup with the shortest units of a causal prompt, 25 of them
+// where others had 2, made the call 1.6 times longer).  Blocks are found
 // by numbers too: block k of sequence b has the number cu[b] group / kRows + b
 // + k (rounded down), which leaves room for each sequence's blocks and skips
 // at most one number a sequence, so that a thread finds a number's sequence by
@@ -331,16 +334,23 @@ __device__ __forceinline__ bool kv_numbered(const KvAttendLaunch& a, int64_t num
   return true;
 }
 
-// A workgroup's stretch: `left` groups from group `group` of unit `u` on.
+// A workgroup's stretch: `left` counted groups from the `at`-th of unit `u` on.
 struct KvStretch {
   KvUnit u;
-  int group;
+  int at;
   int64_t left;
 };
+// The groups [from, to) that a stretch has of its current unit: none where it
+// ends within the unit's kCost.
+template <int kCost>
+__device__ __forceinline__ void kv_part(const KvStretch& st, int& from, int& to) {
+  from = max(0, st.at - kCost);
+  to = max(0, (int)min((int64_t)st.u.groups + kCost, st.at + st.left) - kCost);
+}
 
 // Every thread of the workgroup calls it, with all query block numbers below
 // `numbers`; scratch: 8 + 2 waves words of LDS.  False: nothing to do.
-template <int kRows, int kTokens, int kThreadsWg>
+template <int kRows, int kTokens, int kCost, int kThreadsWg>
 __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numbers, KvStretch& st, long long* scratch) {
   constexpr int kW = kThreadsWg / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -349,7 +359,7 @@ __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numb
   long long mine = 0;
   for (int64_t x = x0; x < x1; ++x) {
     KvUnit u;
-    if (kv_numbered<kRows, kTokens>(a, x, u)) mine += (long long)u.groups * a.p.heads;
+    if (kv_numbered<kRows, kTokens>(a, x, u)) mine += (long long)(u.groups + kCost) * a.p.heads;
   }
   long long upto = mine;     // inclusive scan over the workgroup
 #pragma unroll
@@ -373,7 +383,7 @@ __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numb
     KvUnit u;
     for (int64_t x = x0; x < x1; ++x) {
       if (!kv_numbered<kRows, kTokens>(a, x, u)) continue;
-      const long long here = (long long)u.groups * a.p.heads;
+      const long long here = (long long)(u.groups + kCost) * a.p.heads;
       if (begin < before + here) break;
       before += here;
     }
@@ -387,16 +397,20 @@ __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numb
   const int64_t in_block = scratch[kW + 2];
   kv_sequence<kRows, kTokens>(a, b, st.u);
   kv_block<kRows, kTokens>(a, block, st.u);
-  st.u.head = __builtin_amdgcn_readfirstlane((int)(in_block / st.u.groups));
-  st.group = __builtin_amdgcn_readfirstlane((int)(in_block - (int64_t)st.u.head * st.u.groups));
+  st.u.head = __builtin_amdgcn_readfirstlane((int)(in_block / (st.u.groups + kCost)));
+  st.at = __builtin_amdgcn_readfirstlane((int)(in_block - (int64_t)st.u.head * (st.u.groups + kCost)));
   st.left = total - begin < share ? total - begin : share;
   return true;
 }
 
-// The next unit (there is one while groups are left).
-template <int kRows, int kTokens>
-__device__ __forceinline__ void kv_next(const KvAttendLaunch& a, KvUnit& u) {
-  if (++u.head < a.p.heads) return;
+// Goes on to the next unit; false: the stretch is done.
+template <int kRows, int kTokens, int kCost>
+__device__ __forceinline__ bool kv_next(const KvAttendLaunch& a, KvStretch& st) {
+  KvUnit& u = st.u;
+  st.left -= u.groups + kCost - st.at;
+  if (st.left <= 0) return false;
+  st.at = 0;
+  if (++u.head < a.p.heads) return true;
   u.head = 0;
   int block = u.block + 1;
   while (block >= u.blocks && u.b + 1 < a.seqs) {
@@ -404,6 +418,7 @@ __device__ __forceinline__ void kv_next(const KvAttendLaunch& a, KvUnit& u) {
     block = 0;
   }
   kv_block<kRows, kTokens>(a, block, u);
+  return true;
 }
 
 // Numbers of all query blocks lie below this.

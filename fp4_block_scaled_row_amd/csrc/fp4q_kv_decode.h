@@ -17,6 +17,7 @@
 namespace fp4q {
 
 constexpr int kGroupTokens = 128;
+constexpr int kGroupCost = 2;     // groups that beginning and ending a unit takes as long as
 
 template <int FMT, int D, int kTiles, int kQ, int kP>
 struct DecodeShape {
@@ -56,17 +57,16 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   uint16_t* sq = reinterpret_cast<uint16_t*>(s_main + (Shape::kQRegs ? 0 : Shape::kMain));
 
   KvStretch st;
-  if (!kv_stretch<kRows, kGroupTokens, kThreads>(a, numbers, st, s_scan)) {
+  if (!kv_stretch<kRows, kGroupTokens, kGroupCost, kThreads>(a, numbers, st, s_scan)) {
     if (tid == 0) kv_shared(a)[blockIdx.x] = KvShared{0, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
   int shared_first = 0, shared_last = 0, shared_b = 0, shared_head = 0, shared_row0 = 0;
-  KvUnit u = st.u;
-  int group = st.group;
-  int64_t left = st.left;
-  for (;;) {
-    // the unit's groups [group, last) are this workgroup's
-    const int last = (int)min((int64_t)u.groups, group + left);
+  const KvUnit& u = st.u;
+  do {
+    int group, last;      // the unit's groups [group, last) are this workgroup's
+    kv_part<kGroupCost>(st, group, last);
+    if (group == last) continue;
     stage_queries<FMT, D, kQ, kRows>(a, u, sq, s_factor, s_most);
 
     u32x4_t qf[Shape::kQRegs ? kTiles : 1][Shape::kQRegs ? kQ : 1][Shape::kQRegs ? kChunks : 1];
@@ -302,12 +302,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       }
     }
     __syncthreads();
-
-    left -= last - group;
-    if (left <= 0) break;
-    group = 0;
-    kv_next<kRows, kGroupTokens>(a, u);
-  }
+  } while (kv_next<kRows, kGroupTokens, kGroupCost>(a, st));
   if (tid == 0)
     kv_shared(a)[blockIdx.x] = KvShared{shared_first, shared_last, shared_b, shared_head, shared_row0, 0, 0, 0};
 }
@@ -317,7 +312,7 @@ hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   constexpr int kRows = 16 * kTiles;
   const int64_t numbers = kv_block_numbers<kRows>(a);
   const int64_t groups = (a.most_tokens + kGroupTokens - 1) / kGroupTokens;
-  const int64_t most = numbers * a.p.heads * (groups < 1 ? 1 : groups);
+  const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kGroupCost);
   const int64_t resident = (int64_t)cus * DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd;
   const int grid = (int)(most < resident ? most : resident);
   hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP>), dim3(grid), dim3(kThreads), 0, st, a, numbers);

@@ -15,6 +15,7 @@
 namespace fp4q {
 
 constexpr int kStepTokens = 64;
+constexpr int kStepCost = 6;      // steps that beginning and ending a unit takes as long as
 
 template <int FMT, int D, int kW, int kQ, int kP>
 struct PrefillShape {
@@ -113,35 +114,19 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
   const int r = lane & 15, g = lane >> 4, col = lane & 31, half = lane >> 5;
 
   KvStretch st;
-  if (!kv_stretch<kRows, kStepTokens, 64 * kW>(a, numbers, st, s_scan)) {
+  if (!kv_stretch<kRows, kStepTokens, kStepCost, 64 * kW>(a, numbers, st, s_scan)) {
     if (tid == 0) kv_shared(a)[blockIdx.x] = KvShared{0, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
   int shared_first = 0, shared_last = 0, shared_b = 0, shared_head = 0, shared_row0 = 0;
-  KvUnit u = st.u;
-  int group = st.group;
-  int64_t left = st.left;
-  for (;;) {
-    const int last = (int)min((int64_t)u.groups, group + left);
+  const KvUnit& u = st.u;
+  do {
+    int group, last;      // the unit's groups [group, last) are this workgroup's
+    kv_part<kStepCost>(st, group, last);
+    if (group == last) continue;
     const int row0 = u.row0 + 32 * wave;
-    u32x4_t qf[kQ][D / 16];
-    const float factor = wave_queries<FMT, D, kQ>(a, u, row0 + col, half, qf);
-    int sees_from;
-    uint32_t sees;
-    kv_sees(a, u, row0 + col, sees_from, sees);
-    // tokens that all rows of the block, all of the wave, any of the wave see
-    int block_from, block_to, all_from, all_to;
+    int block_from, block_to;     // tokens that all rows of the block see
     kv_all_see<kRows>(a, u, block_from, block_to);
-    KvUnit wu = u;
-    kv_block_at<32, kStepTokens>(a, row0, wu);
-    kv_all_see<32>(a, wu, all_from, all_to);
-    const bool rows = (int)quotient((uint32_t)row0, a.group_div) < u.m;
-
-    f32x16_t o[D / 32];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) o[c] = f32x16_t{};
-    float m = kNoMax, l = 0.0f;
-
     const int32_t* table = a.table + u.b * a.table_stride;
     const KvHead planes = kv_head(a.p, u.head);
     const int n = u.hi;
@@ -189,12 +174,32 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         for (int c = 0; c < D / 32; ++c) *reinterpret_cast<u32x4_t*>(dst + Lane::element(c, g)) = in[x].values(c, sc);
       }
     };
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
+    // (the first loads are on their way while the queries are prepared)
     if (n > 0) {
       find(group);
       fetch(group);
       find(group + 1);
+    }
+    if (tid == 0) s_bad = 0;
+    u32x4_t qf[kQ][D / 16];
+    const float factor = wave_queries<FMT, D, kQ>(a, u, row0 + col, half, qf);
+    int sees_from;
+    uint32_t sees;
+    kv_sees(a, u, row0 + col, sees_from, sees);
+    // tokens that all of the wave's rows see; any of them: [wu.lo, wu.hi)
+    int all_from, all_to;
+    KvUnit wu = u;
+    kv_block_at<32, kStepTokens>(a, row0, wu);
+    kv_all_see<32>(a, wu, all_from, all_to);
+    const bool rows = (int)quotient((uint32_t)row0, a.group_div) < u.m;
+
+    f32x16_t o[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] = f32x16_t{};
+    float m = kNoMax, l = 0.0f;
+
+    __syncthreads();
+    if (n > 0) {
       put(group);
       fetch(group + 1);
       find(group + 2);
@@ -324,12 +329,8 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         part[(int64_t)kRows * (D + 1) + rr] = l;
       }
     }
-    left -= last - group;
-    if (left <= 0) break;
-    group = 0;
-    kv_next<kRows, kStepTokens>(a, u);
     __syncthreads();      // (everyone has read s_bad)
-  }
+  } while (kv_next<kRows, kStepTokens, kStepCost>(a, st));
   if (tid == 0)
     kv_shared(a)[blockIdx.x] = KvShared{shared_first, shared_last, shared_b, shared_head, shared_row0, 0, 0, 0};
 }
@@ -340,7 +341,7 @@ hipError_t launch_prefill_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   constexpr int kRows = Shape::kRows;
   const int64_t numbers = kv_block_numbers<kRows>(a);
   const int64_t groups = (a.most_tokens + kStepTokens - 1) / kStepTokens;
-  const int64_t most = numbers * a.p.heads * (groups < 1 ? 1 : groups);
+  const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kStepCost);
   const int64_t resident = (int64_t)cus * (4 * Shape::kWavesPerSimd / kW);
   const int grid = (int)(most < resident ? most : resident);
   hipLaunchKernelGGL((kv_prefill_kernel<FMT, D, kW, kQ, kP>), dim3(grid), dim3(64 * kW), 0, st, a, numbers);
