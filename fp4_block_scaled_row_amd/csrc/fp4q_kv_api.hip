@@ -118,16 +118,18 @@ fp4q_status check_attention(const fp4q_kv_cache* cache, const fp4q_kv_attention_
   return FP4Q_OK;
 }
 
-// Which kernels: up to 32 query rows of a cache head the few-row ones with
-// blocks of 16 or 32 rows, above them the many-row ones with 32 rows a wave.
+// Which kernels: the few-row ones up to 16 query rows of a cache head, up to
+// 32 where those fit their registers (bf16, head_dim to 128); above that the
+// many-row ones, with 32 rows a wave.
 struct Plan {
   bool prefill;
   int tiles, waves;
 };
 Plan attend_plan(const KvAttendLaunch& a) {
   const int64_t rows = (int64_t)a.max_q * a.group;
-  Plan p = {rows > 32, rows <= 16 ? 1 : 2, 4};
-  if (rows > 128 && a.head_dim <= 128 && a.dtype == kBF16) p.waves = 8;
+  const bool wide = a.dtype == kBF16 && a.head_dim <= 128;
+  Plan p = {rows > (wide ? 32 : 16), rows <= 16 ? 1 : 2, 4};
+  if (rows > 128 && wide) p.waves = 8;
   return p;
 }
 

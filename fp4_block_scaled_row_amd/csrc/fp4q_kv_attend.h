@@ -12,8 +12,11 @@
 // applies the scale).  The tensor scales are applied in fp32, the keys' to
 // the scores and the values' to the output.
 //   The queries enter as a sum of kQ pieces in that type, each the rounding of
-// what the ones before left: a bf16 query is exact in one piece, a rotated one
-// keeps 16 (bf16) or 22 (fp16) bits in two, an fp32 one 22 to 24.  fp16 pieces
+// what the ones before left.  A bf16 query is exact in one piece; rotated, it
+// keeps 16 bits in two bf16 pieces, or 11 in one fp16 piece, which moves a
+// score by 2^-12 of its terms and the output by less than its rounding to
+// bf16 (a call that returns log-sum-exps takes two, 22 bits); an fp32 one
+// keeps 22 (fp16) or 24 (bf16).  fp16 pieces
 // are scaled by a power of two per row that puts the row's largest value in
 // [2^8, 2^9).  The softmax weights enter in kP pieces: one (2^-12 in fp16,
 // 2^-9 in bf16 relative to the weight, below the bf16 output's own rounding)
@@ -507,6 +510,12 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttendLaunch a, int
   }
   if (a.lse && lane == 0)
     a.lse[o.at] = all == 0.0f ? -INFINITY : (top - KvType<FMT>::kUp + __builtin_amdgcn_logf(all)) * kLn2;
+}
+
+// Pieces of bf16 queries.
+template <int FMT>
+inline int kv_rotated_pieces(const KvAttendLaunch& a) {
+  return a.rotate && (FMT == 0 || a.lse) ? 2 : 1;
 }
 
 template <int FMT, int kQ>

@@ -75,59 +75,81 @@ __device__ __forceinline__ uint32_t mx_encode_block(const float v[8], uint32_t a
   return codes;
 }
 
-template <int FMT, int IN>
+// A thread takes kSlots slots, a workgroup's width apart (all loads first).
+template <int FMT, int IN, int kSlots>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteLaunch w, float rot_scale, FastDiv row_slots,
                                                             FastDiv heads, uint32_t nslots) {
   const bool values = blockIdx.y != 0;
-  const uint32_t s = blockIdx.x * kThreads + threadIdx.x;
-  const bool in_range = s < nslots;
-  const uint32_t row = quotient(in_range ? s : 0u, row_slots), at = (in_range ? s : 0u) - row * row_slots.d;
-  const uint32_t token = quotient(row, heads), head = row - token * heads.d;
-  const int64_t slot = w.slots[token];
-  const bool active = in_range && slot >= 0 && slot < (int64_t)w.p.num_pages * w.p.page.d;
-  SlotRaw<IN> r;
+  const uint32_t s0 = blockIdx.x * (kSlots * kThreads) + threadIdx.x;
+  const int64_t token_stride = values ? w.v_stride[0] : w.k_stride[0], head_stride = values ? w.v_stride[1] : w.k_stride[1];
+  const void* x = values ? w.v : w.k;
+  uint32_t head[kSlots], at[kSlots];
+  int64_t slot[kSlots];
+  SlotRaw<IN> raw[kSlots];
 #pragma unroll
-  for (int i = 0; i < (IN == kF32 ? 8 : 4); ++i) r.w[i] = 0u;
-  if (active) {
-    const int64_t off = values ? token * w.v_stride[0] + head * w.v_stride[1] : token * w.k_stride[0] + head * w.k_stride[1];
-    const void* x = values ? w.v : w.k;
+  for (int u = 0; u < kSlots; ++u) {
+    const uint32_t s = min(s0 + u * kThreads, nslots - 1);
+    const uint32_t row = quotient(s, row_slots), token = quotient(row, heads);
+    at[u] = s - row * row_slots.d;
+    head[u] = row - token * heads.d;
+    slot[u] = w.slots[token];
+    const int64_t off = token * token_stride + head[u] * head_stride + 8 * at[u];
     if constexpr (IN == kF32) {
-      const float* p = static_cast<const float*>(x) + off + 8 * at;
+      const float* p = static_cast<const float*>(x) + off;
       const u32x4_t a = load16<true>(p), b = load16<true>(p + 4);
-      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
-      r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+      raw[u].w[0] = a.x; raw[u].w[1] = a.y; raw[u].w[2] = a.z; raw[u].w[3] = a.w;
+      raw[u].w[4] = b.x; raw[u].w[5] = b.y; raw[u].w[6] = b.z; raw[u].w[7] = b.w;
     } else {
-      const u32x4_t a = load16<true>(static_cast<const uint16_t*>(x) + off + 8 * at);
-      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+      const u32x4_t a = load16<true>(static_cast<const uint16_t*>(x) + off);
+      raw[u].w[0] = a.x; raw[u].w[1] = a.y; raw[u].w[2] = a.z; raw[u].w[3] = a.w;
     }
   }
-  float v[8];
-  widen_slot<IN>(r, v);
-  // (head_dim is a multiple of 128 here, so 16 consecutive lanes hold one chunk)
-  if (w.rotate && !values) fwht128_lanes(v, threadIdx.x & 15, rot_scale);
-  uint32_t amax = abs_max_bits8(v);
-  amax = max(amax, dpp_u32<kQuadXor1>(amax));
-  if constexpr (FMT == 0) amax = max(amax, dpp_u32<kQuadXor2>(amax));
-  uint32_t scale, codes;
-  if constexpr (FMT == 0) codes = mx_encode_block(v, amax, scale);
-  else codes = nv_encode_block(v, as_f(amax), *(values ? w.p.vg : w.p.kg), scale);
-  if (amax >= 0x7F800000u) {   // a block with an infinity or NaN: the NaN scale code
-    codes = 0u;
-    scale = FMT == 0 ? 0xFFu : 0x7Fu;
+  const int64_t held = (int64_t)w.p.num_pages * w.p.page.d;
+  const float g = FMT == 0 ? 1.0f : *(values ? w.p.vg : w.p.kg);
+  uint8_t* cbase = values ? w.p.vc : w.p.kc;
+  uint8_t* sbase = values ? w.p.vs : w.p.ks;
+#pragma unroll
+  for (int u = 0; u < kSlots; ++u) {
+    float v[8];
+    widen_slot<IN>(raw[u], v);
+    // (head_dim is a multiple of 128 here, so 16 consecutive lanes hold one chunk)
+    if (w.rotate && !values) fwht128_lanes(v, threadIdx.x & 15, rot_scale);
+    uint32_t amax = abs_max_bits8(v);
+    amax = max(amax, dpp_u32<kQuadXor1>(amax));
+    if constexpr (FMT == 0) amax = max(amax, dpp_u32<kQuadXor2>(amax));
+    uint32_t scale, codes;
+    if constexpr (FMT == 0) codes = mx_encode_block(v, amax, scale);
+    else codes = nv_encode_block(v, as_f(amax), g, scale);
+    if (amax >= 0x7F800000u) {   // a block with an infinity or NaN: the NaN scale code
+      codes = 0u;
+      scale = FMT == 0 ? 0xFFu : 0x7Fu;
+    }
+    if (s0 + u * kThreads >= nslots || slot[u] < 0 || slot[u] >= held) continue;
+    // (64-bit division only where a slot does not fit 32 bits)
+    const int64_t page = slot[u] <= 0x7FFFFFFF ? (int64_t)quotient((uint32_t)slot[u], w.p.page) : slot[u] / w.p.page.d;
+    const int64_t offset = slot[u] - page * w.p.page.d;
+    const int64_t c = page * w.p.code_stride[0] + (int64_t)head[u] * w.p.code_stride[1] + offset * w.p.code_stride[2];
+    *reinterpret_cast<uint32_t*>(cbase + c + 4 * at[u]) = codes;
+    constexpr uint32_t per = FMT == 0 ? 4u : 2u;   // lanes of one block
+    if ((at[u] & (per - 1)) == 0) {
+      const int64_t e = page * w.p.scale_stride[0] + (int64_t)head[u] * w.p.scale_stride[1] + offset * w.p.scale_stride[2];
+      sbase[e + at[u] / per] = (uint8_t)scale;
+    }
   }
-  if (!active) return;
-  // (slot < 2^31 * 2^31: 64-bit division only where it does not fit 32 bits)
-  const int64_t page = slot <= 0x7FFFFFFF ? (int64_t)quotient((uint32_t)slot, w.p.page) : slot / w.p.page.d;
-  const int64_t offset = slot - page * w.p.page.d;
-  uint8_t* cp = (values ? w.p.vc : w.p.kc) + page * w.p.code_stride[0] + (int64_t)head * w.p.code_stride[1] +
-                offset * w.p.code_stride[2];
-  *reinterpret_cast<uint32_t*>(cp + 4 * at) = codes;
-  constexpr uint32_t per = FMT == 0 ? 4u : 2u;   // lanes of one block
-  if ((at & (per - 1)) == 0) {
-    uint8_t* sp = (values ? w.p.vs : w.p.ks) + page * w.p.scale_stride[0] + (int64_t)head * w.p.scale_stride[1] +
-                  offset * w.p.scale_stride[2];
-    sp[at / per] = (uint8_t)scale;
-  }
+}
+
+template <int FMT, int kSlots>
+hipError_t launch_write_n(const KvWriteLaunch& w, uint32_t nslots, hipStream_t st) {
+  const uint32_t per = (uint32_t)w.head_dim / 8;
+  const dim3 grid((nslots + kSlots * kThreads - 1) / (kSlots * kThreads), 2);
+  const float c = (float)(1.0 / sqrt(128.0));
+  if (w.in_dtype == kF32)
+    hipLaunchKernelGGL((kv_write_kernel<FMT, kF32, kSlots>), grid, dim3(kThreads), 0, st, w, c, fast_div(per),
+                       fast_div((uint32_t)w.p.heads), nslots);
+  else
+    hipLaunchKernelGGL((kv_write_kernel<FMT, kBF16, kSlots>), grid, dim3(kThreads), 0, st, w, c, fast_div(per),
+                       fast_div((uint32_t)w.p.heads), nslots);
+  return hipGetLastError();
 }
 
 template <int FMT>
@@ -137,16 +159,10 @@ hipError_t launch_write_t(const KvWriteLaunch& w, int64_t first, int64_t count, 
   part.k = static_cast<const char*>(w.k) + first * w.k_stride[0] * esz;
   part.v = static_cast<const char*>(w.v) + first * w.v_stride[0] * esz;
   part.slots = w.slots + first;
-  const uint32_t per = (uint32_t)w.head_dim / 8, nslots = (uint32_t)(count * w.p.heads * per);
-  const dim3 grid((nslots + kThreads - 1) / kThreads, 2);
-  const float c = (float)(1.0 / sqrt(128.0));
-  if (w.in_dtype == kF32)
-    hipLaunchKernelGGL((kv_write_kernel<FMT, kF32>), grid, dim3(kThreads), 0, st, part, c, fast_div(per),
-                       fast_div((uint32_t)w.p.heads), nslots);
-  else
-    hipLaunchKernelGGL((kv_write_kernel<FMT, kBF16>), grid, dim3(kThreads), 0, st, part, c, fast_div(per),
-                       fast_div((uint32_t)w.p.heads), nslots);
-  return hipGetLastError();
+  const uint32_t nslots = (uint32_t)(count * w.p.heads * (w.head_dim / 8));
+  // four slots a thread once that still leaves every CU several workgroups
+  if (nslots >= (uint32_t)device_cu_count() * 4 * 4 * kThreads) return launch_write_n<FMT, 4>(part, nslots, st);
+  return launch_write_n<FMT, 1>(part, nslots, st);
 }
 
 // ----------------------------------------------------------------------------
@@ -161,90 +177,119 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int64_t t) 
   return lo;
 }
 
+// A thread takes kReadSlots slots, a workgroup's width apart, so that their
+// loads (page, codes, scale) overlap.
+constexpr int kReadSlots = 4;
+
 template <int FMT, int OUT>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float rot_scale, FastDiv row_slots,
                                                            FastDiv heads, uint32_t nslots, int64_t first) {
   const bool values = r.k_out == nullptr || blockIdx.y != 0;
-  const uint32_t s = blockIdx.x * kThreads + threadIdx.x;
-  const bool in_range = s < nslots;
-  const uint32_t row = quotient(in_range ? s : 0u, row_slots), at = (in_range ? s : 0u) - row * row_slots.d;
-  const uint32_t token = quotient(row, heads), head = row - token * heads.d;
-  const int64_t t = first + token;
-  const int b = sequence_of(r.cu, r.seqs, t);
-  const int64_t pos = t - r.cu[b] + (r.starts ? r.starts[b] : 0);
-  const bool there = t < r.cu[b + 1] && pos >= 0 && pos < (int64_t)r.table_cols * r.p.page.d;
-  uint32_t cw = 0u, sb = FMT == 0 ? 127u : 0u;
-  if (there && in_range) {
-    const int64_t col = pos <= 0x7FFFFFFF ? (int64_t)quotient((uint32_t)pos, r.p.page) : pos / r.p.page.d;
-    const int64_t offset = pos - col * r.p.page.d;
-    const int32_t page = r.table[b * r.table_stride + col];
-    if (page >= 0 && page < r.p.num_pages) {
-      const uint8_t* cp = (values ? r.p.vc : r.p.kc) + (int64_t)page * r.p.code_stride[0] + (int64_t)head * r.p.code_stride[1] +
-                          offset * r.p.code_stride[2];
-      const uint8_t* sp = (values ? r.p.vs : r.p.ks) + (int64_t)page * r.p.scale_stride[0] + (int64_t)head * r.p.scale_stride[1] +
-                          offset * r.p.scale_stride[2];
-      cw = *reinterpret_cast<const uint32_t*>(cp + 4 * at);
-      sb = sp[FMT == 0 ? at >> 2 : at >> 1];
-    }
-  }
   const bool rotate = r.rotate && !values;
+  const uint8_t* cbase = values ? r.p.vc : r.p.kc;
+  const uint8_t* sbase = values ? r.p.vs : r.p.ks;
+  const int64_t holds = (int64_t)r.table_cols * r.p.page.d;
+  const uint32_t s0 = blockIdx.x * (kReadSlots * kThreads) + threadIdx.x;
+  uint32_t head[kReadSlots], at[kReadSlots], offset[kReadSlots], cw[kReadSlots], sb[kReadSlots];
+  int32_t page[kReadSlots];
+  int b = 0;
+#pragma unroll
+  for (int u = 0; u < kReadSlots; ++u) {
+    const uint32_t s = min(s0 + u * kThreads, nslots - 1);
+    const uint32_t row = quotient(s, row_slots), token = quotient(row, heads);
+    at[u] = s - row * row_slots.d;
+    head[u] = row - token * heads.d;
+    const int64_t t = first + token;
+    if (u == 0) b = sequence_of(r.cu, r.seqs, t);
+    while (b + 1 < r.seqs && t >= r.cu[b + 1]) ++b;
+    const int64_t pos = t - r.cu[b] + (r.starts ? r.starts[b] : 0);
+    page[u] = -1;
+    if (t < r.cu[b + 1] && pos >= 0 && pos < holds && pos <= 0x7FFFFFFF) {
+      const uint32_t col = quotient((uint32_t)pos, r.p.page);
+      offset[u] = (uint32_t)pos - col * r.p.page.d;
+      page[u] = r.table[b * r.table_stride + col];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kReadSlots; ++u) {
+    cw[u] = 0u;
+    sb[u] = FMT == 0 ? 127u : 0u;
+    if ((uint32_t)page[u] < (uint32_t)r.p.num_pages) {
+      const uint64_t c = (uint64_t)page[u] * r.p.code_stride[0] + (uint64_t)head[u] * r.p.code_stride[1] +
+                         (uint64_t)offset[u] * r.p.code_stride[2];
+      const uint64_t e = (uint64_t)page[u] * r.p.scale_stride[0] + (uint64_t)head[u] * r.p.scale_stride[1] +
+                         (uint64_t)offset[u] * r.p.scale_stride[2];
+      cw[u] = *reinterpret_cast<const uint32_t*>(cbase + c + 4 * at[u]);
+      sb[u] = sbase[e + (FMT == 0 ? at[u] >> 2 : at[u] >> 1)];
+    }
+  }
   const float g = FMT == 0 ? 1.0f : *(values ? r.p.vg : r.p.kg);
-  float v[8], sd = 1.0f;
-  const float sc = FMT == 0 ? e8m0_operand(sb) : e8m0_operand(127u);
-  float2_t p;
-  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 0); v[0] = p.x; v[1] = p.y;
-  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 1); v[2] = p.x; v[3] = p.y;
-  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 2); v[4] = p.x; v[5] = p.y;
-  p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw, sc, 3); v[6] = p.x; v[7] = p.y;
-  bool nan = FMT == 0 ? sb == 255u : (sb & 0x7Fu) == 0x7Fu;
-  if constexpr (FMT != 0) {
-    sd = e4m3_value(sb & 0x7Fu);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= sd;   // exact: 2 and 4 significant bits
-  }
-  if (nan) {
+  for (int u = 0; u < kReadSlots; ++u) {
+    float v[8];
+    const float sc = e8m0_operand(FMT == 0 ? sb[u] : 127u);
+    float2_t p;
+    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 0); v[0] = p.x; v[1] = p.y;
+    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 1); v[2] = p.x; v[3] = p.y;
+    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 2); v[4] = p.x; v[5] = p.y;
+    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 3); v[6] = p.x; v[7] = p.y;
+    const bool nan = FMT == 0 ? sb[u] == 255u : (sb[u] & 0x7Fu) == 0x7Fu;
+    const float nanf = as_f(0x7FC00000u);
+    if constexpr (FMT != 0) {
+      const float sd = e4m3_value(sb[u] & 0x7Fu);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = as_f(0x7FC00000u);
-  }
-  if (rotate) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= g;
-    fwht128_lanes(v, threadIdx.x & 15, rot_scale);
-  }
-  if (!in_range) return;
-  const int64_t o = ((t * heads.d + head) * row_slots.d + at) * 8;
-  void* out = values ? r.v_out : r.k_out;
-  if constexpr (OUT == kF32) {
-    if (!rotate) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= g;
+      for (int i = 0; i < 8; ++i) v[i] *= sd;   // exact: 2 and 4 significant bits
     }
-    u32x4_t* dst = reinterpret_cast<u32x4_t*>(static_cast<float*>(out) + o);
-    __builtin_nontemporal_store(u32x4_t{as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])}, dst);
-    __builtin_nontemporal_store(u32x4_t{as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])}, dst + 1);
-  } else {
-    uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = rotate ? v[2 * i] : v[2 * i] * g, c = rotate ? v[2 * i + 1] : v[2 * i + 1] * g;
-      const bf16x2_t pk = {(__bf16)a, (__bf16)c};
-      h[i] = __builtin_bit_cast(uint32_t, pk);
-      // v s g is rounded once: where its fp32 product sits on a bf16 midpoint
-      // the exact product decides (the rotated values are sums, rounded twice)
-      if (FMT != 0 && !rotate) {
-        if ((as_u(a) & 0xFFFFu) == 0x8000u) h[i] = (h[i] & 0xFFFF0000u) | bf16_of_product(v[2 * i], g);
-        if ((as_u(c) & 0xFFFFu) == 0x8000u) h[i] = (h[i] & 0xFFFFu) | (bf16_of_product(v[2 * i + 1], g) << 16);
+    for (int i = 0; i < 8; ++i) v[i] = nan ? nanf : v[i];
+    if (rotate) {
+      if constexpr (FMT != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= g;
       }
+      fwht128_lanes(v, threadIdx.x & 15, rot_scale);
     }
-    __builtin_nontemporal_store(u32x4_t{h[0], h[1], h[2], h[3]},
-                                reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + o));
+    const uint32_t s = s0 + u * kThreads;
+    if (s >= nslots) return;
+    const int64_t o = (first * heads.d * row_slots.d + s) * 8;
+    void* out = values ? r.v_out : r.k_out;
+    if constexpr (OUT == kF32) {
+      if (FMT != 0 && !rotate) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= g;
+      }
+      u32x4_t* dst = reinterpret_cast<u32x4_t*>(static_cast<float*>(out) + o);
+      __builtin_nontemporal_store(u32x4_t{as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])}, dst);
+      __builtin_nontemporal_store(u32x4_t{as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])}, dst + 1);
+    } else {
+      uint32_t h[4], tie = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool scale = FMT != 0 && !rotate;
+        const float a = scale ? v[2 * i] * g : v[2 * i], c = scale ? v[2 * i + 1] * g : v[2 * i + 1];
+        const bf16x2_t pk = {(__bf16)a, (__bf16)c};
+        h[i] = __builtin_bit_cast(uint32_t, pk);
+        if (scale) {
+          tie |= (as_u(a) & 0xFFFFu) == 0x8000u ? 1u : 0u;
+          tie |= (as_u(c) & 0xFFFFu) == 0x8000u ? 1u : 0u;
+        }
+      }
+      // v s g is rounded once: where an fp32 product sits on a bf16 midpoint
+      // the exact products decide (the rotated values are sums, rounded twice)
+      if (FMT != 0 && tie != 0u && !nan) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = bf16_of_product(v[2 * i], g) | (bf16_of_product(v[2 * i + 1], g) << 16);
+      }
+      __builtin_nontemporal_store(u32x4_t{h[0], h[1], h[2], h[3]},
+                                  reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + o));
+    }
   }
 }
 
 template <int FMT>
 hipError_t launch_read_t(const KvReadLaunch& r, int64_t first, int64_t count, hipStream_t st) {
   const uint32_t per = (uint32_t)r.head_dim / 8, nslots = (uint32_t)(count * r.p.heads * per);
-  const dim3 grid((nslots + kThreads - 1) / kThreads, r.k_out && r.v_out ? 2 : 1);
+  const dim3 grid((nslots + kReadSlots * kThreads - 1) / (kReadSlots * kThreads), r.k_out && r.v_out ? 2 : 1);
   const float c = (float)(1.0 / sqrt(128.0));
   if (r.out_dtype == kF32)
     hipLaunchKernelGGL((kv_read_kernel<FMT, kF32>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),

@@ -33,7 +33,7 @@ struct DecodeShape {
   static constexpr int kMax1 = kVBytes > kOBytes ? kVBytes : kOBytes;
   static constexpr int kMain = kQRegs && kQBytes > kMax1 ? kQBytes : kMax1;
   static constexpr int kShared = kMain + (kQRegs ? 0 : kQBytes);
-  static constexpr int kWavesPerSimd = D > 128 ? 1 : (kTiles == 2 ? 2 : 3);
+  static constexpr int kWavesPerSimd = D > 128 ? 1 : (kTiles == 2 || kQ > 1 ? 2 : 3);
 };
 
 template <int FMT, int D, int kTiles, int kQ, int kP>
@@ -102,13 +102,16 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
     const int32_t* table = a.table + u.b * a.table_stride;
     const KvHead planes = kv_head(a.p, u.head);
     const int first = u.lo + 32 * wave, n = u.hi;
-    // Codes of 2 x 16 tokens a lane, those of the next group in flight, and
-    // the page numbers of the group after that.  No branches: tokens past the
-    // end are looked for at the last one's place, pages that are none at page
-    // 0, and then zeroed.
-    Lane kl[2], vl[2];
+    // Codes of 2 x 16 tokens a lane, those of the next two groups in flight,
+    // and the page numbers of the group after them.  No branches: tokens past
+    // the end are looked for at the last one's place, pages that are none at
+    // page 0, and then zeroed.
+    struct Tile {
+      Lane k[2], v[2];
+      bool there[2];
+    };
+    Tile even, odd;
     int32_t pages[2];
-    bool there[2];
     auto find = [&](int grp) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -116,47 +119,48 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
         pages[x] = table[quotient((uint32_t)t, a.p.page)];
       }
     };
-    auto fetch = [&](int grp) {
+    auto fetch = [&](int grp, Tile& in) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int t = first + grp * kGroupTokens + 16 * x + r;
         const uint32_t tt = (uint32_t)min(t, n - 1);
         const bool page = (uint32_t)pages[x] < (uint32_t)a.p.num_pages;
         const KvAt at = kv_at(a.p, page ? (uint32_t)pages[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
-        kl[x].load(planes.kc + at.code, planes.ks + at.scale, g);
-        vl[x].load(planes.vc + at.code, planes.vs + at.scale, g);
-        there[x] = page && t < n;
+        in.k[x].load(planes.kc + at.code, planes.ks + at.scale, g);
+        in.v[x].load(planes.vc + at.code, planes.vs + at.scale, g);
+        in.there[x] = page && t < n;
       }
     };
     bool bad = false;       // a value that is no finite number was left out
     if (n > 0) {
       find(group);
-      fetch(group);
+      fetch(group, even);
       find(group + 1);
+      fetch(group + 1, odd);
+      find(group + 2);
     }
-    for (int grp = group; grp < last; ++grp) {
+    auto step = [&](int grp, Tile& in) {
       const int t0 = first + grp * kGroupTokens;
-      if (t0 >= n) break;
       const bool edge = t0 + 32 > all_to || t0 < all_from;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        kl[x].keep_if(there[x]);
-        vl[x].keep_if(there[x]);
+        in.k[x].keep_if(in.there[x]);
+        in.v[x].keep_if(in.there[x]);
       }
       if (edge) {
-        const bool left_out = vl[0].drop_not_finite() | vl[1].drop_not_finite();
+        const bool left_out = in.v[0].drop_not_finite() | in.v[1].drop_not_finite();
         bad |= __any(left_out) != 0;
       }
       // scores of 32 tokens x 16 rows, transposed: token 16 x + 4 g + i, row r
       f32x4_t s[kTiles][2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const typename Lane::Scales sc = kl[x].prepare();
+        const typename Lane::Scales sc = in.k[x].prepare();
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) s[t][x] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          const u32x4_t kf = kl[x].values(c, sc);
+          const u32x4_t kf = in.k[x].values(c, sc);
 #pragma unroll
           for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -174,13 +178,13 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       // values into the wave's LDS rows
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const typename Lane::Scales sc = vl[x].prepare();
+        const typename Lane::Scales sc = in.v[x].prepare();
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          *reinterpret_cast<u32x4_t*>(sv + (16 * x + r) * Shape::kVStride + Lane::element(c, g)) = vl[x].values(c, sc);
+          *reinterpret_cast<u32x4_t*>(sv + (16 * x + r) * Shape::kVStride + Lane::element(c, g)) = in.v[x].values(c, sc);
       }
-      fetch(grp + 1);
-      find(grp + 2);
+      fetch(grp + 2, in);
+      find(grp + 3);
 
       // (scalars and selects throughout: hipcc 7.2 moves the wrong elements of
       // a vector when one is replaced under a lane's condition)
@@ -242,6 +246,12 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 #pragma unroll
           for (int q = 0; q < kP; ++q) o[t][c] = T::mfma16(vf, w[t][q], o[t][c]);
       }
+    };
+    // (this wave's groups: those that begin before the end)
+    const int mine = min(last, first < n ? (n - first + kGroupTokens - 1) / kGroupTokens : 0);
+    for (int grp = group; grp < mine; grp += 2) {
+      step(grp, even);
+      if (grp + 1 < mine) step(grp + 1, odd);
     }
 
     // join the four waves: maxima and sums of every row, then the values
@@ -323,17 +333,16 @@ hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The choice of pieces (see fp4q_kv_attend.h): fp32, bf16 rotated, bf16.
-template <int FMT, int D, int kTiles>
-hipError_t launch_decode_pieces(const KvAttendLaunch& a, int cus, hipStream_t st) {
-  if (a.dtype == kF32) return launch_decode_t<FMT, D, kTiles, FMT == 1 ? 2 : 3, 2>(a, cus, st);
-  if (a.rotate) return launch_decode_t<FMT, D, kTiles, 2, 1>(a, cus, st);
-  return launch_decode_t<FMT, D, kTiles, 1, 1>(a, cus, st);
-}
-
+// The choice of pieces (see fp4q_kv_attend.h): fp32, bf16 rotated, bf16.  More
+// than 16 rows only where they fit the registers: bf16, head_dim to 128.
 template <int D, int FMT>
 hipError_t launch_decode_d(const KvAttendLaunch& a, int tiles, int cus, hipStream_t st) {
-  return tiles == 1 ? launch_decode_pieces<FMT, D, 1>(a, cus, st) : launch_decode_pieces<FMT, D, 2>(a, cus, st);
+  if (a.dtype == kF32) return launch_decode_t<FMT, D, 1, FMT == 1 ? 2 : 3, 2>(a, cus, st);
+  const bool two = kv_rotated_pieces<FMT>(a) == 2;
+  if constexpr (D <= 128) {
+    if (tiles == 2) return two ? launch_decode_t<FMT, D, 2, 2, 1>(a, cus, st) : launch_decode_t<FMT, D, 2, 1, 1>(a, cus, st);
+  }
+  return two ? launch_decode_t<FMT, D, 1, 2, 1>(a, cus, st) : launch_decode_t<FMT, D, 1, 1, 1>(a, cus, st);
 }
 
 }  // namespace fp4q
