@@ -186,8 +186,8 @@ def kv_cache_read(cache, page_table, cu, *, total, starts=None, rotation=None, o
     return out
 
 
-# One workspace per (device, stream), grown as calls need it: calls on one
-# stream are ordered, and a call leaves nothing in it.
+# One zeroed workspace per (device, stream), grown as calls need it: calls on
+# one stream are ordered, and a call leaves its counters zero.
 _workspaces = {}
 
 
@@ -197,7 +197,7 @@ def _workspace(device, stream, need):
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("fp4q: the workspace of this stream is missing or too small; pass workspace= or make "
                                "one call of this size on the stream before capturing it")
-        ws = _workspaces[(device, stream)] = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _workspaces[(device, stream)] = torch.zeros(need, dtype=torch.uint8, device=device)
     return ws
 
 

@@ -139,8 +139,8 @@ Plan attend_plan(const KvAttendLaunch& a) {
 size_t kv_attend_workspace(const KvAttendLaunch& a) {
   const Plan p = attend_plan(a);
   const int64_t cus = device_cu_count();
-  if (p.prefill) return kv_partial_bytes(cus * 8 / p.waves, 32 * p.waves, a.head_dim);
-  return kv_partial_bytes(cus * 3, 16 * p.tiles, a.head_dim);
+  if (p.prefill) return kv_workspace_bytes(cus * 8 / p.waves, 32 * p.waves, a.head_dim);
+  return kv_workspace_bytes(cus * 3, 16 * p.tiles, a.head_dim);
 }
 
 hipError_t launch_kv_attend(const KvAttendLaunch& a, hipStream_t s) {

@@ -337,11 +337,12 @@ __device__ __forceinline__ bool kv_numbered(const KvAttendLaunch& a, int64_t num
   return true;
 }
 
-// A workgroup's stretch: `left` counted groups from the `at`-th of unit `u` on.
+// A workgroup's stretch: `left` counted groups from the `at`-th of unit `u` on,
+// whose own first one has the number `begins`; `share` groups a workgroup.
 struct KvStretch {
   KvUnit u;
   int at;
-  int64_t left;
+  int64_t left, begins, share;
 };
 // The groups [from, to) that a stretch has of its current unit: none where it
 // ends within the unit's kCost.
@@ -403,6 +404,8 @@ __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numb
   st.u.head = __builtin_amdgcn_readfirstlane((int)(in_block / (st.u.groups + kCost)));
   st.at = __builtin_amdgcn_readfirstlane((int)(in_block - (int64_t)st.u.head * (st.u.groups + kCost)));
   st.left = total - begin < share ? total - begin : share;
+  st.begins = begin - st.at;
+  st.share = share;
   return true;
 }
 
@@ -412,6 +415,7 @@ __device__ __forceinline__ bool kv_next(const KvAttendLaunch& a, KvStretch& st) 
   KvUnit& u = st.u;
   st.left -= u.groups + kCost - st.at;
   if (st.left <= 0) return false;
+  st.begins += u.groups + kCost;
   st.at = 0;
   if (++u.head < a.p.heads) return true;
   u.head = 0;
@@ -430,24 +434,49 @@ inline int64_t kv_block_numbers(const KvAttendLaunch& a) {
   return a.total_q * a.group / kRows + a.seqs;
 }
 
-// What a workgroup leaves in the workspace: a header saying which units it
-// shares with its neighbours, and for either end of its stretch the partial
-// result of that unit: kRows x D weighted values, kRows maxima, kRows sums.
-//   first: 0 none, 1 a piece of a unit that began before, 2 its last piece
-//   last:  1 the first piece of a unit that goes on in the next workgroup
+// The workspace: a record a workgroup, then for either end of each workgroup's
+// stretch the partial result of the unit it shares with its neighbours: kRows x
+// D weighted values, then each row's maximum and sum.  Units that several
+// workgroups share are joined
+//   - few rows: by whichever of them finishes last, found by counting arrivals
+//     in the record of the workgroup where the unit begins; it clears the
+//     counter again, so that all are zero between calls.  Saves a launch.
+//   - many rows: by a second kernel with many more workgroups, since one would
+//     take too long over them (a call of 16 units of 64 rows x 256 in 16 pieces
+//     each took 93 us that way, 45 with a second kernel).  The records then
+//     also say which units are shared.
+constexpr int kMostWorkgroups = 1024;      // of a launch
 struct KvShared {
-  int32_t first, last, b, head, row0, pad0, pad1, pad2;
+  uint32_t arrived;
+  int32_t first;     // 1: the stretch begins with a piece of an earlier unit, 2: with its last one
+  int32_t last;      // 1: it ends with the first piece of a unit, sequence b, rows row0 on of `head`
+  int32_t b, head, row0;
+  int32_t unused[10];     // (64 bytes: each record in a cache line of its own)
 };
-__device__ __forceinline__ KvShared* kv_shared(const KvAttendLaunch& a) {
-  return reinterpret_cast<KvShared*>(a.ws);
+__device__ __forceinline__ KvShared* kv_shared(const KvAttendLaunch& a, int64_t workgroup) {
+  return reinterpret_cast<KvShared*>(a.ws) + workgroup;
 }
 template <int D, int kRows>
-__device__ __forceinline__ float* kv_partial(const KvAttendLaunch& a, int64_t workgroups, int64_t workgroup, bool last) {
-  return reinterpret_cast<float*>(a.ws + workgroups * sizeof(KvShared)) +
+__device__ __forceinline__ float* kv_partial(const KvAttendLaunch& a, int64_t workgroup, bool last) {
+  return reinterpret_cast<float*>(a.ws + kMostWorkgroups * sizeof(KvShared)) +
          (2 * workgroup + (last ? 1 : 0)) * (int64_t)kRows * (D + 2);
 }
-inline size_t kv_partial_bytes(int64_t workgroups, int64_t rows, int64_t head_dim) {
-  return (size_t)workgroups * (sizeof(KvShared) + 2 * rows * (head_dim + 2) * sizeof(float));
+inline size_t kv_workspace_bytes(int64_t workgroups, int64_t rows, int64_t head_dim) {
+  return kMostWorkgroups * sizeof(KvShared) + (size_t)(workgroups * 2 * rows * (head_dim + 2)) * sizeof(float);
+}
+
+// Partial results are written and read by relaxed atomics of agent scope, which
+// go past the caches that the chip's parts do not share; a workgroup counts its
+// arrival after its own have completed (vmcnt 0 of every wave, then a barrier).
+// Agent fences, which write back and invalidate whole L2 caches, made a call
+// over a batch of 64 four times longer.
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  const uint64_t w = (uint64_t)as_u(a) | ((uint64_t)as_u(b) << 32);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2_t get2(const float* p) {
+  const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return float2_t{as_f((uint32_t)w), as_f((uint32_t)(w >> 32))};
 }
 
 // Query head and row of q of row rr of a sequence; false: past its queries.
@@ -458,58 +487,6 @@ __device__ __forceinline__ bool kv_out_row(const KvAttendLaunch& a, int q0, int 
   const int i = (int)quotient((uint32_t)rr, a.group_div);
   o.at = ((int64_t)q0 + i) * ((int64_t)a.p.heads * a.group) + (int64_t)head * a.group + (rr - i * a.group);
   return i < m;
-}
-
-// Joins the pieces of the unit that begins in workgroup blockIdx.x's last
-// piece: each wave takes one of its rows.
-template <int FMT, int D, int kRows>
-__global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttendLaunch a, int workgroups) {
-  const int lane = threadIdx.x & 63, row = blockIdx.y * kWaves + (threadIdx.x >> 6);
-  const int w0 = blockIdx.x;
-  const KvShared h = kv_shared(a)[w0];
-  if (!h.last) return;
-  int pieces = 0;          // of the workgroups after w0, up to the one that ends the unit
-  for (int w = w0 + 1; w < workgroups; w += 64) {
-    const bool ends = w + lane < workgroups && kv_shared(a)[w + lane].first == 2;
-    const unsigned long long found = __ballot(ends);
-    if (found) {
-      pieces += __ffsll((long long)found);
-      break;
-    }
-    pieces += 64;
-  }
-  KvOutRow o;
-  const int q0 = kv_first_query(a, h.b), m = kv_first_query(a, h.b + 1) - q0;
-  if (row >= kRows || !kv_out_row(a, q0, m, h.head, h.row0 + row, o)) return;
-  float top = kNoMax;
-  for (int i = lane; i <= pieces; i += 64)
-    top = fmaxf(top, kv_partial<D, kRows>(a, workgroups, w0 + i, i == 0)[(int64_t)kRows * D + row]);
-#pragma unroll
-  for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
-  constexpr int kEach = (D + 63) / 64;
-  float sum[kEach], all = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) sum[k] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i <= pieces; ++i) {
-    const float* part = kv_partial<D, kRows>(a, workgroups, w0 + i, i == 0);
-    const float f = __builtin_amdgcn_exp2f(part[(int64_t)kRows * D + row] - top);
-    all += f * part[(int64_t)kRows * (D + 1) + row];
-#pragma unroll
-    for (int k = 0; k < kEach; ++k)
-      if (lane + 64 * k < D) sum[k] += f * part[(int64_t)row * D + lane + 64 * k];
-  }
-  const float inv = all == 0.0f ? 0.0f : (FMT == 1 ? *a.p.vg : 1.0f) / all;
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int d = lane + 64 * k;
-    if (d >= D) continue;
-    const float x = all == 0.0f ? 0.0f : sum[k] * inv;
-    if (a.dtype == kF32) static_cast<float*>(a.out)[o.at * D + d] = x;
-    else static_cast<uint16_t*>(a.out)[o.at * D + d] = (uint16_t)KvType<0>::pack(x, x);
-  }
-  if (a.lse && lane == 0)
-    a.lse[o.at] = all == 0.0f ? -INFINITY : (top - KvType<FMT>::kUp + __builtin_amdgcn_logf(all)) * kLn2;
 }
 
 // Pieces of bf16 queries.
@@ -670,6 +647,112 @@ __device__ __forceinline__ void kv_finish4(const KvAttendLaunch& a, const KvUnit
   store_out4(a, out.at * D + d, total == 0.0f ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : sum * inv);
   if (a.lse && d == 0)
     a.lse[out.at] = total == 0.0f ? -INFINITY : (top - KvType<FMT>::kUp + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+// After a workgroup has stored its piece of a shared unit: counts it, and where
+// it is the last one joins the pieces into the output.  kBatch pieces' loads
+// are in flight together.  Every thread of the workgroup calls it; `word`: LDS.
+template <int FMT, int D, int kRows, int kCost, int kThreadsWg, int kBatch>
+__device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u, int64_t begins, int64_t share,
+                                        unsigned int* word) {
+  // its first real group and its last one say which workgroups have pieces
+  const int64_t w0 = (begins + kCost) / share, w1 = (begins + kCost + u.groups - 1) / share;
+  const int pieces = (int)(w1 - w0) + 1;
+  __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t* counter = &kv_shared(a, w0)->arrived;
+    const unsigned int arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+    if (arrived == (unsigned int)pieces) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *word = arrived;
+  }
+  __syncthreads();
+  if (*word != (unsigned int)pieces) return;
+  const int rows = (int)min((int64_t)kRows, (int64_t)u.m * a.group - u.row0);
+  for (int item = threadIdx.x; item < rows * (D / 4); item += kThreadsWg) {
+    const int rr = item / (D / 4), d = 4 * (item % (D / 4));
+    f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    float top = kNoMax, total = 0.0f;
+    for (int p = 0; p < pieces; p += kBatch) {
+      f32x4_t v[kBatch];
+      float m[kBatch], l[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int q = min(p + i, pieces - 1);
+        const float* part = kv_partial<D, kRows>(a, w0 + q, q == 0);
+        const float2_t x = get2(part + (int64_t)rr * D + d), y = get2(part + (int64_t)rr * D + d + 2);
+        const float2_t ml = get2(part + (int64_t)kRows * D + 2 * rr);
+        v[i] = f32x4_t{x.x, x.y, y.x, y.y};
+        m[i] = p + i < pieces ? ml.x : kNoMax;
+        l[i] = ml.y;
+      }
+      float most = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) most = fmaxf(most, m[i]);
+      const float f = __builtin_amdgcn_exp2f(top - most);
+      top = most;
+      sum *= f;
+      total *= f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float e = p + i < pieces ? __builtin_amdgcn_exp2f(m[i] - top) : 0.0f;
+        sum += v[i] * e;
+        total += l[i] * e;
+      }
+    }
+    kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, top, total);
+  }
+}
+
+// The second kernel of the many-row form: a thread takes 4 elements of a row
+// of the unit that begins in workgroup blockIdx.x's last piece.
+template <int FMT, int D, int kRows>
+__global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttendLaunch a, int workgroups) {
+  constexpr int kBatch = 8;
+  const int lane = threadIdx.x & 63, w0 = blockIdx.x;
+  const KvShared* h = kv_shared(a, w0);
+  if (!h->last) return;
+  int pieces = 1;          // up to the workgroup whose first piece ends the unit
+  for (int w = w0 + 1; w < workgroups; w += 64) {
+    const unsigned long long found = __ballot(w + lane < workgroups && kv_shared(a, min(w + lane, workgroups - 1))->first == 2);
+    pieces += found ? __ffsll((long long)found) : 64;
+    if (found) break;
+  }
+  KvUnit u;
+  u.b = h->b;
+  u.head = h->head;
+  u.row0 = h->row0;
+  u.q0 = kv_first_query(a, u.b);
+  u.m = kv_first_query(a, u.b + 1) - u.q0;
+  const int item = blockIdx.y * kThreads + threadIdx.x, rr = item / (D / 4), d = 4 * (item % (D / 4));
+  if (rr >= min((int64_t)kRows, (int64_t)u.m * a.group - u.row0)) return;
+  f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  float top = kNoMax, total = 0.0f;
+  for (int p = 0; p < pieces; p += kBatch) {
+    f32x4_t v[kBatch];
+    float2_t ml[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int q = min(p + i, pieces - 1);
+      const float* part = kv_partial<D, kRows>(a, w0 + q, q == 0);
+      v[i] = *reinterpret_cast<const f32x4_t*>(part + (int64_t)rr * D + d);
+      ml[i] = *reinterpret_cast<const float2_t*>(part + (int64_t)kRows * D + 2 * rr);
+    }
+    float most = top;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) most = fmaxf(most, ml[i].x);
+    const float f = __builtin_amdgcn_exp2f(top - most);
+    top = most;
+    sum *= f;
+    total *= f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float e = p + i < pieces ? __builtin_amdgcn_exp2f(ml[i].x - top) : 0.0f;
+      sum += v[i] * e;
+      total += ml[i].y * e;
+    }
+  }
+  kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, top, total);
 }
 
 }  // namespace fp4q

@@ -3,8 +3,8 @@
 // One read of the cache is what such a call costs; its groups of 128 tokens
 // are shared out evenly (the schedule of fp4q_kv_attend.h), lengths being read
 // on the device, so that a captured launch follows them.  A unit inside one
-// stretch is finished there; the others leave partial results that a second
-// kernel joins.
+// stretch is finished there; the others leave partial results that the last of
+// their workgroups joins.
 //
 // In a workgroup each of the 4 waves works on 32 tokens of a group by itself:
 // keys from memory into the left operand of 16x16x32 products (16 tokens x 16
@@ -57,16 +57,70 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   uint16_t* sq = reinterpret_cast<uint16_t*>(s_main + (Shape::kQRegs ? 0 : Shape::kMain));
 
   KvStretch st;
-  if (!kv_stretch<kRows, kGroupTokens, kGroupCost, kThreads>(a, numbers, st, s_scan)) {
-    if (tid == 0) kv_shared(a)[blockIdx.x] = KvShared{0, 0, 0, 0, 0, 0, 0, 0};
-    return;
-  }
-  int shared_first = 0, shared_last = 0, shared_b = 0, shared_head = 0, shared_row0 = 0;
+  if (!kv_stretch<kRows, kGroupTokens, kGroupCost, kThreads>(a, numbers, st, s_scan)) return;
   const KvUnit& u = st.u;
-  do {
-    int group, last;      // the unit's groups [group, last) are this workgroup's
-    kv_part<kGroupCost>(st, group, last);
-    if (group == last) continue;
+
+  // Codes of 2 x 16 tokens a lane, those of two groups in flight, and the page
+  // numbers of the group after them.  No branches: tokens past the end are
+  // looked for at the last one's place, pages that are none at page 0, and then
+  // zeroed.
+  struct Tile {
+    Lane k[2], v[2];
+    bool there[2];
+  };
+  struct Pages {
+    int32_t x[2];
+  };
+  Tile even, odd;
+  Pages pages = {{0, 0}};
+  const int32_t* table = nullptr;
+  KvHead planes = {};
+  int group = 0, last = 0;      // the unit's groups [group, last) are this workgroup's
+  int first = 0, n = 0;         // this wave's first token of group 0, the tokens' end
+  auto find = [&](int grp) {
+    Pages p;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int t = min(first + grp * kGroupTokens + 16 * x + r, n - 1);
+      p.x[x] = table[quotient((uint32_t)t, a.p.page)];
+    }
+    return p;
+  };
+  auto fetch = [&](int grp, const Pages& pages, Tile& in) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int t = first + grp * kGroupTokens + 16 * x + r;
+      const uint32_t tt = (uint32_t)min(t, n - 1);
+      const bool page = (uint32_t)pages.x[x] < (uint32_t)a.p.num_pages;
+      const KvAt at = kv_at(a.p, page ? (uint32_t)pages.x[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
+      in.k[x].load(planes.kc + at.code, planes.ks + at.scale, g);
+      in.v[x].load(planes.vc + at.code, planes.vs + at.scale, g);
+      in.there[x] = page && t < n;
+    }
+  };
+  // Takes up the stretch's next unit with groups of its own, its first loads
+  // on their way; false: there is none.
+  auto take = [&](bool more) {
+    for (; more; more = kv_next<kRows, kGroupTokens, kGroupCost>(a, st)) {
+      kv_part<kGroupCost>(st, group, last);
+      if (group == last) continue;
+      table = a.table + u.b * a.table_stride;
+      planes = kv_head(a.p, u.head);
+      first = u.lo + 32 * wave;
+      n = u.hi;
+      if (n > 0) {
+        const Pages p0 = find(group), p1 = find(group + 1);
+        pages = find(group + 2);
+        fetch(group, p0, even);
+        fetch(group + 1, p1, odd);
+      }
+      return true;
+    }
+    return false;
+  };
+
+  bool more = take(true);
+  while (more) {
     stage_queries<FMT, D, kQ, kRows>(a, u, sq, s_factor, s_most);
 
     u32x4_t qf[Shape::kQRegs ? kTiles : 1][Shape::kQRegs ? kQ : 1][Shape::kQRegs ? kChunks : 1];
@@ -99,46 +153,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       for (int c = 0; c < D / 16; ++c) o[t][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    const int32_t* table = a.table + u.b * a.table_stride;
-    const KvHead planes = kv_head(a.p, u.head);
-    const int first = u.lo + 32 * wave, n = u.hi;
-    // Codes of 2 x 16 tokens a lane, those of the next two groups in flight,
-    // and the page numbers of the group after them.  No branches: tokens past
-    // the end are looked for at the last one's place, pages that are none at
-    // page 0, and then zeroed.
-    struct Tile {
-      Lane k[2], v[2];
-      bool there[2];
-    };
-    Tile even, odd;
-    int32_t pages[2];
-    auto find = [&](int grp) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int t = min(first + grp * kGroupTokens + 16 * x + r, n - 1);
-        pages[x] = table[quotient((uint32_t)t, a.p.page)];
-      }
-    };
-    auto fetch = [&](int grp, Tile& in) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int t = first + grp * kGroupTokens + 16 * x + r;
-        const uint32_t tt = (uint32_t)min(t, n - 1);
-        const bool page = (uint32_t)pages[x] < (uint32_t)a.p.num_pages;
-        const KvAt at = kv_at(a.p, page ? (uint32_t)pages[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
-        in.k[x].load(planes.kc + at.code, planes.ks + at.scale, g);
-        in.v[x].load(planes.vc + at.code, planes.vs + at.scale, g);
-        in.there[x] = page && t < n;
-      }
-    };
     bool bad = false;       // a value that is no finite number was left out
-    if (n > 0) {
-      find(group);
-      fetch(group, even);
-      find(group + 1);
-      fetch(group + 1, odd);
-      find(group + 2);
-    }
     auto step = [&](int grp, Tile& in) {
       const int t0 = first + grp * kGroupTokens;
       const bool edge = t0 + 32 > all_to || t0 < all_from;
@@ -183,8 +198,11 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
         for (int c = 0; c < kChunks; ++c)
           *reinterpret_cast<u32x4_t*>(sv + (16 * x + r) * Shape::kVStride + Lane::element(c, g)) = in.v[x].values(c, sc);
       }
-      fetch(grp + 2, in);
-      find(grp + 3);
+      // (loads come back in order: page numbers asked for before the codes can
+      // be waited for without waiting for those)
+      const Pages next = find(grp + 3);
+      fetch(grp + 2, pages, in);
+      pages = next;
 
       // (scalars and selects throughout: hipcc 7.2 moves the wrong elements of
       // a vector when one is replaced under a lane's condition)
@@ -254,6 +272,14 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       if (grp + 1 < mine) step(grp + 1, odd);
     }
 
+    // the next unit's loads set out before this one is finished
+    const KvUnit done = u;
+    const int64_t begins = st.begins;
+    const bool whole = group == 0 && last == u.groups;
+    const int t_begin = u.lo + group * kGroupTokens, t_end = min(u.hi, u.lo + last * kGroupTokens);
+    float* part = kv_partial<D, kRows>(a, blockIdx.x, group == 0);
+    more = take(kv_next<kRows, kGroupTokens, kGroupCost>(a, st));
+
     // join the four waves: maxima and sums of every row, then the values
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -265,18 +291,6 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       }
     }
     if (lane == 0) s_bad[wave] = bad;
-    const bool whole = group == 0 && last == u.groups;
-    float* part = kv_partial<D, kRows>(a, gridDim.x, blockIdx.x, group == 0);
-    if (!whole) {
-      if (group == 0) {
-        shared_last = 1;
-        shared_b = u.b;
-        shared_head = u.head;
-        shared_row0 = u.row0;
-      } else {
-        shared_first = last == u.groups ? 2 : 1;
-      }
-    }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       __syncthreads();
@@ -293,28 +307,25 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4_t*>(so + (w * 16 + row) * Shape::kOStride + d);
         if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) {
-          const int t1 = min(u.hi, u.lo + last * kGroupTokens);
-          if (kv_sees_nan<FMT, D>(a, u, u.row0 + rr, d, u.lo + group * kGroupTokens, t1)) sum *= as_f(0x7FC00000u);
+          if (kv_sees_nan<FMT, D>(a, done, done.row0 + rr, d, t_begin, t_end)) sum *= as_f(0x7FC00000u);
         }
         const float mx = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
         float total = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) total += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mx);
         if (whole) {
-          kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, mx, total);
-        } else {
-          *reinterpret_cast<f32x4_t*>(part + (int64_t)rr * D + d) = sum;
-          if (d == 0) {
-            part[(int64_t)kRows * D + rr] = mx;
-            part[(int64_t)kRows * (D + 1) + rr] = total;
-          }
+          kv_finish4<FMT, D>(a, done, done.row0 + rr, d, sum, mx, total);
+        } else if (done.row0 + rr < done.m * a.group) {
+          put2(part + (int64_t)rr * D + d, sum.x, sum.y);
+          put2(part + (int64_t)rr * D + d + 2, sum.z, sum.w);
+          if (d == 0) put2(part + (int64_t)kRows * D + 2 * rr, mx, total);
         }
       }
     }
     __syncthreads();
-  } while (kv_next<kRows, kGroupTokens, kGroupCost>(a, st));
-  if (tid == 0)
-    kv_shared(a)[blockIdx.x] = KvShared{shared_first, shared_last, shared_b, shared_head, shared_row0, 0, 0, 0};
+    if (!whole) kv_join<FMT, D, kRows, kGroupCost, kThreads, 8>(a, done, begins, st.share, s_most);
+    __syncthreads();
+  }
 }
 
 template <int FMT, int D, int kTiles, int kQ, int kP>
@@ -324,12 +335,8 @@ hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   const int64_t groups = (a.most_tokens + kGroupTokens - 1) / kGroupTokens;
   const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kGroupCost);
   const int64_t resident = (int64_t)cus * DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd;
-  const int grid = (int)(most < resident ? most : resident);
+  const int grid = (int)min(min(most, resident), (int64_t)kMostWorkgroups);
   hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP>), dim3(grid), dim3(kThreads), 0, st, a, numbers);
-  hipError_t e = hipGetLastError();
-  // (a stretch is at least a group, and a unit of one group is never shared)
-  if (e != hipSuccess || groups <= 1) return e;
-  hipLaunchKernelGGL((kv_join_kernel<FMT, D, kRows>), dim3(grid, kRows / kWaves), dim3(kThreads), 0, st, a, grid);
   return hipGetLastError();
 }
 

@@ -114,11 +114,9 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
   const int r = lane & 15, g = lane >> 4, col = lane & 31, half = lane >> 5;
 
   KvStretch st;
-  if (!kv_stretch<kRows, kStepTokens, kStepCost, 64 * kW>(a, numbers, st, s_scan)) {
-    if (tid == 0) kv_shared(a)[blockIdx.x] = KvShared{0, 0, 0, 0, 0, 0, 0, 0};
-    return;
-  }
-  int shared_first = 0, shared_last = 0, shared_b = 0, shared_head = 0, shared_row0 = 0;
+  KvShared* shared = kv_shared(a, blockIdx.x);
+  if (tid == 0) shared->first = shared->last = 0;
+  if (!kv_stretch<kRows, kStepTokens, kStepCost, 64 * kW>(a, numbers, st, s_scan)) return;
   const KvUnit& u = st.u;
   do {
     int group, last;      // the unit's groups [group, last) are this workgroup's
@@ -309,30 +307,29 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
           kv_finish4<FMT, D>(a, u, u.row0 + rr, 32 * c + 2 * i + 4 * half,
                              f32x4_t{o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]}, m, l);
     } else {
-      if (group == 0) {
-        shared_last = 1;
-        shared_b = u.b;
-        shared_head = u.head;
-        shared_row0 = u.row0;
-      } else {
-        shared_first = last == u.groups ? 2 : 1;
+      float* part = kv_partial<D, kRows>(a, blockIdx.x, group == 0);
+      if (tid == 0) {
+        if (group == 0) {
+          shared->b = u.b;
+          shared->head = u.head;
+          shared->row0 = u.row0;
+          shared->last = 1;
+        } else {
+          shared->first = last == u.groups ? 2 : 1;
+        }
       }
-      float* part = kv_partial<D, kRows>(a, gridDim.x, blockIdx.x, group == 0);
+      if (u.row0 + rr < u.m * a.group) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
+        for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<f32x4_t*>(part + (int64_t)rr * D + 32 * c + 2 * i + 4 * half) =
-              f32x4_t{o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]};
-      if (half == 0) {
-        part[(int64_t)kRows * D + rr] = m;
-        part[(int64_t)kRows * (D + 1) + rr] = l;
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4_t*>(part + (int64_t)rr * D + 32 * c + 2 * i + 4 * half) =
+                f32x4_t{o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]};
+        if (half == 0) *reinterpret_cast<float2_t*>(part + (int64_t)kRows * D + 2 * rr) = float2_t{m, l};
       }
     }
     __syncthreads();      // (everyone has read s_bad)
   } while (kv_next<kRows, kStepTokens, kStepCost>(a, st));
-  if (tid == 0)
-    kv_shared(a)[blockIdx.x] = KvShared{shared_first, shared_last, shared_b, shared_head, shared_row0, 0, 0, 0};
 }
 
 template <int FMT, int D, int kW, int kQ, int kP>
@@ -343,11 +340,14 @@ hipError_t launch_prefill_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   const int64_t groups = (a.most_tokens + kStepTokens - 1) / kStepTokens;
   const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kStepCost);
   const int64_t resident = (int64_t)cus * (4 * Shape::kWavesPerSimd / kW);
-  const int grid = (int)(most < resident ? most : resident);
+  const int grid = (int)min(min(most, resident), (int64_t)kMostWorkgroups);
   hipLaunchKernelGGL((kv_prefill_kernel<FMT, D, kW, kQ, kP>), dim3(grid), dim3(64 * kW), 0, st, a, numbers);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  // (a unit of one step is never shared)
   if (e != hipSuccess || groups <= 1) return e;
-  hipLaunchKernelGGL((kv_join_kernel<FMT, D, kRows>), dim3(grid, kRows / kWaves), dim3(kThreads), 0, st, a, grid);
+  const int64_t rows = min((int64_t)kRows, (int64_t)a.max_q * a.group);
+  hipLaunchKernelGGL((kv_join_kernel<FMT, D, kRows>), dim3(grid, (uint32_t)((rows * (D / 4) + kThreads - 1) / kThreads)),
+                     dim3(kThreads), 0, st, a, grid);
   return hipGetLastError();
 }
 

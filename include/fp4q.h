@@ -355,8 +355,10 @@ typedef struct {
 } fp4q_kv_attention_args;
 
 /* Bytes of device workspace an attention call uses (0 for arguments it would
- * refuse), 16-byte aligned; it needs no clearing and keeps nothing between
- * calls.  It depends on the shapes and max_q alone, not on the lengths. */
+ * refuse), 16-byte aligned.  It has to be zero-filled before its first use
+ * (counters of finished parts lie in it, which every call leaves zero again)
+ * and may then serve any calls that are ordered on the GPU.  It depends on the
+ * shapes and max_q alone, not on the lengths. */
 size_t fp4q_kv_attention_workspace_bytes(const fp4q_kv_cache *cache, const fp4q_kv_attention_args *args);
 
 /* Attention of new queries over the cache: out = softmax(scale q k^T) v over
