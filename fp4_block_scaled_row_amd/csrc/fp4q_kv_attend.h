@@ -52,6 +52,8 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -0x1p126f;       // a maximum before any score
+// The larger one, NaN if either is: one instruction for two of them.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 constexpr float kRaise = 8.0f;            // slack of the running maximum
 
 // The element type of a format's matrix products: fp16 for NVFP4 (FMT 1),
@@ -128,9 +130,11 @@ struct KvLane {
   uint32_t codes[kChunks];
   uint32_t scales;                         // kScales bytes (at most 4)
 
-  __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* srow, int g) {
+  // From byte `c` of a code row and byte `e` of a scale row on (offsets apart,
+  // so that the rows may be scalars).
+  __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* srow, uint32_t c0, uint32_t e0, int g) {
     if constexpr (kRun) {
-      const uint8_t* p = row + g * (D / 8);
+      const uint8_t* p = row + (c0 + g * (D / 8));
       if constexpr (kChunks == 2) {
         const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
         codes[0] = w.x;
@@ -145,7 +149,7 @@ struct KvLane {
           codes[c + 3] = w.w;
         }
       }
-      const uint8_t* q = srow + (g * (D / 4)) / kBlock;
+      const uint8_t* q = srow + (e0 + (g * (D / 4)) / kBlock);
       if constexpr (kScales == 1) scales = *q;
       else if constexpr (kScales == 2) scales = *reinterpret_cast<const uint16_t*>(q);
       else scales = *reinterpret_cast<const uint32_t*>(q);
@@ -153,8 +157,8 @@ struct KvLane {
       scales = 0u;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        codes[c] = *reinterpret_cast<const uint32_t*>(row + 16 * c + 4 * g);
-        scales |= (uint32_t)srow[FMT == 0 ? c : 2 * c + (g >> 1)] << (8 * c);
+        codes[c] = *reinterpret_cast<const uint32_t*>(row + (c0 + 16 * c + 4 * g));
+        scales |= (uint32_t)srow[e0 + (FMT == 0 ? c : 2 * c + (g >> 1))] << (8 * c);
       }
     }
   }
@@ -212,7 +216,7 @@ struct KvLane {
       o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[c], sc, 1));
       o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[c], sc, 2));
       o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[c], sc, 3));
-      if (not_finite(b)) o = u32x4_t{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+      // (scale byte 255 gives NaN, values past bf16's range infinity)
     } else {
       const f16x2_t pair = __builtin_bit_cast(f16x2_t, s.h[i / 2]);
       const _Float16 one = pair[i % 2];
@@ -312,7 +316,7 @@ __device__ __forceinline__ void kv_block_at(const KvAttendLaunch& a, int row0, K
   const int64_t hi = a.causal ? past + i1 + 1 : u.n;
   const int64_t lo = a.window > 0 ? past + i0 + 1 - a.window : 0;
   u.hi = (int)(hi < 0 ? 0 : hi);
-  u.lo = (int)(lo < 0 ? 0 : (lo > u.hi ? u.hi : lo));
+  u.lo = (int)(lo < 0 ? 0 : (lo > u.hi ? u.hi : lo)) & ~31;     // (whole tiles of 32: a page's, where pages allow)
   u.groups = max(1, (u.hi - u.lo + kTokens - 1) / kTokens);
 }
 template <int kRows, int kTokens>
@@ -352,19 +356,23 @@ __device__ __forceinline__ void kv_part(const KvStretch& st, int& from, int& to)
   to = max(0, (int)min((int64_t)st.u.groups + kCost, st.at + st.left) - kCost);
 }
 
+// x / d of a non-negative x: in 32 bits where that holds it.
+__device__ __forceinline__ int64_t quotient64(int64_t x, int64_t d) {
+  return ((x | d) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+}
+
 // Every thread of the workgroup calls it, with all query block numbers below
-// `numbers`; scratch: 8 + 2 waves words of LDS.  False: nothing to do.
+// `numbers`; scratch: 8 + waves words of LDS.  False: nothing to do.
 template <int kRows, int kTokens, int kCost, int kThreadsWg>
 __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numbers, KvStretch& st, long long* scratch) {
   constexpr int kW = kThreadsWg / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t each = (numbers + kThreadsWg - 1) / kThreadsWg;
+  const int64_t each = quotient64(numbers + kThreadsWg - 1, kThreadsWg);
   const int64_t x0 = tid * each, x1 = x0 + each < numbers ? x0 + each : numbers;
   long long mine = 0;
-  for (int64_t x = x0; x < x1; ++x) {
-    KvUnit u;
+  KvUnit u = {};
+  for (int64_t x = x0; x < x1; ++x)
     if (kv_numbered<kRows, kTokens>(a, x, u)) mine += (long long)(u.groups + kCost) * a.p.heads;
-  }
   long long upto = mine;     // inclusive scan over the workgroup
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -379,30 +387,38 @@ __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numb
     if (w < wave) upto += scratch[w];
     total += scratch[w];
   }
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long share = quotient64(total + gridDim.x - 1, gridDim.x);
   const long long begin = share * blockIdx.x;
   if (begin >= total) return false;
   long long before = upto - mine;
+  int* found = reinterpret_cast<int*>(scratch + kW);
   if (begin >= before && begin < upto) {
-    KvUnit u;
-    for (int64_t x = x0; x < x1; ++x) {
-      if (!kv_numbered<kRows, kTokens>(a, x, u)) continue;
-      const long long here = (long long)(u.groups + kCost) * a.p.heads;
-      if (begin < before + here) break;
-      before += here;
+    if (each > 1) {
+      for (int64_t x = x0; x < x1; ++x) {
+        if (!kv_numbered<kRows, kTokens>(a, x, u)) continue;
+        const long long here = (long long)(u.groups + kCost) * a.p.heads;
+        if (begin < before + here) break;
+        before += here;
+      }
     }
-    scratch[kW] = u.b;
-    scratch[kW + 1] = u.block;
-    scratch[kW + 2] = begin - before;
+    found[0] = u.b;
+    found[1] = u.block;
+    found[2] = u.q0;
+    found[3] = u.m;
+    found[4] = u.n;
+    scratch[kW + 3] = begin - before;
   }
   __syncthreads();
-  const int b = __builtin_amdgcn_readfirstlane((int)scratch[kW]);
-  const int block = __builtin_amdgcn_readfirstlane((int)scratch[kW + 1]);
-  const int64_t in_block = scratch[kW + 2];
-  kv_sequence<kRows, kTokens>(a, b, st.u);
-  kv_block<kRows, kTokens>(a, block, st.u);
-  st.u.head = __builtin_amdgcn_readfirstlane((int)(in_block / (st.u.groups + kCost)));
-  st.at = __builtin_amdgcn_readfirstlane((int)(in_block - (int64_t)st.u.head * (st.u.groups + kCost)));
+  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  st.u.b = uniform(found[0]);
+  st.u.q0 = uniform(found[2]);
+  st.u.m = uniform(found[3]);
+  st.u.n = uniform(found[4]);
+  st.u.blocks = (int)(((int64_t)st.u.m * a.group + kRows - 1) / kRows);
+  kv_block<kRows, kTokens>(a, uniform(found[1]), st.u);
+  const int64_t in_block = scratch[kW + 3];
+  st.u.head = uniform((int)quotient64(in_block, st.u.groups + kCost));
+  st.at = uniform((int)(in_block - (int64_t)st.u.head * (st.u.groups + kCost)));
   st.left = total - begin < share ? total - begin : share;
   st.begins = begin - st.at;
   st.share = share;
@@ -498,82 +514,100 @@ inline int kv_rotated_pieces(const KvAttendLaunch& a) {
 template <int FMT, int kQ>
 constexpr bool kv_scaled_rows() { return FMT == 1; }
 
-// 8 elements of q, widened and rotated; rows past the last are zero.
-__device__ __forceinline__ void load_q8(const KvAttendLaunch& a, const KvUnit& u, int row, int at, float v[8]) {
+// 8 elements of q as they are; rows past the last are zero.
+struct RawQ {
+  u32x4_t w[2];      // (bf16: the first alone)
+};
+__device__ __forceinline__ RawQ load_q8(const KvAttendLaunch& a, const KvUnit& u, int row, int at) {
   const uint32_t i = quotient((uint32_t)row, a.group_div);
+  RawQ q = {{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}}};
   if ((int)i < u.m) {
     const int64_t off = (u.q0 + (int64_t)i) * a.q_stride[0] +
                         ((int64_t)u.head * a.group + (row - (int)i * a.group)) * a.q_stride[1] + 8 * at;
     if (a.dtype == kF32) {
-      SlotRaw<kF32> r;
       const float* p = static_cast<const float*>(a.q) + off;
-      const u32x4_t x = load16<false>(p), y = load16<false>(p + 4);
-      r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
-      r.w[4] = y.x; r.w[5] = y.y; r.w[6] = y.z; r.w[7] = y.w;
-      widen_slot<kF32>(r, v);
+      q.w[0] = load16<false>(p);
+      q.w[1] = load16<false>(p + 4);
     } else {
-      SlotRaw<kBF16> r;
-      const u32x4_t x = load16<false>(static_cast<const uint16_t*>(a.q) + off);
-      r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
-      widen_slot<kBF16>(r, v);
+      q.w[0] = load16<false>(static_cast<const uint16_t*>(a.q) + off);
     }
+  }
+  return q;
+}
+__device__ __forceinline__ void widen_q8(const KvAttendLaunch& a, const RawQ& q, float v[8]) {
+  if (a.dtype == kF32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = as_f(q.w[k >> 2][k & 3]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf_lo(q.w[0][k]);
+      v[2 * k + 1] = bf_hi(q.w[0][k]);
+    }
   }
 }
 
-// Stages ROWS query rows as kQ pieces in LDS, rows of D + 8 halves, pieces
-// ROWS rows apart, and each row's factor from raw score to exponent of two in
-// factor[].  Every thread of the workgroup calls it; it ends synchronised.
-// most[]: ROWS words of scratch.
+// A workgroup's ROWS query rows on their way into LDS: its threads' parts of
+// them as they were loaded, and then as kQ pieces in rows of D + 8 halves,
+// pieces ROWS rows apart, with each row's factor from raw score to exponent of
+// two in factor[].  The factors are not negative: a negative scale goes into
+// the queries' signs.
+template <int D, int ROWS>
+struct QueryRows {
+  static constexpr int kPer = D / 8, kItems = ROWS * kPer;
+  static constexpr int kEach = (kItems + kThreads - 1) / kThreads;
+  RawQ raw[kEach];
+};
+template <int D, int ROWS>
+__device__ __forceinline__ void load_queries(const KvAttendLaunch& a, const KvUnit& u, QueryRows<D, ROWS>& q) {
+  using Q = QueryRows<D, ROWS>;
+#pragma unroll
+  for (int k = 0; k < Q::kEach; ++k) {
+    const int item = threadIdx.x + k * kThreads;      // (whole waves: kItems is a multiple of 64)
+    if (item < Q::kItems) q.raw[k] = load_q8(a, u, u.row0 + item / Q::kPer, item % Q::kPer);
+  }
+}
+// Every thread of the workgroup calls it; it ends synchronised.  most[]: ROWS
+// words of scratch.
 template <int FMT, int D, int kQ, int ROWS>
-__device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, const KvUnit& u, uint16_t* sq, float* factor,
-                                              uint32_t* most) {
-  constexpr int kPer = D / 8, kItems = ROWS * kPer;
-  constexpr int kEach = (kItems + kThreads - 1) / kThreads;
+__device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, const QueryRows<D, ROWS>& in, uint16_t* sq,
+                                              float* factor, uint32_t* most) {
+  using Q = QueryRows<D, ROWS>;
   const int tid = threadIdx.x;
-  float v[kEach][8];
+  const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+  float v[Q::kEach][8];
   if constexpr (kv_scaled_rows<FMT, kQ>()) {
     for (int i = tid; i < ROWS; i += kThreads) most[i] = 0u;
     __syncthreads();
   }
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
+  for (int k = 0; k < Q::kEach; ++k) {
     const int item = tid + k * kThreads;
-    if (item < kItems) {      // (whole waves: kItems is a multiple of 64)
-      const int row = item / kPer, at = item % kPer;
-      load_q8(a, u, u.row0 + row, at, v[k]);
+    if (item < Q::kItems) {
+      widen_q8(a, in.raw[k], v[k]);
       if constexpr (D % 128 == 0) {
         if (a.rotate) fwht128_lanes(v[k], tid & 15, a.rot_scale);
       }
-      if constexpr (kv_scaled_rows<FMT, kQ>()) atomicMax(most + row, abs_max_bits8(v[k]));
+      if constexpr (kv_scaled_rows<FMT, kQ>()) atomicMax(most + item / Q::kPer, abs_max_bits8(v[k]));
     }
   }
   __syncthreads();
-  const float base = a.scale * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f);
+  const float base = fabsf(a.scale) * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f);
   for (int i = tid; i < ROWS; i += kThreads) {
     float f = base;
-    if constexpr (kv_scaled_rows<FMT, kQ>()) {
-      const uint32_t e = min(max(most[i] >> 23, 9u), 254u);
-      f = base * as_f((e - 8u) << 23);
-    }
+    if constexpr (kv_scaled_rows<FMT, kQ>()) f *= as_f((min(max(most[i] >> 23, 9u), 254u) - 8u) << 23);
     factor[i] = f;
   }
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
+  for (int k = 0; k < Q::kEach; ++k) {
     const int item = tid + k * kThreads;
-    if (item < kItems) {
-      const int row = item / kPer, at = item % kPer;
-      if constexpr (kv_scaled_rows<FMT, kQ>()) {
-        const uint32_t e = min(max(most[row] >> 23, 9u), 254u);
-        const float f = as_f((262u - e) << 23);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] *= f;
-      }
+    if (item < Q::kItems) {
+      const int row = item / Q::kPer, at = item % Q::kPer;
+      float f = sign;
+      if constexpr (kv_scaled_rows<FMT, kQ>()) f *= as_f((262u - min(max(most[row] >> 23, 9u), 254u)) << 23);
       uint32_t w[4][kQ];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) pieces<FMT, kQ>(v[k][2 * j], v[k][2 * j + 1], w[j]);
+      for (int j = 0; j < 4; ++j) pieces<FMT, kQ>(v[k][2 * j] * f, v[k][2 * j + 1] * f, w[j]);
 #pragma unroll
       for (int q = 0; q < kQ; ++q)
         *reinterpret_cast<u32x4_t*>(sq + ((size_t)q * ROWS + row) * (D + 8) + 8 * at) =
@@ -656,7 +690,7 @@ template <int FMT, int D, int kRows, int kCost, int kThreadsWg, int kBatch>
 __device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u, int64_t begins, int64_t share,
                                         unsigned int* word) {
   // its first real group and its last one say which workgroups have pieces
-  const int64_t w0 = (begins + kCost) / share, w1 = (begins + kCost + u.groups - 1) / share;
+  const int64_t w0 = quotient64(begins + kCost, share), w1 = quotient64(begins + kCost + u.groups - 1, share);
   const int pieces = (int)(w1 - w0) + 1;
   __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0
   __syncthreads();

@@ -36,7 +36,7 @@ struct DecodeShape {
   static constexpr int kWavesPerSimd = D > 128 ? 1 : (kTiles == 2 || kQ > 1 ? 2 : 3);
 };
 
-template <int FMT, int D, int kTiles, int kQ, int kP>
+template <int FMT, int D, int kTiles, int kQ, int kP, bool kWhole>
 __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd)) void kv_decode_kernel(
     KvAttendLaunch a, int64_t numbers) {
   using Shape = DecodeShape<FMT, D, kTiles, kQ, kP>;
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   __shared__ uint32_t s_most[kRows];
   __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
   __shared__ int s_bad[kWaves];
-  __shared__ long long s_scan[kWaves + 3];
+  __shared__ long long s_scan[kWaves + 4];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -61,9 +61,13 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   const KvUnit& u = st.u;
 
   // Codes of 2 x 16 tokens a lane, those of two groups in flight, and the page
-  // numbers of the group after them.  No branches: tokens past the end are
-  // looked for at the last one's place, pages that are none at page 0, and then
-  // zeroed.
+  // numbers of the group after them.
+  //   kWhole: pages are multiples of 32 tokens, so that a wave's 32 tokens lie
+  // in one page: its number and their place are scalars, the lanes' offsets
+  // constants.  Tokens past the end are in the page too and are read.
+  //   Other pages: every lane finds its token's page.  No branches: tokens past
+  // the end are looked for at the last one's place.
+  //   Pages that are none are read at page 0 and then zeroed.
   struct Tile {
     Lane k[2], v[2];
     bool there[2];
@@ -73,29 +77,50 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   };
   Tile even, odd;
   Pages pages = {{0, 0}};
+  QueryRows<D, kRows> rows;
   const int32_t* table = nullptr;
   KvHead planes = {};
   int group = 0, last = 0;      // the unit's groups [group, last) are this workgroup's
   int first = 0, n = 0;         // this wave's first token of group 0, the tokens' end
+  const uint32_t c_lane = r * a.p.code_stride[2], s_lane = r * a.p.scale_stride[2];
   auto find = [&](int grp) {
-    Pages p;
+    Pages p = {{0, 0}};
+    if constexpr (kWhole) {
+      const int t = min(first + grp * kGroupTokens, n - 1);
+      p.x[0] = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(
+          reinterpret_cast<uintptr_t>(table))[quotient((uint32_t)t, a.p.page)];
+    } else {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = min(first + grp * kGroupTokens + 16 * x + r, n - 1);
-      p.x[x] = table[quotient((uint32_t)t, a.p.page)];
+      for (int x = 0; x < 2; ++x) {
+        const int t = min(first + grp * kGroupTokens + 16 * x + r, n - 1);
+        p.x[x] = table[quotient((uint32_t)t, a.p.page)];
+      }
     }
     return p;
   };
   auto fetch = [&](int grp, const Pages& pages, Tile& in) {
+    if constexpr (kWhole) {
+      const uint32_t t = (uint32_t)min(first + grp * kGroupTokens, n - 1) & ~31u;
+      const bool page = (uint32_t)pages.x[0] < (uint32_t)a.p.num_pages;
+      const KvAt at = kv_at(a.p, page ? (uint32_t)pages.x[0] : 0u, t - quotient(t, a.p.page) * a.p.page.d);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = first + grp * kGroupTokens + 16 * x + r;
-      const uint32_t tt = (uint32_t)min(t, n - 1);
-      const bool page = (uint32_t)pages.x[x] < (uint32_t)a.p.num_pages;
-      const KvAt at = kv_at(a.p, page ? (uint32_t)pages.x[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
-      in.k[x].load(planes.kc + at.code, planes.ks + at.scale, g);
-      in.v[x].load(planes.vc + at.code, planes.vs + at.scale, g);
-      in.there[x] = page && t < n;
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t c = c_lane + 16 * x * a.p.code_stride[2], e = s_lane + 16 * x * a.p.scale_stride[2];
+        in.k[x].load(planes.kc + at.code, planes.ks + at.scale, c, e, g);
+        in.v[x].load(planes.vc + at.code, planes.vs + at.scale, c, e, g);
+        in.there[x] = page;
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = first + grp * kGroupTokens + 16 * x + r;
+        const uint32_t tt = (uint32_t)min(t, n - 1);
+        const bool page = (uint32_t)pages.x[x] < (uint32_t)a.p.num_pages;
+        const KvAt at = kv_at(a.p, page ? (uint32_t)pages.x[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
+        in.k[x].load(planes.kc + at.code, planes.ks + at.scale, 0, 0, g);
+        in.v[x].load(planes.vc + at.code, planes.vs + at.scale, 0, 0, g);
+        in.there[x] = page;
+      }
     }
   };
   // Takes up the stretch's next unit with groups of its own, its first loads
@@ -108,6 +133,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       planes = kv_head(a.p, u.head);
       first = u.lo + 32 * wave;
       n = u.hi;
+      load_queries(a, u, rows);
       if (n > 0) {
         const Pages p0 = find(group), p1 = find(group + 1);
         pages = find(group + 2);
@@ -121,7 +147,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 
   bool more = take(true);
   while (more) {
-    stage_queries<FMT, D, kQ, kRows>(a, u, sq, s_factor, s_most);
+    stage_queries<FMT, D, kQ, kRows>(a, rows, sq, s_factor, s_most);
 
     u32x4_t qf[Shape::kQRegs ? kTiles : 1][Shape::kQRegs ? kQ : 1][Shape::kQRegs ? kChunks : 1];
     float factor[kTiles];
@@ -157,14 +183,19 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
     auto step = [&](int grp, Tile& in) {
       const int t0 = first + grp * kGroupTokens;
       const bool edge = t0 + 32 > all_to || t0 < all_from;
+      if (kWhole ? !in.there[0] : true) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        in.k[x].keep_if(in.there[x]);
-        in.v[x].keep_if(in.there[x]);
+        for (int x = 0; x < 2; ++x) {
+          in.k[x].keep_if(in.there[x]);
+          in.v[x].keep_if(in.there[x]);
+        }
       }
       if (edge) {
-        const bool left_out = in.v[0].drop_not_finite() | in.v[1].drop_not_finite();
-        bad |= __any(left_out) != 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const bool left_out = in.v[x].drop_not_finite() && t0 + 16 * x + r < n;
+          bad |= __any(left_out) != 0;
+        }
       }
       // scores of 32 tokens x 16 rows, transposed: token 16 x + 4 g + i, row r
       f32x4_t s[kTiles][2];
@@ -212,7 +243,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[t][k] = s[t][k >> 2][k & 3] * factor[t];
+        for (int k = 0; k < 8; ++k) y[t][k] = s[t][k >> 2][k & 3];
         if (edge) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -220,17 +251,19 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
             y[t][k] = j < sees[t] ? y[t][k] : -INFINITY;
           }
         }
-        most[t] = fmaxf(fmaxf(fmaxf(y[t][0], y[t][1]), fmaxf(y[t][2], y[t][3])),
-                        fmaxf(fmaxf(y[t][4], y[t][5]), fmaxf(y[t][6], y[t][7])));
+        most[t] = y[t][0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) most[t] = larger(most[t], y[t][k]);
+        most[t] *= factor[t];
         raise |= most[t] > m[t] + kRaise;
       }
       // raise the maxima where a score exceeds them by more than the slack
       if (__any(raise)) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-          float x = fmaxf(most[t], __shfl_xor(most[t], 16, 64));
-          x = fmaxf(x, __shfl_xor(x, 32, 64));
-          x = fmaxf(x, m[t]);
+          float x = larger(most[t], __shfl_xor(most[t], 16, 64));
+          x = larger(x, __shfl_xor(x, 32, 64));
+          x = larger(x, m[t]);
           const float f = __builtin_amdgcn_exp2f(m[t] - x);
           m[t] = x;
           l[t] *= f;
@@ -241,15 +274,15 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       u32x4_t w[kTiles][kP];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        const float top = m[t] - T::kUp;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          y[t][k] = __builtin_amdgcn_exp2f(y[t][k] - top);
-          l[t] += y[t][k];
-        }
+        const float top = T::kUp - m[t];
         uint32_t h[4][kP];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pieces<FMT, kP>(y[t][2 * j], y[t][2 * j + 1], h[j]);
+        for (int j = 0; j < 4; ++j) {
+          const float p0 = __builtin_amdgcn_exp2f(fmaf(y[t][2 * j], factor[t], top));
+          const float p1 = __builtin_amdgcn_exp2f(fmaf(y[t][2 * j + 1], factor[t], top));
+          l[t] += p0 + p1;       // (before rounding: the log-sum-exp is held to fp32)
+          pieces<FMT, kP>(p0, p1, h[j]);
+        }
 #pragma unroll
         for (int q = 0; q < kP; ++q) w[t][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
       }
@@ -336,7 +369,10 @@ hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kGroupCost);
   const int64_t resident = (int64_t)cus * DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd;
   const int grid = (int)min(min(most, resident), (int64_t)kMostWorkgroups);
-  hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP>), dim3(grid), dim3(kThreads), 0, st, a, numbers);
+  if (a.p.page.d % 32 == 0)
+    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, true>), dim3(grid), dim3(kThreads), 0, st, a, numbers);
+  else
+    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, false>), dim3(grid), dim3(kThreads), 0, st, a, numbers);
   return hipGetLastError();
 }
 

@@ -37,7 +37,7 @@ __device__ __forceinline__ float wave_queries(const KvAttendLaunch& a, const KvU
                                               u32x4_t qf[kQ][D / 16]) {
   float v[D / 16][8];
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) load_q8(a, u, row, 2 * c + half, v[c]);
+  for (int c = 0; c < D / 16; ++c) widen_q8(a, load_q8(a, u, row, 2 * c + half), v[c]);
   if constexpr (D % 128 == 0) {
     if (a.rotate) {
       // elements 1, 2, 4 apart in a lane's 8, 8 apart between the lanes' two
@@ -77,14 +77,14 @@ __device__ __forceinline__ float wave_queries(const KvAttendLaunch& a, const KvU
         for (int i = 0; i < 8; ++i) v[c][i] *= a.rot_scale;
     }
   }
-  float factor = a.scale * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f), up = 1.0f;
+  float factor = fabsf(a.scale) * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f), up = a.scale < 0.0f ? -1.0f : 1.0f;
   if constexpr (kv_scaled_rows<FMT, kQ>()) {
     uint32_t most = 0u;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) most = max(most, abs_max_bits8(v[c]));
     most = max(most, (uint32_t)__shfl_xor((int)most, 32, 64));
     const uint32_t e = min(max(most >> 23, 9u), 254u);
-    up = as_f((262u - e) << 23);
+    up *= as_f((262u - e) << 23);
     factor *= as_f((e - 8u) << 23);
   }
 #pragma unroll
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
   constexpr int kRows = Shape::kRows;
   constexpr int kTasks = 8 / kW;       // 16 tokens' keys or values a task: 8 in a step
   __shared__ __align__(16) uint16_t s_kv[2 * Shape::kHalf];
-  __shared__ long long s_scan[kW + 3];
+  __shared__ long long s_scan[kW + 4];
   __shared__ int s_bad;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         const bool page = (uint32_t)pages[x] < (uint32_t)a.p.num_pages;
         const KvAt at = kv_at(a.p, page ? (uint32_t)pages[x] : 0u, tt - quotient(tt, a.p.page) * a.p.page.d);
         const bool values = (task0 + x) & 1;
-        in[x].load((values ? planes.vc : planes.kc) + at.code, (values ? planes.vs : planes.ks) + at.scale, g);
+        in[x].load((values ? planes.vc : planes.kc) + at.code, (values ? planes.vs : planes.ks) + at.scale, 0, 0, g);
         there[x] = page && t < n;
       }
     };
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         // token 32 x + 8 (i / 4) + 4 half + i % 4 of the step
         float y[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = s[i >> 4][i & 15] * factor;
+        for (int i = 0; i < 32; ++i) y[i] = s[i >> 4][i & 15];
         if (t0 + kStepTokens > all_to || t0 < all_from) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -232,24 +232,25 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         }
         float most = y[0];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) most = fmaxf(most, y[i]);
+        for (int i = 1; i < 32; ++i) most = larger(most, y[i]);
+        most *= factor;
         if (__any(most > m + kRaise)) {
-          const float x = fmaxf(fmaxf(most, __shfl_xor(most, 32, 64)), m);
+          const float x = larger(larger(most, __shfl_xor(most, 32, 64)), m);
           const float f = __builtin_amdgcn_exp2f(m - x);
           m = x;
           l *= f;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) o[c] *= f;
         }
-        const float top = m - T::kUp;
+        const float top = T::kUp - m;
         u32x4_t w[4][kP];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t h[4][kP];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float p0 = __builtin_amdgcn_exp2f(y[8 * k + 2 * j] - top);
-            const float p1 = __builtin_amdgcn_exp2f(y[8 * k + 2 * j + 1] - top);
+            const float p0 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j], factor, top));
+            const float p1 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j + 1], factor, top));
             l += p0 + p1;
             pieces<FMT, kP>(p0, p1, h[j]);
           }
