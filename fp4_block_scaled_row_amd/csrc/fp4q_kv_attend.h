@@ -272,11 +272,20 @@ __device__ __forceinline__ u32x2_t read_transposed(const uint16_t* p) {
 // length: whatever the lengths are, all have the same to do.  A unit counts
 // kCost groups more than it has, for what it takes to begin and end it (without
 // that the workgroup with the shortest units of a causal prompt, 25 of them
-// where others had 2, made the call 1.6 times longer).  Blocks are found
-// by numbers too: block k of sequence b has the number cu[b] group / kRows + b
-// + k (rounded down), which leaves room for each sequence's blocks and skips
-// at most one number a sequence, so that a thread finds a number's sequence by
-// bisection and no list has to be built.
+// where others had 2, made the call 1.6 times longer).
+//   Blocks go by numbers of which some are skipped, so that no list has to be
+// built.  Either block k of sequence b has the number b * per_seq + k, with
+// per_seq blocks the most of any sequence; or, where lengths of queries differ
+// so much that most of those would be skipped, cu[b] group / kRows + b + k
+// (rounded down), which skips at most one a sequence, and a thread finds a
+// number's sequence by bisection.
+// A value that the whole wave reads, through the scalar cache: its wait does
+// not take in the vector loads that are on their way.
+template <typename T>
+__device__ __forceinline__ T scalar(const T* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) T*>(reinterpret_cast<uintptr_t>(p));
+}
+
 struct KvUnit {
   int b, block, blocks;   // sequence, block of its query rows, its blocks
   int head;               // cache head
@@ -287,8 +296,9 @@ struct KvUnit {
 };
 
 // Row of q of sequence b's first query (never past the rows there are).
+template <bool kUniform = false>
 __device__ __forceinline__ int kv_first_query(const KvAttendLaunch& a, int b) {
-  const int q = a.cu_q ? a.cu_q[b] : b;
+  const int q = a.cu_q ? (kUniform ? scalar(a.cu_q + b) : a.cu_q[b]) : b;
   return q < 0 ? 0 : (q > (int)a.total_q ? (int)a.total_q : q);
 }
 
@@ -297,12 +307,12 @@ __device__ __forceinline__ int64_t kv_block_number(const KvAttendLaunch& a, int 
   return (int64_t)kv_first_query(a, b) * a.group / kRows + b;
 }
 
-template <int kRows, int kTokens>
+template <int kRows, int kTokens, bool kUniform = false>
 __device__ __forceinline__ void kv_sequence(const KvAttendLaunch& a, int b, KvUnit& u) {
   u.b = b;
-  u.q0 = kv_first_query(a, b);
-  u.m = kv_first_query(a, b + 1) - u.q0;
-  const int len = a.lens[b];
+  u.q0 = kv_first_query<kUniform>(a, b);
+  u.m = kv_first_query<kUniform>(a, b + 1) - u.q0;
+  const int len = kUniform ? scalar(a.lens + b) : a.lens[b];
   u.n = len < 0 ? 0 : (len > a.most_tokens ? (int)a.most_tokens : len);
   u.blocks = u.m > 0 ? (int)(((int64_t)u.m * a.group + kRows - 1) / kRows) : 0;
 }
@@ -328,25 +338,74 @@ __device__ __forceinline__ void kv_block(const KvAttendLaunch& a, int block, KvU
 // Block number -> sequence and block; false: a skipped number.
 template <int kRows, int kTokens>
 __device__ __forceinline__ bool kv_numbered(const KvAttendLaunch& a, int64_t number, KvUnit& u) {
-  int lo = 0, hi = a.seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (kv_block_number<kRows>(a, mid) <= number) lo = mid;
-    else hi = mid;
+  int64_t block;
+  if (a.per_seq.d) {
+    const int b = (int)quotient((uint32_t)number, a.per_seq);      // (all below 2^31)
+    kv_sequence<kRows, kTokens>(a, b, u);
+    block = number - (int64_t)b * a.per_seq.d;
+  } else {
+    int lo = 0, hi = a.seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (kv_block_number<kRows>(a, mid) <= number) lo = mid;
+      else hi = mid;
+    }
+    kv_sequence<kRows, kTokens>(a, lo, u);
+    block = number - kv_block_number<kRows>(a, lo);
   }
-  kv_sequence<kRows, kTokens>(a, lo, u);
-  const int64_t block = number - kv_block_number<kRows>(a, lo);
   if (block < 0 || block >= u.blocks) return false;
   kv_block<kRows, kTokens>(a, (int)block, u);
   return true;
 }
 
+// The workgroups' stretches.  A CU issues its oldest waves first, so that of
+// three workgroups on each CU the first ones were done in 66 us, the second in
+// 72 and the third in 78 where all had the same; where a launch fills the chip
+// with three a CU, they take shares of 36, 32 and 28 parts instead.
+constexpr int kPart0 = 36, kPart1 = 32, kPart2 = 28;
+struct KvShares {
+  int64_t size0, size1, size2;      // groups of a workgroup of the first, second and last `per`
+  int64_t from1, from2;             // where the second and the last begin
+  int per;
+};
+// x / d of a non-negative x: in 32 bits where that holds it.
+__device__ __forceinline__ int64_t quotient64(int64_t x, int64_t d) {
+  return ((x | d) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+}
+__device__ __forceinline__ KvShares kv_shares(int64_t total, int workgroups, bool thirds) {
+  KvShares s;
+  if (thirds) {
+    s.per = workgroups / 3;
+    const int64_t all = (int64_t)s.per * (kPart0 + kPart1 + kPart2);
+    s.size0 = quotient64(total * kPart0 + all - 1, all);
+    s.size1 = quotient64(total * kPart1 + all - 1, all);
+    s.size2 = quotient64(total * kPart2 + all - 1, all);
+    s.from1 = s.per * s.size0;
+    s.from2 = s.from1 + s.per * s.size1;
+  } else {
+    s.per = workgroups;
+    s.size0 = s.size1 = s.size2 = quotient64(total + workgroups - 1, workgroups);
+    s.from1 = s.from2 = s.per * s.size0;
+  }
+  return s;
+}
+__device__ __forceinline__ int64_t kv_begin(const KvShares& s, int w) {
+  return w < s.per ? w * s.size0 : (w < 2 * s.per ? s.from1 + (w - s.per) * s.size1 : s.from2 + (w - 2 * s.per) * s.size2);
+}
+// The workgroup that has group x.
+__device__ __forceinline__ int64_t kv_owner(const KvShares& s, int64_t x) {
+  return x < s.from1 ? quotient64(x, s.size0)
+                     : (x < s.from2 ? s.per + quotient64(x - s.from1, s.size1)
+                                    : 2 * s.per + quotient64(x - s.from2, s.size2));
+}
+
 // A workgroup's stretch: `left` counted groups from the `at`-th of unit `u` on,
-// whose own first one has the number `begins`; `share` groups a workgroup.
+// whose own first one has the number `begins`.
 struct KvStretch {
   KvUnit u;
   int at;
-  int64_t left, begins, share;
+  int64_t left, begins;
+  KvShares shares;
 };
 // The groups [from, to) that a stretch has of its current unit: none where it
 // ends within the unit's kCost.
@@ -356,72 +415,98 @@ __device__ __forceinline__ void kv_part(const KvStretch& st, int& from, int& to)
   to = max(0, (int)min((int64_t)st.u.groups + kCost, st.at + st.left) - kCost);
 }
 
-// x / d of a non-negative x: in 32 bits where that holds it.
-__device__ __forceinline__ int64_t quotient64(int64_t x, int64_t d) {
-  return ((x | d) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+// Inclusive sum over the lanes of a wave: within rows of 16 lanes, then rows 0
+// and 2 into 1 and 3, then the first two into the last two.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);     // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);     // row_shr:2
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);     // row_shr:4
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);     // row_shr:8
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);    // row_bcast:15
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);    // row_bcast:31
+  return v;
 }
 
 // Every thread of the workgroup calls it, with all query block numbers below
-// `numbers`; scratch: 8 + waves words of LDS.  False: nothing to do.
-template <int kRows, int kTokens, int kCost, int kThreadsWg>
+// `numbers`; scratch: 4 + waves words of LDS.  False: nothing to do.  To 256
+// numbers each wave goes through them all by itself, which spares the first
+// step of every call its barriers.
+template <int kRows, int kTokens, int kCost, int kThreadsWg, bool kThirds>
 __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numbers, KvStretch& st, long long* scratch) {
   constexpr int kW = kThreadsWg / 64;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t each = quotient64(numbers + kThreadsWg - 1, kThreadsWg);
-  const int64_t x0 = tid * each, x1 = x0 + each < numbers ? x0 + each : numbers;
+  const bool alone = numbers <= 256 && a.few_groups;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int id = alone ? lane : (int)threadIdx.x;
+  const int64_t each = alone ? ((int)numbers + 63) >> 6 : quotient64(numbers + kThreadsWg - 1, kThreadsWg);
+  const int64_t x0 = id * each, x1 = x0 + each < numbers ? x0 + each : numbers;
   long long mine = 0;
   KvUnit u = {};
   for (int64_t x = x0; x < x1; ++x)
     if (kv_numbered<kRows, kTokens>(a, x, u)) mine += (long long)(u.groups + kCost) * a.p.heads;
-  long long upto = mine;     // inclusive scan over the workgroup
+  long long upto = mine, total = 0;     // inclusive scan
+  if (a.few_groups) {
+    upto = (long long)wave_scan((uint32_t)mine);
+  } else {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const long long x = __shfl_up(upto, o, 64);
-    if (lane >= o) upto += x;
-  }
-  if (lane == 63) scratch[wave] = upto;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    if (w < wave) upto += scratch[w];
-    total += scratch[w];
-  }
-  const long long share = quotient64(total + gridDim.x - 1, gridDim.x);
-  const long long begin = share * blockIdx.x;
-  if (begin >= total) return false;
-  long long before = upto - mine;
-  int* found = reinterpret_cast<int*>(scratch + kW);
-  if (begin >= before && begin < upto) {
-    if (each > 1) {
-      for (int64_t x = x0; x < x1; ++x) {
-        if (!kv_numbered<kRows, kTokens>(a, x, u)) continue;
-        const long long here = (long long)(u.groups + kCost) * a.p.heads;
-        if (begin < before + here) break;
-        before += here;
-      }
+    for (int o = 1; o < 64; o <<= 1) {
+      const long long x = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += x;
     }
-    found[0] = u.b;
-    found[1] = u.block;
-    found[2] = u.q0;
-    found[3] = u.m;
-    found[4] = u.n;
-    scratch[kW + 3] = begin - before;
   }
-  __syncthreads();
-  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
-  st.u.b = uniform(found[0]);
-  st.u.q0 = uniform(found[2]);
-  st.u.m = uniform(found[3]);
-  st.u.n = uniform(found[4]);
+  if (alone) {
+    total = __builtin_amdgcn_readlane((int)upto, 63);
+  } else {
+    if (lane == 63) scratch[wave] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (w < wave) upto += scratch[w];
+      total += scratch[w];
+    }
+  }
+  st.shares = kv_shares(total, gridDim.x, kThirds && gridDim.x == a.thirds);
+  const long long begin = kv_begin(st.shares, blockIdx.x);
+  const long long end = min((long long)kv_begin(st.shares, blockIdx.x + 1), total);
+  if (begin >= end) return false;
+  long long before = upto - mine;
+  const bool owner = begin >= before && begin < upto;
+  if (owner && each > 1) {
+    for (int64_t x = x0; x < x1; ++x) {
+      if (!kv_numbered<kRows, kTokens>(a, x, u)) continue;
+      const long long here = (long long)(u.groups + kCost) * a.p.heads;
+      if (begin < before + here) break;
+      before += here;
+    }
+  }
+  int found[5] = {u.b, u.block, u.q0, u.m, u.n};
+  long long in_block = begin - before;
+  if (alone) {
+    const int from = __ffsll((long long)__ballot(owner)) - 1;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) found[i] = __builtin_amdgcn_readlane(found[i], from);
+    in_block = __builtin_amdgcn_readlane((int)in_block, from);
+  } else {
+    int* out = reinterpret_cast<int*>(scratch + kW);
+    if (owner) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) out[i] = found[i];
+      scratch[kW + 3] = in_block;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 5; ++i) found[i] = __builtin_amdgcn_readfirstlane(out[i]);
+    in_block = scratch[kW + 3];
+  }
+  st.u.b = found[0];
+  st.u.q0 = found[2];
+  st.u.m = found[3];
+  st.u.n = found[4];
   st.u.blocks = (int)(((int64_t)st.u.m * a.group + kRows - 1) / kRows);
-  kv_block<kRows, kTokens>(a, uniform(found[1]), st.u);
-  const int64_t in_block = scratch[kW + 3];
-  st.u.head = uniform((int)quotient64(in_block, st.u.groups + kCost));
-  st.at = uniform((int)(in_block - (int64_t)st.u.head * (st.u.groups + kCost)));
-  st.left = total - begin < share ? total - begin : share;
+  kv_block<kRows, kTokens>(a, found[1], st.u);
+  st.u.head = __builtin_amdgcn_readfirstlane((int)quotient64(in_block, st.u.groups + kCost));
+  st.at = __builtin_amdgcn_readfirstlane((int)(in_block - (int64_t)st.u.head * (st.u.groups + kCost)));
+  st.left = end - begin;
   st.begins = begin - st.at;
-  st.share = share;
   return true;
 }
 
@@ -437,17 +522,22 @@ __device__ __forceinline__ bool kv_next(const KvAttendLaunch& a, KvStretch& st) 
   u.head = 0;
   int block = u.block + 1;
   while (block >= u.blocks && u.b + 1 < a.seqs) {
-    kv_sequence<kRows, kTokens>(a, u.b + 1, u);
+    kv_sequence<kRows, kTokens, true>(a, u.b + 1, u);
     block = 0;
   }
   kv_block<kRows, kTokens>(a, block, u);
   return true;
 }
 
-// Numbers of all query blocks lie below this.
+// Numbers of all query blocks lie below this; sets the kind of numbering.
 template <int kRows>
-inline int64_t kv_block_numbers(const KvAttendLaunch& a) {
-  return a.total_q * a.group / kRows + a.seqs;
+inline int64_t kv_block_numbers(KvAttendLaunch& a) {
+  const int64_t most = ((int64_t)a.max_q * a.group + kRows - 1) / kRows;
+  const int64_t all = a.seqs * (most < 1 ? 1 : most), compact = a.total_q * a.group / kRows + a.seqs;
+  a.per_seq = fast_div(0);
+  if (all > 2 * compact || all > (1 << 30)) return compact;
+  a.per_seq = fast_div((uint32_t)(most < 1 ? 1 : most));
+  return all;
 }
 
 // The workspace: a record a workgroup, then for either end of each workgroup's
@@ -570,8 +660,8 @@ __device__ __forceinline__ void load_queries(const KvAttendLaunch& a, const KvUn
 // Every thread of the workgroup calls it; it ends synchronised.  most[]: ROWS
 // words of scratch.
 template <int FMT, int D, int kQ, int ROWS>
-__device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, const QueryRows<D, ROWS>& in, uint16_t* sq,
-                                              float* factor, uint32_t* most) {
+__device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, float kg, const QueryRows<D, ROWS>& in,
+                                              uint16_t* sq, float* factor, uint32_t* most) {
   using Q = QueryRows<D, ROWS>;
   const int tid = threadIdx.x;
   const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
@@ -592,7 +682,7 @@ __device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, const Que
     }
   }
   __syncthreads();
-  const float base = fabsf(a.scale) * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f);
+  const float base = fabsf(a.scale) * kLog2e * kg;
   for (int i = tid; i < ROWS; i += kThreads) {
     float f = base;
     if constexpr (kv_scaled_rows<FMT, kQ>()) f *= as_f((min(max(most[i] >> 23, 9u), 254u) - 8u) << 23);
@@ -677,7 +767,7 @@ __device__ __forceinline__ void kv_finish4(const KvAttendLaunch& a, const KvUnit
                                            float top, float total) {
   KvOutRow out;
   if (!kv_out_row(a, u.q0, u.m, u.head, rr, out)) return;
-  const float inv = total == 0.0f ? 0.0f : (FMT == 1 ? *a.p.vg : 1.0f) / total;
+  const float inv = total == 0.0f ? 0.0f : (FMT == 1 ? scalar(a.p.vg) : 1.0f) / total;
   store_out4(a, out.at * D + d, total == 0.0f ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : sum * inv);
   if (a.lse && d == 0)
     a.lse[out.at] = total == 0.0f ? -INFINITY : (top - KvType<FMT>::kUp + __builtin_amdgcn_logf(total)) * kLn2;
@@ -687,10 +777,10 @@ __device__ __forceinline__ void kv_finish4(const KvAttendLaunch& a, const KvUnit
 // it is the last one joins the pieces into the output.  kBatch pieces' loads
 // are in flight together.  Every thread of the workgroup calls it; `word`: LDS.
 template <int FMT, int D, int kRows, int kCost, int kThreadsWg, int kBatch>
-__device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u, int64_t begins, int64_t share,
+__device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u, int64_t begins, const KvShares& shares,
                                         unsigned int* word) {
   // its first real group and its last one say which workgroups have pieces
-  const int64_t w0 = quotient64(begins + kCost, share), w1 = quotient64(begins + kCost + u.groups - 1, share);
+  const int64_t w0 = kv_owner(shares, begins + kCost), w1 = kv_owner(shares, begins + kCost + u.groups - 1);
   const int pieces = (int)(w1 - w0) + 1;
   __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0
   __syncthreads();

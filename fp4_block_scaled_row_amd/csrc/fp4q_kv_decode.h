@@ -12,6 +12,8 @@
 // in flight while one is worked on.  Bound by HBM.
 #pragma once
 
+#include <limits.h>
+
 #include "fp4q_kv_attend.h"
 
 namespace fp4q {
@@ -56,8 +58,9 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   float* so = reinterpret_cast<float*>(s_main);
   uint16_t* sq = reinterpret_cast<uint16_t*>(s_main + (Shape::kQRegs ? 0 : Shape::kMain));
 
+  const float kg = FMT == 1 ? scalar(a.p.kg) : 1.0f;
   KvStretch st;
-  if (!kv_stretch<kRows, kGroupTokens, kGroupCost, kThreads>(a, numbers, st, s_scan)) return;
+  if (!kv_stretch<kRows, kGroupTokens, kGroupCost, kThreads, Shape::kWavesPerSimd == 3>(a, numbers, st, s_scan)) return;
   const KvUnit& u = st.u;
 
   // Codes of 2 x 16 tokens a lane, those of two groups in flight, and the page
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 
   bool more = take(true);
   while (more) {
-    stage_queries<FMT, D, kQ, kRows>(a, rows, sq, s_factor, s_most);
+    stage_queries<FMT, D, kQ, kRows>(a, kg, rows, sq, s_factor, s_most);
 
     u32x4_t qf[Shape::kQRegs ? kTiles : 1][Shape::kQRegs ? kQ : 1][Shape::kQRegs ? kChunks : 1];
     float factor[kTiles];
@@ -356,7 +359,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       }
     }
     __syncthreads();
-    if (!whole) kv_join<FMT, D, kRows, kGroupCost, kThreads, 8>(a, done, begins, st.share, s_most);
+    if (!whole) kv_join<FMT, D, kRows, kGroupCost, kThreads, 8>(a, done, begins, st.shares, s_most);
     __syncthreads();
   }
 }
@@ -364,15 +367,18 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 template <int FMT, int D, int kTiles, int kQ, int kP>
 hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   constexpr int kRows = 16 * kTiles;
-  const int64_t numbers = kv_block_numbers<kRows>(a);
+  KvAttendLaunch b = a;
+  const int64_t numbers = kv_block_numbers<kRows>(b);
   const int64_t groups = (a.most_tokens + kGroupTokens - 1) / kGroupTokens;
   const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kGroupCost);
   const int64_t resident = (int64_t)cus * DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd;
   const int grid = (int)min(min(most, resident), (int64_t)kMostWorkgroups);
+  b.thirds = resident;
+  b.few_groups = most < INT_MAX;
   if (a.p.page.d % 32 == 0)
-    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, true>), dim3(grid), dim3(kThreads), 0, st, a, numbers);
+    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, true>), dim3(grid), dim3(kThreads), 0, st, b, numbers);
   else
-    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, false>), dim3(grid), dim3(kThreads), 0, st, a, numbers);
+    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, false>), dim3(grid), dim3(kThreads), 0, st, b, numbers);
   return hipGetLastError();
 }
 

@@ -10,6 +10,8 @@
 // operand, the left one being the values read transposed.
 #pragma once
 
+#include <limits.h>
+
 #include "fp4q_kv_attend.h"
 
 namespace fp4q {
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
   KvStretch st;
   KvShared* shared = kv_shared(a, blockIdx.x);
   if (tid == 0) shared->first = shared->last = 0;
-  if (!kv_stretch<kRows, kStepTokens, kStepCost, 64 * kW>(a, numbers, st, s_scan)) return;
+  if (!kv_stretch<kRows, kStepTokens, kStepCost, 64 * kW, false>(a, numbers, st, s_scan)) return;
   const KvUnit& u = st.u;
   do {
     int group, last;      // the unit's groups [group, last) are this workgroup's
@@ -337,12 +339,14 @@ template <int FMT, int D, int kW, int kQ, int kP>
 hipError_t launch_prefill_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   using Shape = PrefillShape<FMT, D, kW, kQ, kP>;
   constexpr int kRows = Shape::kRows;
-  const int64_t numbers = kv_block_numbers<kRows>(a);
+  KvAttendLaunch b = a;
+  const int64_t numbers = kv_block_numbers<kRows>(b);
   const int64_t groups = (a.most_tokens + kStepTokens - 1) / kStepTokens;
   const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kStepCost);
   const int64_t resident = (int64_t)cus * (4 * Shape::kWavesPerSimd / kW);
   const int grid = (int)min(min(most, resident), (int64_t)kMostWorkgroups);
-  hipLaunchKernelGGL((kv_prefill_kernel<FMT, D, kW, kQ, kP>), dim3(grid), dim3(64 * kW), 0, st, a, numbers);
+  b.few_groups = most < INT_MAX;
+  hipLaunchKernelGGL((kv_prefill_kernel<FMT, D, kW, kQ, kP>), dim3(grid), dim3(64 * kW), 0, st, b, numbers);
   const hipError_t e = hipGetLastError();
   // (a unit of one step is never shared)
   if (e != hipSuccess || groups <= 1) return e;
