@@ -57,6 +57,7 @@ class KvCache:
         self.device = k_codes.device
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_global, self.v_global = k_global, v_global
+        # (the planes are kept here, so that the addresses stay theirs)
         a = _lib.KvCacheArgs()
         a.format, a.kv_heads, a.head_dim, a.page_size, a.num_pages = code, heads, half * 2, page, pages
         for what, t in planes:
@@ -66,6 +67,7 @@ class KvCache:
         a.code_stride[:] = k_codes.stride()[:3]
         a.scale_stride[:] = k_scales.stride()[:3]
         self._args = a
+        self._index = k_codes.get_device()
 
 
 def kv_cache(num_pages, page_size, kv_heads, head_dim, *, format="nvfp4", k_global=1.0, v_global=1.0, device="cuda"):
@@ -85,35 +87,55 @@ def kv_cache(num_pages, page_size, kv_heads, head_dim, *, format="nvfp4", k_glob
     return KvCache(format, *planes, *scales)
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# The raw handle of a device's current stream; what torch.cuda.current_stream()
+# wraps into an object, which takes as long as a small kernel.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(cache, function, *args):
+    """function(*args) with the cache's device as the current one."""
+    if torch.cuda.current_device() == cache._index:
+        return function(*args)
+    with torch.cuda.device(cache._index):
+        return function(*args)
 
 
 def _rotation(rotation):
     try:
         return _ROTATIONS[rotation]
-    except KeyError:
+    except (KeyError, TypeError):
         raise ValueError("fp4q: a cache's rotation is None or 'fwht128', got %r" % (rotation,)) from None
 
 
 def _rows(t, what, cache, heads):
-    """A [tokens, heads, head_dim] tensor of fp32 or bf16 on the cache's device."""
-    if not isinstance(t, torch.Tensor) or t.device != cache.device:
+    """Checks a [tokens, heads, head_dim] tensor of fp32 or bf16 on the cache's
+    device; its shape, strides and dtype code."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != cache._index:
         raise ValueError("fp4q: %s must be a tensor on the cache's device" % what)
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError("fp4q: %s must be float32 or bfloat16, got %s" % (what, t.dtype))
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads and t.shape[1] != heads):
-        raise ValueError("fp4q: %s must be [tokens, %s, %d], got %s" %
-                         (what, heads or "heads", cache.head_dim, tuple(t.shape)))
-    if t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != cache.head_dim or (heads and shape[1] != heads):
+        raise ValueError("fp4q: %s must be [tokens, %s, %d], got %s" % (what, heads or "heads", cache.head_dim, tuple(shape)))
+    if stride[2] != 1:
         raise ValueError("fp4q: rows of %s must be contiguous (stride(2) == 1)" % what)
+    return shape, stride, code
 
 
 def _index(t, what, cache, dtype, dims):
-    if not isinstance(t, torch.Tensor) or t.device != cache.device or t.dtype != dtype or t.dim() != dims:
+    if not isinstance(t, torch.Tensor) or t.get_device() != cache._index or t.dtype != dtype or t.dim() != dims:
         raise ValueError("fp4q: %s must be a %d-D %s tensor on the cache's device" % (what, dims, dtype))
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("fp4q: %s must be contiguous along its last dimension" % what)
+    return t.shape
+
+
+def _table(page_table, cache):
+    """Sequences, pages a sequence and the row stride of a page table."""
+    seqs, cols = _index(page_table, "page_table", cache, torch.int32, 2)
+    return seqs, cols, max(page_table.stride(0), cols) if seqs <= 1 else page_table.stride(0)
 
 
 def kv_cache_write(cache, k, v, slots, *, rotation=None):
@@ -127,21 +149,17 @@ def kv_cache_write(cache, k, v, slots, *, rotation=None):
     the basis of the normalised Hadamard transform of each 128 elements
     (head_dim a multiple of 128); pass the same to kv_cache_attention and
     kv_cache_read.  The bytes are those of quantize_nvfp4 / quantize_mxfp4."""
-    _rows(k, "k", cache, cache.kv_heads)
-    _rows(v, "v", cache, cache.kv_heads)
-    if k.shape != v.shape or k.dtype != v.dtype:
+    shape, ks, code = _rows(k, "k", cache, cache.kv_heads)
+    v_shape, vs, v_code = _rows(v, "v", cache, cache.kv_heads)
+    if shape != v_shape or code != v_code:
         raise ValueError("fp4q: k and v must have the same shape and dtype")
-    _index(slots, "slots", cache, torch.int64, 1)
-    if slots.shape[0] != k.shape[0]:
+    if _index(slots, "slots", cache, torch.int64, 1)[0] != shape[0]:
         raise ValueError("fp4q: slots must have one entry a token")
-    a = _lib.KvWriteArgs()
-    a.tokens = k.shape[0]
-    a.k, a.v, a.slots = k.data_ptr(), v.data_ptr(), slots.data_ptr()
-    a.k_stride[0], a.k_stride[1], _ = k.stride()
-    a.v_stride[0], a.v_stride[1], _ = v.stride()
-    a.in_dtype, a.rotation = _DTYPES[k.dtype], _rotation(rotation)
-    with torch.cuda.device(cache.device):
-        _lib.check(_lib.load().fp4q_kv_write(cache._args, a, _stream(cache.device)), "fp4q_kv_write")
+    a = _lib.KvWriteArgs(shape[0], k.data_ptr(), v.data_ptr(), ks[:2], vs[:2], slots.data_ptr(), code,
+                         _rotation(rotation))
+    status = _call(cache, _lib.load().fp4q_kv_write, cache._args, a, _raw_stream(cache._index))
+    if status:
+        _lib.check(status, "fp4q_kv_write")
 
 
 def kv_cache_read(cache, page_table, cu, *, total, starts=None, rotation=None, out_dtype=torch.bfloat16, out=None):
@@ -153,16 +171,13 @@ def kv_cache_read(cache, page_table, cu, *, total, starts=None, rotation=None, o
     onwards of sequence b; total: rows of the output.  Keys written with a
     rotation come back in their original basis when it is given here.  out: a
     pair of buffers to write, either of them None to leave it out."""
-    _index(page_table, "page_table", cache, torch.int32, 2)
-    _index(cu, "cu", cache, torch.int32, 1)
-    seqs = page_table.shape[0]
-    if cu.shape[0] != seqs + 1:
+    seqs, cols, stride = _table(page_table, cache)
+    if _index(cu, "cu", cache, torch.int32, 1)[0] != seqs + 1:
         raise ValueError("fp4q: cu must have one entry more than page_table has rows")
-    if starts is not None:
-        _index(starts, "starts", cache, torch.int32, 1)
-        if starts.shape[0] != seqs:
-            raise ValueError("fp4q: starts must have one entry a sequence")
-    if out_dtype not in _DTYPES:
+    if starts is not None and _index(starts, "starts", cache, torch.int32, 1)[0] != seqs:
+        raise ValueError("fp4q: starts must have one entry a sequence")
+    code = _DTYPES.get(out_dtype)
+    if code is None:
         raise TypeError("fp4q: out_dtype must be float32 or bfloat16, got %s" % out_dtype)
     shape = (int(total), cache.kv_heads, cache.head_dim)
     if out is None:
@@ -170,19 +185,16 @@ def kv_cache_read(cache, page_table, cu, *, total, starts=None, rotation=None, o
                torch.empty(shape, dtype=out_dtype, device=cache.device))
     else:
         for t in out:
-            if t is not None and (t.device != cache.device or t.dtype != out_dtype or tuple(t.shape) != shape
+            if t is not None and (t.get_device() != cache._index or t.dtype != out_dtype or tuple(t.shape) != shape
                                   or not t.is_contiguous()):
                 raise ValueError("fp4q: out must be contiguous %s tensors of shape %s" % (out_dtype, shape))
-    a = _lib.KvReadArgs()
-    a.page_table, a.table_stride = page_table.data_ptr(), page_table.stride(0)
-    a.table_cols, a.seqs, a.cu, a.total = page_table.shape[1], seqs, cu.data_ptr(), shape[0]
-    if seqs <= 1:
-        a.table_stride = max(a.table_stride, a.table_cols)
-    a.starts = None if starts is None else starts.data_ptr()
-    a.k_out, a.v_out = (None if t is None else t.data_ptr() for t in out)
-    a.out_dtype, a.rotation = _DTYPES[out_dtype], _rotation(rotation)
-    with torch.cuda.device(cache.device):
-        _lib.check(_lib.load().fp4q_kv_read(cache._args, a, _stream(cache.device)), "fp4q_kv_read")
+    k_out, v_out = (None if t is None else t.data_ptr() for t in out)
+    a = _lib.KvReadArgs(page_table.data_ptr(), stride, cols, seqs, cu.data_ptr(),
+                        None if starts is None else starts.data_ptr(), shape[0], k_out, v_out, code,
+                        _rotation(rotation))
+    status = _call(cache, _lib.load().fp4q_kv_read, cache._args, a, _raw_stream(cache._index))
+    if status:
+        _lib.check(status, "fp4q_kv_read")
     return out
 
 
@@ -191,13 +203,12 @@ def kv_cache_read(cache, page_table, cu, *, total, starts=None, rotation=None, o
 _workspaces = {}
 
 
-def _workspace(device, stream, need):
-    ws = _workspaces.get((device, stream))
-    if ws is None or ws.numel() < need:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("fp4q: the workspace of this stream is missing or too small; pass workspace= or make "
-                               "one call of this size on the stream before capturing it")
-        ws = _workspaces[(device, stream)] = torch.zeros(need, dtype=torch.uint8, device=device)
+def _grow_workspace(cache, a, stream):
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("fp4q: the workspace of this stream is missing or too small; pass workspace= or make one "
+                           "call of this size on the stream before capturing it")
+    need = _lib.load().fp4q_kv_attention_workspace_bytes(cache._args, a)
+    ws = _workspaces[(cache._index, stream)] = torch.zeros(need, dtype=torch.uint8, device=cache.device)
     return ws
 
 
@@ -218,50 +229,46 @@ def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None,
     Returns out [total, q_heads, head_dim] in q's dtype, or (out, lse) with
     the fp32 log-sum-exps [total, q_heads].  A query that sees no token gives
     zeros and -inf.  Nothing waits for the GPU: lengths and tables are read
-    there, so a captured call may be replayed with others in place."""
-    _rows(q, "q", cache, 0)
-    _index(page_table, "page_table", cache, torch.int32, 2)
-    _index(seq_lens, "seq_lens", cache, torch.int32, 1)
-    seqs, total, q_heads = page_table.shape[0], q.shape[0], q.shape[1]
-    if seq_lens.shape[0] != seqs:
+    there, so a captured call may be replayed with others in place.  Calls on
+    one stream share a workspace that is kept for it; workspace: another one
+    (a zeroed GPU tensor of fp4q_kv_attention_workspace_bytes bytes)."""
+    shape, qs, code = _rows(q, "q", cache, 0)
+    seqs, cols, stride = _table(page_table, cache)
+    total, q_heads = shape[0], shape[1]
+    if _index(seq_lens, "seq_lens", cache, torch.int32, 1)[0] != seqs:
         raise ValueError("fp4q: seq_lens must have one entry a sequence")
+    cu = None
     if cu_q is None:
         if total != seqs:
             raise ValueError("fp4q: without cu_q, q must have one row a sequence")
+        max_q = 1
     else:
-        _index(cu_q, "cu_q", cache, torch.int32, 1)
-        if cu_q.shape[0] != seqs + 1:
+        if _index(cu_q, "cu_q", cache, torch.int32, 1)[0] != seqs + 1:
             raise ValueError("fp4q: cu_q must have one entry more than there are sequences")
+        cu = cu_q.data_ptr()
+        max_q = total if max_q is None else int(max_q)
     if out is None:
-        out = torch.empty((total, q_heads, cache.head_dim), dtype=q.dtype, device=cache.device)
-    elif out.device != cache.device or out.dtype != q.dtype or tuple(out.shape) != tuple(q.shape) \
-            or not out.is_contiguous():
-        raise ValueError("fp4q: out must be a contiguous %s tensor of shape %s" % (q.dtype, tuple(q.shape)))
-    a = _lib.KvAttentionArgs()
-    a.q, a.out, a.total_q, a.q_heads, a.dtype = q.data_ptr(), out.data_ptr(), total, q_heads, _DTYPES[q.dtype]
-    a.q_stride[0], a.q_stride[1], _ = q.stride()
-    lse = None
-    if return_lse:
-        lse = torch.empty((total, q_heads), dtype=torch.float32, device=cache.device)
-        a.lse = lse.data_ptr()
-    if cu_q is not None:
-        a.cu_q = cu_q.data_ptr()
-        a.max_q = total if max_q is None else int(max_q)
-    a.seq_lens, a.page_table, a.table_stride = seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0)
-    a.table_cols, a.seqs = page_table.shape[1], seqs
-    if seqs <= 1:
-        a.table_stride = max(a.table_stride, a.table_cols)
-    a.causal, a.window, a.rotation = int(bool(causal)), int(window), _rotation(rotation)
-    a.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
-    lib = _lib.load()
-    with torch.cuda.device(cache.device):
-        stream = _stream(cache.device)
-        if workspace is None:
-            need = lib.fp4q_kv_attention_workspace_bytes(cache._args, a)
-            workspace = _workspace(cache.device, stream, need) if need else None
-        elif not workspace.is_cuda or not workspace.is_contiguous():
+        out = torch.empty(shape, dtype=q.dtype, device=cache.device)
+    elif out.get_device() != cache._index or out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
+        raise ValueError("fp4q: out must be a contiguous %s tensor of shape %s" % (q.dtype, tuple(shape)))
+    lse = torch.empty((total, q_heads), dtype=torch.float32, device=cache.device) if return_lse else None
+    a = _lib.KvAttentionArgs(q.data_ptr(), qs[:2], out.data_ptr(), lse.data_ptr() if return_lse else None, cu,
+                             seq_lens.data_ptr(), page_table.data_ptr(), stride, total, cols, seqs, max_q, q_heads,
+                             code, 1 if causal else 0, int(window), _rotation(rotation),
+                             cache.head_dim ** -0.5 if scale is None else float(scale))
+    run, stream = _lib.load().fp4q_kv_attention, _raw_stream(cache._index)
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("fp4q: the workspace must be a contiguous GPU tensor")
-        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _lib.check(lib.fp4q_kv_attention(cache._args, a, None if workspace is None else workspace.data_ptr(), size,
-                                         stream), "fp4q_kv_attention")
+        status = _call(cache, run, cache._args, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                       stream)
+    else:
+        ws, status = _workspaces.get((cache._index, stream)), _lib.FP4Q_ERR_WORKSPACE
+        if ws is not None:
+            status = _call(cache, run, cache._args, a, ws.data_ptr(), ws.numel(), stream)
+        if status == _lib.FP4Q_ERR_WORKSPACE:
+            ws = _grow_workspace(cache, a, stream)
+            status = _call(cache, run, cache._args, a, ws.data_ptr(), ws.numel(), stream)
+    if status:
+        _lib.check(status, "fp4q_kv_attention")
     return (out, lse) if return_lse else out

@@ -94,6 +94,8 @@ _lib = None
 def load():
     """Load libfp4q.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
