@@ -14,11 +14,21 @@ namespace {
 // NVFP4 encoding against a given tensor scale g, one block's factors computed
 // where they are used: the calls that matter most write a few rows, where a
 // table of every scale's factors would take longer than the rows.
-//   s = RNE_E4M3(bamax / (6 g)) and codes RNE_E2M1(x / (s g)) are decided on
-//   the exact quotients: fp32 products with the reciprocal off by -+2^-21
-//   bracket each quotient (product, reciprocal and bracket round by 2^-24
-//   each), brackets that disagree are resolved by the sign of an exact FMA
-//   residual, and tensor scales outside [2^-100, 2^100] take fp64 quotients.
+//   s = RNE_E4M3(bamax / (6 g)) and codes RNE_E2M1(x / (s g)) are the roundings
+// of the exact quotients.
+//   - g of at most 16 significant bits (a power of two, say): 6 g, s g and
+//     every decision point p times them (p to 5 bits, s 4) are fp32 numbers.
+//     x is one of them or differs by a unit in the last place at least, which
+//     moves the quotient by more than half of p's, so the correctly rounded
+//     fp32 quotient is on the same side of p as the exact one, or on it.  It is
+//     x times the rounded reciprocal, corrected by two FMAs.  (Such g make
+//     exact ties common in bf16 values, in every other wave's worth: a
+//     resolution of each was most of this kernel's time.)
+//   - other g in [2^-100, 2^100]: fp32 products with the reciprocal off by
+//     -+2^-21 bracket each quotient (product, reciprocal and bracket round by
+//     2^-24 each); brackets that disagree are resolved by the sign of an exact
+//     FMA residual.
+//   - the rest: fp64 quotients.
 __device__ __noinline__ uint32_t nv_encode_wide(const float v[8], float bamax, float g, uint32_t& scale) {
   const double mg = 6.0 * (double)g;
   scale = e4m3_encode_exact(bamax, (double)bamax / mg, mg);
@@ -32,29 +42,69 @@ __device__ __noinline__ uint32_t nv_encode_wide(const float v[8], float bamax, f
   return codes;
 }
 
-__device__ __forceinline__ uint32_t nv_encode_block(const float v[8], float bamax, float g, uint32_t& scale) {
-  if (!(g >= 0x1p-100f && g <= 0x1p100f)) return nv_encode_wide(v, bamax, g, scale);
+struct NvScale {
+  float g, g6, inv6;
+  bool few_bits, wide;
+};
+__device__ __forceinline__ NvScale nv_scale(float g) {
+  NvScale n;
+  n.g = g;
+  n.g6 = 6.0f * g;
+  n.inv6 = 1.0f / n.g6;
+  n.wide = !(g >= 0x1p-100f && g <= 0x1p100f);
+  n.few_bits = !n.wide && (as_u(g) & 0xFFu) == 0u;
+  return n;
+}
+
+__device__ __forceinline__ uint32_t pack_fp4(const float q[8]) {
+  const float one = e8m0_operand(127u);
+  uint32_t c = 0u;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[0], q[1], one, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[2], q[3], one, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[4], q[5], one, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[6], q[7], one, 3);
+  return c;
+}
+
+// x / d correctly rounded, from inv = RN(1 / d).  (The residual negated, so that
+// a zero keeps x's sign.)
+__device__ __forceinline__ float quotient_rn(float x, float d, float inv) {
+  const float q = x * inv;
+  return fmaf(-fmaf(q, d, -x), inv, q);
+}
+
+__device__ __forceinline__ uint32_t nv_encode_block(const float v[8], float bamax, const NvScale& n, uint32_t& scale) {
+  if (n.wide) return nv_encode_wide(v, bamax, n.g, scale);
+  // (a block so far above the tensor scale's range that quotients may overflow
+  // takes the next form)
+  if (n.few_bits && bamax * n.inv6 < 0x1p20f) {
+    const float t = fminf(quotient_rn(bamax, n.g6, n.inv6), 448.0f);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, t, 0, false) & 0xFFu;
+    const float d = e4m3_value_hw(c) * n.g;
+    const float inv = c ? 1.0f / d : 0.0f;
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = quotient_rn(v[i], d, inv);
+    scale = c;
+    return pack_fp4(q);
+  }
   constexpr float kBelow = 1.0f - 0x1p-21f, kAbove = 1.0f + 0x1p-21f;
-  const float inv6 = 1.0f / (6.0f * g);
-  const uint32_t c = nv_scale_code(bamax, inv6 * kBelow, inv6 * kAbove, 0.0, 0.0, false, 6.0f, g);
-  const float sd = e4m3_value(c);
-  const float inv = c ? 1.0f / (sd * g) : 0.0f;
-  const float lo = inv * kBelow, hi = inv * kAbove, one = e8m0_operand(127u);
-  uint32_t a = 0u, b = 0u;
-  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[0] * lo, v[1] * lo, one, 0);
-  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[2] * lo, v[3] * lo, one, 1);
-  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[4] * lo, v[5] * lo, one, 2);
-  a = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(a, v[6] * lo, v[7] * lo, one, 3);
-  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[0] * hi, v[1] * hi, one, 0);
-  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[2] * hi, v[3] * hi, one, 1);
-  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[4] * hi, v[5] * hi, one, 2);
-  b = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(b, v[6] * hi, v[7] * hi, one, 3);
-  uint32_t d = (a ^ b) & 0x77777777u;
+  const uint32_t c = nv_scale_code(bamax, n.inv6 * kBelow, n.inv6 * kAbove, 0.0, 0.0, false, 6.0f, n.g);
+  const float sd = e4m3_value_hw(c);
+  const float inv = c ? 1.0f / (sd * n.g) : 0.0f;
+  const float lo = inv * kBelow, hi = inv * kAbove;
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * lo;
+  uint32_t a = pack_fp4(q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * hi;
+  const uint32_t d = (a ^ pack_fp4(q)) & 0x77777777u;
   if (d != 0u) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if ((d >> (4 * i)) & 7u) {
-        const uint32_t mag = e2m1_rne_mag_exact(fabsf(v[i]), (a >> (4 * i)) & 7u, sd, g);
+        const uint32_t mag = e2m1_rne_mag_exact(fabsf(v[i]), (a >> (4 * i)) & 7u, sd, n.g);
         a = (a & ~(7u << (4 * i))) | (mag << (4 * i));
       }
     }
@@ -105,7 +155,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteLaunch w, flo
     }
   }
   const int64_t held = (int64_t)w.p.num_pages * w.p.page.d;
-  const float g = FMT == 0 ? 1.0f : *(values ? w.p.vg : w.p.kg);
+  const NvScale ns = nv_scale(FMT == 0 ? 1.0f : *(values ? w.p.vg : w.p.kg));
   uint8_t* cbase = values ? w.p.vc : w.p.kc;
   uint8_t* sbase = values ? w.p.vs : w.p.ks;
 #pragma unroll
@@ -119,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteLaunch w, flo
     if constexpr (FMT == 0) amax = max(amax, dpp_u32<kQuadXor2>(amax));
     uint32_t scale, codes;
     if constexpr (FMT == 0) codes = mx_encode_block(v, amax, scale);
-    else codes = nv_encode_block(v, as_f(amax), g, scale);
+    else codes = nv_encode_block(v, as_f(amax), ns, scale);
     if (amax >= 0x7F800000u) {   // a block with an infinity or NaN: the NaN scale code
       codes = 0u;
       scale = FMT == 0 ? 0xFFu : 0x7Fu;
@@ -177,111 +227,154 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int64_t t) 
   return lo;
 }
 
-// A thread takes kReadSlots slots, a workgroup's width apart, so that their
-// loads (page, codes, scale) overlap.
+// Reading.  What takes time is the chain of dependent loads from an output row
+// to its bytes (sequence, page number, codes), so a workgroup goes through a
+// run of slots kReadSlots a thread at a time, with the codes of the next step
+// and the page numbers of the one after in flight, and finds its first row's
+// sequence by bisection once.  Bound by the stores.
 constexpr int kReadSlots = 4;
+constexpr int kReadStep = kReadSlots * kThreads;
+
+template <int FMT, int OUT>
+__device__ __forceinline__ void read_store(float v[8], bool rotate, float g, bool nan, void* out, int64_t o) {
+  if constexpr (OUT == kF32) {
+    if (FMT != 0 && !rotate) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= g;
+    }
+    u32x4_t* dst = reinterpret_cast<u32x4_t*>(static_cast<float*>(out) + o);
+    __builtin_nontemporal_store(u32x4_t{as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])}, dst);
+    __builtin_nontemporal_store(u32x4_t{as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])}, dst + 1);
+  } else {
+    uint32_t h[4], tie = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool scale = FMT != 0 && !rotate;
+      const float a = scale ? v[2 * i] * g : v[2 * i], c = scale ? v[2 * i + 1] * g : v[2 * i + 1];
+      const bf16x2_t pk = {(__bf16)a, (__bf16)c};
+      h[i] = __builtin_bit_cast(uint32_t, pk);
+      if (scale) {
+        tie |= (as_u(a) & 0xFFFFu) == 0x8000u ? 1u : 0u;
+        tie |= (as_u(c) & 0xFFFFu) == 0x8000u ? 1u : 0u;
+      }
+    }
+    // v s g is rounded once: where an fp32 product sits on a bf16 midpoint
+    // the exact products decide (the rotated values are sums, rounded twice)
+    if (FMT != 0 && tie != 0u && !nan) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = bf16_of_product(v[2 * i], g) | (bf16_of_product(v[2 * i + 1], g) << 16);
+    }
+    __builtin_nontemporal_store(u32x4_t{h[0], h[1], h[2], h[3]},
+                                reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + o));
+  }
+}
 
 template <int FMT, int OUT>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float rot_scale, FastDiv row_slots,
-                                                           FastDiv heads, uint32_t nslots, int64_t first) {
+                                                           FastDiv heads, uint32_t nslots, int64_t first,
+                                                           uint32_t steps) {
   const bool values = r.k_out == nullptr || blockIdx.y != 0;
   const bool rotate = r.rotate && !values;
   const uint8_t* cbase = values ? r.p.vc : r.p.kc;
   const uint8_t* sbase = values ? r.p.vs : r.p.ks;
-  const int64_t holds = (int64_t)r.table_cols * r.p.page.d;
-  const uint32_t s0 = blockIdx.x * (kReadSlots * kThreads) + threadIdx.x;
-  uint32_t head[kReadSlots], at[kReadSlots], offset[kReadSlots], cw[kReadSlots], sb[kReadSlots];
-  int32_t page[kReadSlots];
-  int b = 0;
-#pragma unroll
-  for (int u = 0; u < kReadSlots; ++u) {
-    const uint32_t s = min(s0 + u * kThreads, nslots - 1);
-    const uint32_t row = quotient(s, row_slots), token = quotient(row, heads);
-    at[u] = s - row * row_slots.d;
-    head[u] = row - token * heads.d;
-    const int64_t t = first + token;
-    if (u == 0) b = sequence_of(r.cu, r.seqs, t);
-    while (b + 1 < r.seqs && t >= r.cu[b + 1]) ++b;
-    const int64_t pos = t - r.cu[b] + (r.starts ? r.starts[b] : 0);
-    page[u] = -1;
-    if (t < r.cu[b + 1] && pos >= 0 && pos < holds && pos <= 0x7FFFFFFF) {
-      const uint32_t col = quotient((uint32_t)pos, r.p.page);
-      offset[u] = (uint32_t)pos - col * r.p.page.d;
-      page[u] = r.table[b * r.table_stride + col];
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kReadSlots; ++u) {
-    cw[u] = 0u;
-    sb[u] = FMT == 0 ? 127u : 0u;
-    if ((uint32_t)page[u] < (uint32_t)r.p.num_pages) {
-      const uint64_t c = (uint64_t)page[u] * r.p.code_stride[0] + (uint64_t)head[u] * r.p.code_stride[1] +
-                         (uint64_t)offset[u] * r.p.code_stride[2];
-      const uint64_t e = (uint64_t)page[u] * r.p.scale_stride[0] + (uint64_t)head[u] * r.p.scale_stride[1] +
-                         (uint64_t)offset[u] * r.p.scale_stride[2];
-      cw[u] = *reinterpret_cast<const uint32_t*>(cbase + c + 4 * at[u]);
-      sb[u] = sbase[e + (FMT == 0 ? at[u] >> 2 : at[u] >> 1)];
-    }
-  }
+  void* out = values ? r.v_out : r.k_out;
   const float g = FMT == 0 ? 1.0f : *(values ? r.p.vg : r.p.kg);
+  const int64_t holds = min((int64_t)r.table_cols * r.p.page.d, (int64_t)0x7FFFFFFF);
+  const uint32_t begin = blockIdx.x * steps * kReadStep + threadIdx.x;
+  if (begin - threadIdx.x >= nslots) return;
+
+  // Where slots of a step are: set by look() as far as the page number, by
+  // codes() from there on.
+  struct Where {
+    int32_t page;
+    uint32_t offset, head, at;
+  };
+  struct Bytes {
+    uint32_t codes, scale;
+  };
+  Where where[kReadSlots];
+  Bytes bytes[kReadSlots];
+  // the sequence of the slot looked at last: rows [row0, row1), token of row 0
+  int b = 0;
+  int64_t row0 = 0, row1 = 0, shift = 0;
+  auto sequence = [&](int next) {
+    b = next;
+    row0 = r.cu[b];
+    row1 = r.cu[b + 1];
+    shift = (r.starts ? r.starts[b] : 0) - row0;
+  };
+  auto look = [&](uint32_t s0) {
 #pragma unroll
-  for (int u = 0; u < kReadSlots; ++u) {
-    float v[8];
-    const float sc = e8m0_operand(FMT == 0 ? sb[u] : 127u);
-    float2_t p;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 0); v[0] = p.x; v[1] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 1); v[2] = p.x; v[3] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 2); v[4] = p.x; v[5] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[u], sc, 3); v[6] = p.x; v[7] = p.y;
-    const bool nan = FMT == 0 ? sb[u] == 255u : (sb[u] & 0x7Fu) == 0x7Fu;
-    const float nanf = as_f(0x7FC00000u);
-    if constexpr (FMT != 0) {
-      const float sd = e4m3_value(sb[u] & 0x7Fu);
+    for (int u = 0; u < kReadSlots; ++u) {
+      const uint32_t s = min(s0 + u * kThreads, nslots - 1);
+      const uint32_t row = quotient(s, row_slots), token = quotient(row, heads);
+      where[u].at = s - row * row_slots.d;
+      where[u].head = row - token * heads.d;
+      const int64_t t = first + token;
+      while (t >= row1 && b + 1 < r.seqs) sequence(b + 1);
+      const int64_t pos = t + shift;
+      where[u].page = -1;
+      if (t >= row0 && t < row1 && pos >= 0 && pos < holds) {
+        const uint32_t col = quotient((uint32_t)pos, r.p.page);
+        where[u].offset = (uint32_t)pos - col * r.p.page.d;
+        where[u].page = r.table[b * r.table_stride + col];
+      }
+    }
+  };
+  auto fetch = [&]() {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= sd;   // exact: 2 and 4 significant bits
+    for (int u = 0; u < kReadSlots; ++u) {
+      bytes[u] = {0u, FMT == 0 ? 127u : 0u};
+      if ((uint32_t)where[u].page < (uint32_t)r.p.num_pages) {
+        const uint64_t c = (uint64_t)where[u].page * r.p.code_stride[0] + (uint64_t)where[u].head * r.p.code_stride[1] +
+                           (uint64_t)where[u].offset * r.p.code_stride[2];
+        const uint64_t e = (uint64_t)where[u].page * r.p.scale_stride[0] + (uint64_t)where[u].head * r.p.scale_stride[1] +
+                           (uint64_t)where[u].offset * r.p.scale_stride[2];
+        bytes[u].codes = *reinterpret_cast<const uint32_t*>(cbase + c + 4 * where[u].at);
+        bytes[u].scale = sbase[e + (FMT == 0 ? where[u].at >> 2 : where[u].at >> 1)];
+      }
+    }
+  };
+  sequence(sequence_of(r.cu, r.seqs, first + quotient(quotient(min(begin, nslots - 1), row_slots), heads)));
+  look(begin);
+  fetch();
+  if (steps > 1) look(begin + kReadStep);
+  for (uint32_t i = 0; i < steps; ++i) {
+    const uint32_t s0 = begin + i * kReadStep;
+    if (s0 - threadIdx.x >= nslots) return;
+    Bytes now[kReadSlots];
+#pragma unroll
+    for (int u = 0; u < kReadSlots; ++u) now[u] = bytes[u];
+    if (i + 1 < steps) {
+      fetch();
+      look(s0 + 2 * kReadStep);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = nan ? nanf : v[i];
-    if (rotate) {
+    for (int u = 0; u < kReadSlots; ++u) {
+      float v[8];
+      const float sc = e8m0_operand(FMT == 0 ? now[u].scale : 127u);     // (E8M0 255 gives NaN)
+      float2_t p;
+      p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(now[u].codes, sc, 0); v[0] = p.x; v[1] = p.y;
+      p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(now[u].codes, sc, 1); v[2] = p.x; v[3] = p.y;
+      p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(now[u].codes, sc, 2); v[4] = p.x; v[5] = p.y;
+      p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(now[u].codes, sc, 3); v[6] = p.x; v[7] = p.y;
+      bool nan = false;
       if constexpr (FMT != 0) {
+        const uint32_t e = now[u].scale & 0x7Fu;
+        nan = e == 0x7Fu;
+        const float sd = e4m3_value_hw(e);        // (0x7F gives NaN)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= g;
+        for (int k = 0; k < 8; ++k) v[k] *= sd;   // exact: 2 and 4 significant bits
       }
-      fwht128_lanes(v, threadIdx.x & 15, rot_scale);
-    }
-    const uint32_t s = s0 + u * kThreads;
-    if (s >= nslots) return;
-    const int64_t o = (first * heads.d * row_slots.d + s) * 8;
-    void* out = values ? r.v_out : r.k_out;
-    if constexpr (OUT == kF32) {
-      if (FMT != 0 && !rotate) {
+      if (rotate) {
+        if constexpr (FMT != 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= g;
-      }
-      u32x4_t* dst = reinterpret_cast<u32x4_t*>(static_cast<float*>(out) + o);
-      __builtin_nontemporal_store(u32x4_t{as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])}, dst);
-      __builtin_nontemporal_store(u32x4_t{as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])}, dst + 1);
-    } else {
-      uint32_t h[4], tie = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool scale = FMT != 0 && !rotate;
-        const float a = scale ? v[2 * i] * g : v[2 * i], c = scale ? v[2 * i + 1] * g : v[2 * i + 1];
-        const bf16x2_t pk = {(__bf16)a, (__bf16)c};
-        h[i] = __builtin_bit_cast(uint32_t, pk);
-        if (scale) {
-          tie |= (as_u(a) & 0xFFFFu) == 0x8000u ? 1u : 0u;
-          tie |= (as_u(c) & 0xFFFFu) == 0x8000u ? 1u : 0u;
+          for (int k = 0; k < 8; ++k) v[k] *= g;
         }
+        fwht128_lanes(v, threadIdx.x & 15, rot_scale);
       }
-      // v s g is rounded once: where an fp32 product sits on a bf16 midpoint
-      // the exact products decide (the rotated values are sums, rounded twice)
-      if (FMT != 0 && tie != 0u && !nan) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = bf16_of_product(v[2 * i], g) | (bf16_of_product(v[2 * i + 1], g) << 16);
-      }
-      __builtin_nontemporal_store(u32x4_t{h[0], h[1], h[2], h[3]},
-                                  reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + o));
+      const uint32_t s = s0 + u * kThreads;
+      if (s < nslots) read_store<FMT, OUT>(v, rotate, g, nan, out, (first * heads.d * row_slots.d + s) * 8);
     }
   }
 }
@@ -289,14 +382,19 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float
 template <int FMT>
 hipError_t launch_read_t(const KvReadLaunch& r, int64_t first, int64_t count, hipStream_t st) {
   const uint32_t per = (uint32_t)r.head_dim / 8, nslots = (uint32_t)(count * r.p.heads * per);
-  const dim3 grid((nslots + kReadSlots * kThreads - 1) / (kReadSlots * kThreads), r.k_out && r.v_out ? 2 : 1);
+  const uint32_t planes = r.k_out && r.v_out ? 2 : 1;
+  // at most 32 workgroups a CU (203 us for 0.9 GB of a batch's values, 209 with
+  // 16, 226 with 8)
+  const uint32_t all = (nslots + kReadStep - 1) / kReadStep, most = (uint32_t)device_cu_count() * 32 / planes;
+  const uint32_t steps = (all + most - 1) / most;
+  const dim3 grid((all + steps - 1) / steps, planes);
   const float c = (float)(1.0 / sqrt(128.0));
   if (r.out_dtype == kF32)
     hipLaunchKernelGGL((kv_read_kernel<FMT, kF32>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
-                       fast_div((uint32_t)r.p.heads), nslots, first);
+                       fast_div((uint32_t)r.p.heads), nslots, first, steps);
   else
     hipLaunchKernelGGL((kv_read_kernel<FMT, kBF16>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
-                       fast_div((uint32_t)r.p.heads), nslots, first);
+                       fast_div((uint32_t)r.p.heads), nslots, first, steps);
   return hipGetLastError();
 }
 
