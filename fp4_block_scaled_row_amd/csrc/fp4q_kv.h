@@ -85,7 +85,6 @@ struct KvAttendLaunch {
   uint8_t* ws;
   int64_t most_tokens;                   // what the table can hold of one sequence
   FastDiv group_div;
-  int32_t few_groups;                    // the groups' numbers fit 31 bits
   FastDiv per_seq;                       // query blocks a sequence where numbered so (d 0: by bisection)
   uint32_t thirds;                       // workgroups of a launch with three on every CU
 };

@@ -143,6 +143,15 @@ size_t kv_attend_workspace(const KvAttendLaunch& a) {
   return kv_workspace_bytes(cus * 3, 16 * p.tiles, a.head_dim);
 }
 
+// The schedule's numbers of a call (see fp4q_kv_attend.h), at most.
+int64_t kv_attend_groups(const KvAttendLaunch& a) {
+  const Plan p = attend_plan(a);
+  KvAttendLaunch b = a;
+  const int64_t numbers = kv_block_numbers(b, p.prefill ? 32 * p.waves : 16 * p.tiles);
+  // (the smaller of the two kernels' steps, the larger of their costs)
+  return kv_most_groups(b, numbers, 64, 16);
+}
+
 hipError_t launch_kv_attend(const KvAttendLaunch& a, hipStream_t s) {
   const Plan p = attend_plan(a);
   const int cus = device_cu_count();
@@ -231,7 +240,8 @@ fp4q_status fp4q_kv_read(const fp4q_kv_cache* cache, const fp4q_kv_read_args* ar
 
 size_t fp4q_kv_attention_workspace_bytes(const fp4q_kv_cache* cache, const fp4q_kv_attention_args* args) {
   KvAttendLaunch l;
-  if (check_attention(cache, args, &l) != FP4Q_OK || l.total_q == 0 || l.seqs == 0) return 0;
+  if (check_attention(cache, args, &l) != FP4Q_OK || l.total_q == 0 || l.seqs == 0 || kv_attend_groups(l) > INT_MAX)
+    return 0;
   return kv_attend_workspace(l);
 }
 
@@ -241,6 +251,7 @@ fp4q_status fp4q_kv_attention(const fp4q_kv_cache* cache, const fp4q_kv_attentio
   const fp4q_status st = check_attention(cache, args, &l);
   if (st != FP4Q_OK) return st;
   if (l.total_q == 0 || l.seqs == 0) return FP4Q_OK;
+  if (kv_attend_groups(l) > INT_MAX) return FP4Q_ERR_UNSUPPORTED;
   const size_t need = kv_attend_workspace(l);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return FP4Q_ERR_WORKSPACE;
   l.ws = static_cast<uint8_t*>(workspace);

@@ -279,13 +279,7 @@ __device__ __forceinline__ u32x2_t read_transposed(const uint16_t* p) {
 // so much that most of those would be skipped, cu[b] group / kRows + b + k
 // (rounded down), which skips at most one a sequence, and a thread finds a
 // number's sequence by bisection.
-// A value that the whole wave reads, through the scalar cache: its wait does
-// not take in the vector loads that are on their way.
-template <typename T>
-__device__ __forceinline__ T scalar(const T* p) {
-  return *reinterpret_cast<const __attribute__((address_space(4))) T*>(reinterpret_cast<uintptr_t>(p));
-}
-
+//   All of these numbers are below 2^31 (calls that could pass it are refused).
 struct KvUnit {
   int b, block, blocks;   // sequence, block of its query rows, its blocks
   int head;               // cache head
@@ -295,38 +289,50 @@ struct KvUnit {
   int groups;             // at least 1: rows without tokens are written too
 };
 
+// A value that the whole wave reads, through the scalar cache: its wait does
+// not take in the vector loads that are on their way.
+template <typename T>
+__device__ __forceinline__ T scalar(const T* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) T*>(reinterpret_cast<uintptr_t>(p));
+}
+
 // Row of q of sequence b's first query (never past the rows there are).
 template <bool kUniform = false>
 __device__ __forceinline__ int kv_first_query(const KvAttendLaunch& a, int b) {
   const int q = a.cu_q ? (kUniform ? scalar(a.cu_q + b) : a.cu_q[b]) : b;
-  return q < 0 ? 0 : (q > (int)a.total_q ? (int)a.total_q : q);
+  return min(max(q, 0), (int)a.total_q);
 }
 
 template <int kRows>
-__device__ __forceinline__ int64_t kv_block_number(const KvAttendLaunch& a, int b) {
-  return (int64_t)kv_first_query(a, b) * a.group / kRows + b;
+__device__ __forceinline__ int kv_block_number(const KvAttendLaunch& a, int b) {
+  return (int)((uint32_t)(kv_first_query(a, b) * a.group) / kRows) + b;
 }
 
-template <int kRows, int kTokens, bool kUniform = false>
+template <int kRows, bool kUniform = false>
 __device__ __forceinline__ void kv_sequence(const KvAttendLaunch& a, int b, KvUnit& u) {
   u.b = b;
   u.q0 = kv_first_query<kUniform>(a, b);
   u.m = kv_first_query<kUniform>(a, b + 1) - u.q0;
-  const int len = kUniform ? scalar(a.lens + b) : a.lens[b];
-  u.n = len < 0 ? 0 : (len > a.most_tokens ? (int)a.most_tokens : len);
-  u.blocks = u.m > 0 ? (int)(((int64_t)u.m * a.group + kRows - 1) / kRows) : 0;
+  u.n = min(max(kUniform ? scalar(a.lens + b) : a.lens[b], 0), (int)a.most_tokens);
+  u.blocks = u.m > 0 ? (int)(((uint32_t)(u.m * a.group) + kRows - 1) / kRows) : 0;
+}
+
+// Queries of the first and last of rows row0 .. row0 + kRows - 1.
+template <int kRows>
+__device__ __forceinline__ void kv_queries(const KvAttendLaunch& a, const KvUnit& u, int row0, int& i0, int& i1) {
+  i0 = (int)quotient((uint32_t)row0, a.group_div);
+  i1 = min((int)quotient((uint32_t)(row0 + kRows - 1), a.group_div), u.m - 1);
 }
 
 template <int kRows, int kTokens>
 __device__ __forceinline__ void kv_block_at(const KvAttendLaunch& a, int row0, KvUnit& u) {
   u.row0 = row0;
-  const int i0 = (int)quotient((uint32_t)u.row0, a.group_div);
-  const int i1 = min((int)quotient((uint32_t)(u.row0 + kRows - 1), a.group_div), u.m - 1);
-  const int64_t past = (int64_t)u.n - u.m;    // tokens before the first query's (may be negative)
-  const int64_t hi = a.causal ? past + i1 + 1 : u.n;
-  const int64_t lo = a.window > 0 ? past + i0 + 1 - a.window : 0;
-  u.hi = (int)(hi < 0 ? 0 : hi);
-  u.lo = (int)(lo < 0 ? 0 : (lo > u.hi ? u.hi : lo)) & ~31;     // (whole tiles of 32: a page's, where pages allow)
+  int i0, i1;
+  kv_queries<kRows>(a, u, row0, i0, i1);
+  const int past = u.n - u.m;                 // tokens before the first query's (may be negative)
+  u.hi = max(0, a.causal ? past + i1 + 1 : u.n);
+  const int first = a.window > 0 && past + i0 + 1 > a.window ? past + i0 + 1 - a.window : 0;
+  u.lo = min(first, u.hi) & ~31;              // (whole tiles of 32: a page's, where pages allow)
   u.groups = max(1, (u.hi - u.lo + kTokens - 1) / kTokens);
 }
 template <int kRows, int kTokens>
@@ -337,24 +343,23 @@ __device__ __forceinline__ void kv_block(const KvAttendLaunch& a, int block, KvU
 
 // Block number -> sequence and block; false: a skipped number.
 template <int kRows, int kTokens>
-__device__ __forceinline__ bool kv_numbered(const KvAttendLaunch& a, int64_t number, KvUnit& u) {
-  int64_t block;
+__device__ __forceinline__ bool kv_numbered(const KvAttendLaunch& a, int number, KvUnit& u) {
+  int b, block;
   if (a.per_seq.d) {
-    const int b = (int)quotient((uint32_t)number, a.per_seq);      // (all below 2^31)
-    kv_sequence<kRows, kTokens>(a, b, u);
-    block = number - (int64_t)b * a.per_seq.d;
+    b = (int)quotient((uint32_t)number, a.per_seq);
+    block = number - b * (int)a.per_seq.d;
   } else {
-    int lo = 0, hi = a.seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (kv_block_number<kRows>(a, mid) <= number) lo = mid;
+    b = 0;
+    for (int hi = a.seqs; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (kv_block_number<kRows>(a, mid) <= number) b = mid;
       else hi = mid;
     }
-    kv_sequence<kRows, kTokens>(a, lo, u);
-    block = number - kv_block_number<kRows>(a, lo);
+    block = number - kv_block_number<kRows>(a, b);
   }
+  kv_sequence<kRows>(a, b, u);
   if (block < 0 || block >= u.blocks) return false;
-  kv_block<kRows, kTokens>(a, (int)block, u);
+  kv_block<kRows, kTokens>(a, block, u);
   return true;
 }
 
@@ -362,49 +367,46 @@ __device__ __forceinline__ bool kv_numbered(const KvAttendLaunch& a, int64_t num
 // three workgroups on each CU the first ones were done in 66 us, the second in
 // 72 and the third in 78 where all had the same; where a launch fills the chip
 // with three a CU, they take shares of 36, 32 and 28 parts instead.
-constexpr int kPart0 = 36, kPart1 = 32, kPart2 = 28;
+constexpr uint32_t kPart0 = 36, kPart1 = 32, kPart2 = 28;
 struct KvShares {
-  int64_t size0, size1, size2;      // groups of a workgroup of the first, second and last `per`
-  int64_t from1, from2;             // where the second and the last begin
-  int per;
+  uint32_t size0, size1, size2;      // groups of a workgroup of the first, second and last `per`
+  uint32_t from1, from2;             // where the second and the last begin
+  uint32_t per;
 };
-// x / d of a non-negative x: in 32 bits where that holds it.
-__device__ __forceinline__ int64_t quotient64(int64_t x, int64_t d) {
-  return ((x | d) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
-}
-__device__ __forceinline__ KvShares kv_shares(int64_t total, int workgroups, bool thirds) {
+__device__ __forceinline__ KvShares kv_shares(uint32_t total, uint32_t workgroups, bool thirds) {
   KvShares s;
   if (thirds) {
     s.per = workgroups / 3;
-    const int64_t all = (int64_t)s.per * (kPart0 + kPart1 + kPart2);
-    s.size0 = quotient64(total * kPart0 + all - 1, all);
-    s.size1 = quotient64(total * kPart1 + all - 1, all);
-    s.size2 = quotient64(total * kPart2 + all - 1, all);
+    // (rounded up: sizes are for per * 96 parts of total)
+    const uint32_t each = (total + s.per - 1) / s.per;
+    s.size0 = (each * kPart0 + 95) / 96;
+    s.size1 = (each * kPart1 + 95) / 96;
+    s.size2 = (each * kPart2 + 95) / 96;
     s.from1 = s.per * s.size0;
     s.from2 = s.from1 + s.per * s.size1;
   } else {
     s.per = workgroups;
-    s.size0 = s.size1 = s.size2 = quotient64(total + workgroups - 1, workgroups);
+    s.size0 = s.size1 = s.size2 = (total + workgroups - 1) / workgroups;
     s.from1 = s.from2 = s.per * s.size0;
   }
   return s;
 }
-__device__ __forceinline__ int64_t kv_begin(const KvShares& s, int w) {
+__device__ __forceinline__ uint32_t kv_begin(const KvShares& s, uint32_t w) {
   return w < s.per ? w * s.size0 : (w < 2 * s.per ? s.from1 + (w - s.per) * s.size1 : s.from2 + (w - 2 * s.per) * s.size2);
 }
 // The workgroup that has group x.
-__device__ __forceinline__ int64_t kv_owner(const KvShares& s, int64_t x) {
-  return x < s.from1 ? quotient64(x, s.size0)
-                     : (x < s.from2 ? s.per + quotient64(x - s.from1, s.size1)
-                                    : 2 * s.per + quotient64(x - s.from2, s.size2));
+__device__ __forceinline__ uint32_t kv_owner(const KvShares& s, uint32_t x) {
+  const uint32_t third = x < s.from1 ? 0u : (x < s.from2 ? 1u : 2u);
+  const uint32_t from = third == 0u ? 0u : (third == 1u ? s.from1 : s.from2);
+  const uint32_t size = third == 0u ? s.size0 : (third == 1u ? s.size1 : s.size2);
+  return third * s.per + (x - from) / size;
 }
 
 // A workgroup's stretch: `left` counted groups from the `at`-th of unit `u` on,
 // whose own first one has the number `begins`.
 struct KvStretch {
   KvUnit u;
-  int at;
-  int64_t left, begins;
+  int at, left, begins;
   KvShares shares;
 };
 // The groups [from, to) that a stretch has of its current unit: none where it
@@ -412,49 +414,39 @@ struct KvStretch {
 template <int kCost>
 __device__ __forceinline__ void kv_part(const KvStretch& st, int& from, int& to) {
   from = max(0, st.at - kCost);
-  to = max(0, (int)min((int64_t)st.u.groups + kCost, st.at + st.left) - kCost);
+  to = max(0, min(st.u.groups + kCost - st.at, st.left) + st.at - kCost);
 }
 
 // Inclusive sum over the lanes of a wave: within rows of 16 lanes, then rows 0
 // and 2 into 1 and 3, then the first two into the last two.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);     // row_shr:1
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);     // row_shr:2
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);     // row_shr:4
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);     // row_shr:8
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);    // row_bcast:15
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);    // row_bcast:31
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);     // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);     // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);     // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // row_bcast:31
   return v;
 }
 
 // Every thread of the workgroup calls it, with all query block numbers below
-// `numbers`; scratch: 4 + waves words of LDS.  False: nothing to do.  To 256
+// `numbers`; scratch: 6 + waves words of LDS.  False: nothing to do.  To 256
 // numbers each wave goes through them all by itself, which spares the first
 // step of every call its barriers.
 template <int kRows, int kTokens, int kCost, int kThreadsWg, bool kThirds>
-__device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numbers, KvStretch& st, long long* scratch) {
+__device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int numbers, KvStretch& st, int* scratch) {
   constexpr int kW = kThreadsWg / 64;
-  const bool alone = numbers <= 256 && a.few_groups;
+  const bool alone = numbers <= 256;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int id = alone ? lane : (int)threadIdx.x;
-  const int64_t each = alone ? ((int)numbers + 63) >> 6 : quotient64(numbers + kThreadsWg - 1, kThreadsWg);
-  const int64_t x0 = id * each, x1 = x0 + each < numbers ? x0 + each : numbers;
-  long long mine = 0;
+  const int each = alone ? (numbers + 63) / 64 : (numbers + kThreadsWg - 1) / kThreadsWg;
+  const int x0 = (alone ? lane : (int)threadIdx.x) * each, x1 = min(x0 + each, numbers);
+  int mine = 0;
   KvUnit u = {};
-  for (int64_t x = x0; x < x1; ++x)
-    if (kv_numbered<kRows, kTokens>(a, x, u)) mine += (long long)(u.groups + kCost) * a.p.heads;
-  long long upto = mine, total = 0;     // inclusive scan
-  if (a.few_groups) {
-    upto = (long long)wave_scan((uint32_t)mine);
-  } else {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const long long x = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += x;
-    }
-  }
+  for (int x = x0; x < x1; ++x)
+    if (kv_numbered<kRows, kTokens>(a, x, u)) mine += (u.groups + kCost) * a.p.heads;
+  int upto = wave_scan(mine), total = 0;     // inclusive scan
   if (alone) {
-    total = __builtin_amdgcn_readlane((int)upto, 63);
+    total = __builtin_amdgcn_readlane(upto, 63);
   } else {
     if (lane == 63) scratch[wave] = upto;
     __syncthreads();
@@ -463,48 +455,45 @@ __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int64_t numb
       if (w < wave) upto += scratch[w];
       total += scratch[w];
     }
+    total = __builtin_amdgcn_readfirstlane(total);
   }
-  st.shares = kv_shares(total, gridDim.x, kThirds && gridDim.x == a.thirds);
-  const long long begin = kv_begin(st.shares, blockIdx.x);
-  const long long end = min((long long)kv_begin(st.shares, blockIdx.x + 1), total);
+  st.shares = kv_shares((uint32_t)total, gridDim.x, kThirds && gridDim.x == a.thirds);
+  const int begin = (int)min(kv_begin(st.shares, blockIdx.x), (uint32_t)total);
+  const int end = (int)min(kv_begin(st.shares, blockIdx.x + 1), (uint32_t)total);
   if (begin >= end) return false;
-  long long before = upto - mine;
+  int before = upto - mine;
   const bool owner = begin >= before && begin < upto;
   if (owner && each > 1) {
-    for (int64_t x = x0; x < x1; ++x) {
+    for (int x = x0; x < x1; ++x) {
       if (!kv_numbered<kRows, kTokens>(a, x, u)) continue;
-      const long long here = (long long)(u.groups + kCost) * a.p.heads;
+      const int here = (u.groups + kCost) * a.p.heads;
       if (begin < before + here) break;
       before += here;
     }
   }
-  int found[5] = {u.b, u.block, u.q0, u.m, u.n};
-  long long in_block = begin - before;
+  int found[6] = {u.b, u.block, u.q0, u.m, u.n, begin - before};
   if (alone) {
     const int from = __ffsll((long long)__ballot(owner)) - 1;
 #pragma unroll
-    for (int i = 0; i < 5; ++i) found[i] = __builtin_amdgcn_readlane(found[i], from);
-    in_block = __builtin_amdgcn_readlane((int)in_block, from);
+    for (int i = 0; i < 6; ++i) found[i] = __builtin_amdgcn_readlane(found[i], from);
   } else {
-    int* out = reinterpret_cast<int*>(scratch + kW);
     if (owner) {
 #pragma unroll
-      for (int i = 0; i < 5; ++i) out[i] = found[i];
-      scratch[kW + 3] = in_block;
+      for (int i = 0; i < 6; ++i) scratch[kW + i] = found[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 5; ++i) found[i] = __builtin_amdgcn_readfirstlane(out[i]);
-    in_block = scratch[kW + 3];
+    for (int i = 0; i < 6; ++i) found[i] = __builtin_amdgcn_readfirstlane(scratch[kW + i]);
   }
   st.u.b = found[0];
   st.u.q0 = found[2];
   st.u.m = found[3];
   st.u.n = found[4];
-  st.u.blocks = (int)(((int64_t)st.u.m * a.group + kRows - 1) / kRows);
+  st.u.blocks = (int)(((uint32_t)(st.u.m * a.group) + kRows - 1) / kRows);
   kv_block<kRows, kTokens>(a, found[1], st.u);
-  st.u.head = __builtin_amdgcn_readfirstlane((int)quotient64(in_block, st.u.groups + kCost));
-  st.at = __builtin_amdgcn_readfirstlane((int)(in_block - (int64_t)st.u.head * (st.u.groups + kCost)));
+  const int counted = st.u.groups + kCost;
+  st.u.head = found[5] / counted;
+  st.at = found[5] - st.u.head * counted;
   st.left = end - begin;
   st.begins = begin - st.at;
   return true;
@@ -522,7 +511,7 @@ __device__ __forceinline__ bool kv_next(const KvAttendLaunch& a, KvStretch& st) 
   u.head = 0;
   int block = u.block + 1;
   while (block >= u.blocks && u.b + 1 < a.seqs) {
-    kv_sequence<kRows, kTokens, true>(a, u.b + 1, u);
+    kv_sequence<kRows, true>(a, u.b + 1, u);
     block = 0;
   }
   kv_block<kRows, kTokens>(a, block, u);
@@ -530,14 +519,18 @@ __device__ __forceinline__ bool kv_next(const KvAttendLaunch& a, KvStretch& st) 
 }
 
 // Numbers of all query blocks lie below this; sets the kind of numbering.
-template <int kRows>
-inline int64_t kv_block_numbers(KvAttendLaunch& a) {
-  const int64_t most = ((int64_t)a.max_q * a.group + kRows - 1) / kRows;
-  const int64_t all = a.seqs * (most < 1 ? 1 : most), compact = a.total_q * a.group / kRows + a.seqs;
+inline int64_t kv_block_numbers(KvAttendLaunch& a, int rows) {
+  const int64_t most = ((int64_t)a.max_q * a.group + rows - 1) / rows;
+  const int64_t all = a.seqs * (most < 1 ? 1 : most), compact = a.total_q * a.group / rows + a.seqs;
   a.per_seq = fast_div(0);
   if (all > 2 * compact || all > (1 << 30)) return compact;
   a.per_seq = fast_div((uint32_t)(most < 1 ? 1 : most));
   return all;
+}
+// The counted groups of a call are at most so many.
+inline int64_t kv_most_groups(const KvAttendLaunch& a, int64_t numbers, int tokens, int cost) {
+  const int64_t groups = (a.most_tokens + tokens - 1) / tokens;
+  return numbers * a.p.heads * ((groups < 1 ? 1 : groups) + cost);
 }
 
 // The workspace: a record a workgroup, then for either end of each workgroup's
@@ -710,21 +703,19 @@ __device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, float kg,
 // Tokens [from, from + count) that row rr of a unit's sequence sees.
 __device__ __forceinline__ void kv_sees(const KvAttendLaunch& a, const KvUnit& u, int rr, int& from, uint32_t& count) {
   const int i = (int)quotient((uint32_t)rr, a.group_div);
-  const int64_t pos = (int64_t)u.n - u.m + i;     // the query's own token
-  const int64_t to = a.causal ? min(pos + 1, (int64_t)u.n) : u.n;
-  const int64_t lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
-  from = (int)min(lo, (int64_t)u.n);
-  count = i < u.m && to > lo ? (uint32_t)(to - lo) : 0u;
+  const int upto = u.n - u.m + i + 1;         // the query's own token is the one before
+  const int to = a.causal ? min(upto, u.n) : u.n;
+  from = a.window > 0 && upto > a.window ? min(upto - a.window, u.n) : 0;
+  count = i < u.m && to > from ? (uint32_t)(to - from) : 0u;
 }
-
-// Tokens [from, to) that every row of the block sees.
+// Tokens [from, to) that every row of a block sees.
 template <int kRows>
 __device__ __forceinline__ void kv_all_see(const KvAttendLaunch& a, const KvUnit& u, int& from, int& to) {
-  const int i0 = (int)quotient((uint32_t)u.row0, a.group_div);
-  const int i1 = min((int)quotient((uint32_t)(u.row0 + kRows - 1), a.group_div), u.m - 1);
-  const int64_t past = (int64_t)u.n - u.m;
-  to = (int)max((int64_t)0, a.causal ? min((int64_t)u.n, past + i0 + 1) : (int64_t)u.n);
-  from = a.window > 0 ? (int)max((int64_t)0, past + i1 - a.window + 1) : 0;
+  int i0, i1;
+  kv_queries<kRows>(a, u, u.row0, i0, i1);
+  const int past = u.n - u.m;
+  to = max(0, a.causal ? min(u.n, past + i0 + 1) : u.n);
+  from = a.window > 0 && past + i1 + 1 > a.window ? past + i1 + 1 - a.window : 0;
 }
 
 // Values that are no finite numbers, in a tile that some rows see only in
@@ -777,11 +768,12 @@ __device__ __forceinline__ void kv_finish4(const KvAttendLaunch& a, const KvUnit
 // it is the last one joins the pieces into the output.  kBatch pieces' loads
 // are in flight together.  Every thread of the workgroup calls it; `word`: LDS.
 template <int FMT, int D, int kRows, int kCost, int kThreadsWg, int kBatch>
-__device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u, int64_t begins, const KvShares& shares,
+__device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u, int begins, const KvShares& shares,
                                         unsigned int* word) {
   // its first real group and its last one say which workgroups have pieces
-  const int64_t w0 = kv_owner(shares, begins + kCost), w1 = kv_owner(shares, begins + kCost + u.groups - 1);
-  const int pieces = (int)(w1 - w0) + 1;
+  const int w0 = (int)kv_owner(shares, (uint32_t)(begins + kCost));
+  const int w1 = (int)kv_owner(shares, (uint32_t)(begins + kCost + u.groups - 1));
+  const int pieces = w1 - w0 + 1;
   __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -792,7 +784,7 @@ __device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u
   }
   __syncthreads();
   if (*word != (unsigned int)pieces) return;
-  const int rows = (int)min((int64_t)kRows, (int64_t)u.m * a.group - u.row0);
+  const int rows = min(kRows, u.m * a.group - u.row0);
   for (int item = threadIdx.x; item < rows * (D / 4); item += kThreadsWg) {
     const int rr = item / (D / 4), d = 4 * (item % (D / 4));
     f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -849,7 +841,7 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttendLaunch a, int
   u.q0 = kv_first_query(a, u.b);
   u.m = kv_first_query(a, u.b + 1) - u.q0;
   const int item = blockIdx.y * kThreads + threadIdx.x, rr = item / (D / 4), d = 4 * (item % (D / 4));
-  if (rr >= min((int64_t)kRows, (int64_t)u.m * a.group - u.row0)) return;
+  if (rr >= min(kRows, u.m * a.group - u.row0)) return;
   f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
   float top = kNoMax, total = 0.0f;
   for (int p = 0; p < pieces; p += kBatch) {

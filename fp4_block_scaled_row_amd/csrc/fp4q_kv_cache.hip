@@ -210,14 +210,23 @@ hipError_t launch_write_t(const KvWriteLaunch& w, int64_t first, int64_t count, 
   part.v = static_cast<const char*>(w.v) + first * w.v_stride[0] * esz;
   part.slots = w.slots + first;
   const uint32_t nslots = (uint32_t)(count * w.p.heads * (w.head_dim / 8));
-  // four slots a thread once that still leaves every CU several workgroups
-  if (nslots >= (uint32_t)device_cu_count() * 4 * 4 * kThreads) return launch_write_n<FMT, 4>(part, nslots, st);
+  // four slots a thread once that still leaves every CU a workgroup (865 thousand
+  // slots a plane: 15 us against 18 with one)
+  if (nslots >= (uint32_t)device_cu_count() * 4 * kThreads) return launch_write_n<FMT, 4>(part, nslots, st);
   return launch_write_n<FMT, 1>(part, nslots, st);
 }
 
 // ----------------------------------------------------------------------------
-// Last index b with cu[b] <= t, of a cumulative array cu[0..n] (cu[0] = 0).
+// Last index b < n with cu[b] <= t, of a cumulative array cu[0..n] (cu[0] = 0),
+// for a t that the wave shares: 64 entries at a time, whose loads do not wait
+// for each other, up to 512 of them, by bisection beyond.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int64_t t) {
+  const int lane = threadIdx.x & 63;
+  if (n <= 512) {
+    int before = 0;
+    for (int i = 0; i < n; i += 64) before += __popcll(__ballot(i + lane < n && cu[min(i + lane, n)] <= t));
+    return max(before - 1, 0);
+  }
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -230,13 +239,23 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int64_t t) 
 // Reading.  What takes time is the chain of dependent loads from an output row
 // to its bytes (sequence, page number, codes), so a workgroup goes through a
 // run of slots kReadSlots a thread at a time, with the codes of the next step
-// and the page numbers of the one after in flight, and finds its first row's
-// sequence by bisection once.  Bound by the stores.
-constexpr int kReadSlots = 4;
-constexpr int kReadStep = kReadSlots * kThreads;
+// and the page numbers of the one after in flight; it finds its first row's
+// sequence once and goes on from there, the next kAhead sequences' bounds being
+// in LDS.  Bound by the stores.
+constexpr int kAhead = kThreads;
+
+// p = RN(v g) moved by its last bit towards the exact product where it is a bf16
+// midpoint and not that product itself.  The sign of the rounding error is that
+// of an FMA, at a scale where nothing underflows.
+__device__ __forceinline__ float off_midpoint(float v, float g, float p) {
+  const float a = fabsf(v), b = fabsf(p), up = b < 1.0f ? 0x1p64f : 1.0f;
+  const float e = fmaf(a * up, g, -(b * up));
+  const int by = (e > 0.0f ? 1 : 0) - (e < 0.0f ? 1 : 0);
+  return (as_u(p) & 0xFFFFu) == 0x8000u ? as_f(as_u(p) + (uint32_t)by) : p;
+}
 
 template <int FMT, int OUT>
-__device__ __forceinline__ void read_store(float v[8], bool rotate, float g, bool nan, void* out, int64_t o) {
+__device__ __forceinline__ void read_store(float v[8], bool rotate, float g, void* out, int64_t o) {
   if constexpr (OUT == kF32) {
     if (FMT != 0 && !rotate) {
 #pragma unroll
@@ -246,33 +265,40 @@ __device__ __forceinline__ void read_store(float v[8], bool rotate, float g, boo
     __builtin_nontemporal_store(u32x4_t{as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])}, dst);
     __builtin_nontemporal_store(u32x4_t{as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])}, dst + 1);
   } else {
-    uint32_t h[4], tie = 0u;
+    // v s g is rounded once (the rotated values are sums, rounded twice): an
+    // fp32 product that sits on a bf16 midpoint is moved off it first, to the
+    // side on which the exact product lies
+    if (FMT != 0 && !rotate) {
+      float p[8];
+      bool tie = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = v[i] * g;
+        tie |= (as_u(p[i]) & 0xFFFFu) == 0x8000u;
+      }
+      if (tie) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = off_midpoint(v[i], g, p[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p[i];
+    }
+    uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool scale = FMT != 0 && !rotate;
-      const float a = scale ? v[2 * i] * g : v[2 * i], c = scale ? v[2 * i + 1] * g : v[2 * i + 1];
-      const bf16x2_t pk = {(__bf16)a, (__bf16)c};
+      const bf16x2_t pk = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
       h[i] = __builtin_bit_cast(uint32_t, pk);
-      if (scale) {
-        tie |= (as_u(a) & 0xFFFFu) == 0x8000u ? 1u : 0u;
-        tie |= (as_u(c) & 0xFFFFu) == 0x8000u ? 1u : 0u;
-      }
-    }
-    // v s g is rounded once: where an fp32 product sits on a bf16 midpoint
-    // the exact products decide (the rotated values are sums, rounded twice)
-    if (FMT != 0 && tie != 0u && !nan) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = bf16_of_product(v[2 * i], g) | (bf16_of_product(v[2 * i + 1], g) << 16);
     }
     __builtin_nontemporal_store(u32x4_t{h[0], h[1], h[2], h[3]},
                                 reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + o));
   }
 }
 
-template <int FMT, int OUT>
+template <int FMT, int OUT, int kReadSlots>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float rot_scale, FastDiv row_slots,
                                                            FastDiv heads, uint32_t nslots, int64_t first,
                                                            uint32_t steps) {
+  constexpr int kReadStep = kReadSlots * kThreads;
   const bool values = r.k_out == nullptr || blockIdx.y != 0;
   const bool rotate = r.rotate && !values;
   const uint8_t* cbase = values ? r.p.vc : r.p.kc;
@@ -281,7 +307,6 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float
   const float g = FMT == 0 ? 1.0f : *(values ? r.p.vg : r.p.kg);
   const int64_t holds = min((int64_t)r.table_cols * r.p.page.d, (int64_t)0x7FFFFFFF);
   const uint32_t begin = blockIdx.x * steps * kReadStep + threadIdx.x;
-  if (begin - threadIdx.x >= nslots) return;
 
   // Where slots of a step are: set by look() as far as the page number, by
   // codes() from there on.
@@ -294,14 +319,31 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float
   };
   Where where[kReadSlots];
   Bytes bytes[kReadSlots];
-  // the sequence of the slot looked at last: rows [row0, row1), token of row 0
-  int b = 0;
+  // the sequence of the slot looked at last: rows [row0, row1), which are its
+  // tokens from row0 + shift on
+  __shared__ int32_t s_cu[kAhead], s_start[kAhead];
+  const int b0 = sequence_of(r.cu, r.seqs,
+                             first + quotient(quotient(min(begin - threadIdx.x, nslots - 1), row_slots), heads));
+  {
+    const int i = min(b0 + (int)threadIdx.x, r.seqs);
+    s_cu[threadIdx.x] = r.cu[i];
+    s_start[threadIdx.x] = r.starts && i < r.seqs ? r.starts[i] : 0;
+  }
+  __syncthreads();
+  int b = b0;
   int64_t row0 = 0, row1 = 0, shift = 0;
   auto sequence = [&](int next) {
     b = next;
-    row0 = r.cu[b];
-    row1 = r.cu[b + 1];
-    shift = (r.starts ? r.starts[b] : 0) - row0;
+    const int i = b - b0;
+    if (i + 1 < kAhead) {
+      row0 = s_cu[i];
+      row1 = s_cu[i + 1];
+      shift = s_start[i] - row0;
+    } else {
+      row0 = r.cu[b];
+      row1 = r.cu[b + 1];
+      shift = (r.starts ? r.starts[b] : 0) - row0;
+    }
   };
   auto look = [&](uint32_t s0) {
 #pragma unroll
@@ -335,7 +377,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float
       }
     }
   };
-  sequence(sequence_of(r.cu, r.seqs, first + quotient(quotient(min(begin, nslots - 1), row_slots), heads)));
+  sequence(b0);
   look(begin);
   fetch();
   if (steps > 1) look(begin + kReadStep);
@@ -358,10 +400,8 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float
       p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(now[u].codes, sc, 1); v[2] = p.x; v[3] = p.y;
       p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(now[u].codes, sc, 2); v[4] = p.x; v[5] = p.y;
       p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(now[u].codes, sc, 3); v[6] = p.x; v[7] = p.y;
-      bool nan = false;
       if constexpr (FMT != 0) {
         const uint32_t e = now[u].scale & 0x7Fu;
-        nan = e == 0x7Fu;
         const float sd = e4m3_value_hw(e);        // (0x7F gives NaN)
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] *= sd;   // exact: 2 and 4 significant bits
@@ -374,15 +414,15 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadLaunch r, float
         fwht128_lanes(v, threadIdx.x & 15, rot_scale);
       }
       const uint32_t s = s0 + u * kThreads;
-      if (s < nslots) read_store<FMT, OUT>(v, rotate, g, nan, out, (first * heads.d * row_slots.d + s) * 8);
+      if (s < nslots) read_store<FMT, OUT>(v, rotate, g, out, (first * heads.d * row_slots.d + s) * 8);
     }
   }
 }
 
-template <int FMT>
-hipError_t launch_read_t(const KvReadLaunch& r, int64_t first, int64_t count, hipStream_t st) {
-  const uint32_t per = (uint32_t)r.head_dim / 8, nslots = (uint32_t)(count * r.p.heads * per);
-  const uint32_t planes = r.k_out && r.v_out ? 2 : 1;
+template <int FMT, int kReadSlots>
+hipError_t launch_read_n(const KvReadLaunch& r, int64_t first, uint32_t nslots, hipStream_t st) {
+  constexpr uint32_t kReadStep = kReadSlots * kThreads;
+  const uint32_t per = (uint32_t)r.head_dim / 8, planes = r.k_out && r.v_out ? 2 : 1;
   // at most 32 workgroups a CU (203 us for 0.9 GB of a batch's values, 209 with
   // 16, 226 with 8)
   const uint32_t all = (nslots + kReadStep - 1) / kReadStep, most = (uint32_t)device_cu_count() * 32 / planes;
@@ -390,12 +430,20 @@ hipError_t launch_read_t(const KvReadLaunch& r, int64_t first, int64_t count, hi
   const dim3 grid((all + steps - 1) / steps, planes);
   const float c = (float)(1.0 / sqrt(128.0));
   if (r.out_dtype == kF32)
-    hipLaunchKernelGGL((kv_read_kernel<FMT, kF32>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
+    hipLaunchKernelGGL((kv_read_kernel<FMT, kF32, kReadSlots>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
                        fast_div((uint32_t)r.p.heads), nslots, first, steps);
   else
-    hipLaunchKernelGGL((kv_read_kernel<FMT, kBF16>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
+    hipLaunchKernelGGL((kv_read_kernel<FMT, kBF16, kReadSlots>), grid, dim3(kThreads), 0, st, r, c, fast_div(per),
                        fast_div((uint32_t)r.p.heads), nslots, first, steps);
   return hipGetLastError();
+}
+
+template <int FMT>
+hipError_t launch_read_t(const KvReadLaunch& r, int64_t first, int64_t count, hipStream_t st) {
+  const uint32_t nslots = (uint32_t)(count * r.p.heads * (r.head_dim / 8));
+  // four slots a thread once that still leaves every CU a workgroup
+  if (nslots >= (uint32_t)device_cu_count() * 4 * kThreads) return launch_read_n<FMT, 4>(r, first, nslots, st);
+  return launch_read_n<FMT, 1>(r, first, nslots, st);
 }
 
 // Slots of one launch fit 31 bits; longer calls run as several launches.

@@ -12,8 +12,6 @@
 // in flight while one is worked on.  Bound by HBM.
 #pragma once
 
-#include <limits.h>
-
 #include "fp4q_kv_attend.h"
 
 namespace fp4q {
@@ -40,7 +38,7 @@ struct DecodeShape {
 
 template <int FMT, int D, int kTiles, int kQ, int kP, bool kWhole>
 __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd)) void kv_decode_kernel(
-    KvAttendLaunch a, int64_t numbers) {
+    KvAttendLaunch a, int numbers) {
   using Shape = DecodeShape<FMT, D, kTiles, kQ, kP>;
   using T = KvType<FMT>;
   using Lane = KvLane<FMT, D>;
@@ -50,7 +48,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   __shared__ uint32_t s_most[kRows];
   __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
   __shared__ int s_bad[kWaves];
-  __shared__ long long s_scan[kWaves + 4];
+  __shared__ int s_scan[kWaves + 6];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -148,8 +146,65 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
     return false;
   };
 
-  bool more = take(true);
-  while (more) {
+  // One unit a turn; it is finished in the next turn, when the next unit's loads
+  // are on their way.
+  KvUnit done = {};
+  int begins = 0, t_begin = 0, t_end = 0;
+  bool have = false, whole = false;
+  float* part = nullptr;
+  f32x4_t o[kTiles][D / 16];
+  float m[kTiles], l[kTiles];
+  bool bad = false;       // a value that is no finite number was left out
+  for (;;) {
+    const bool more = take(have ? kv_next<kRows, kGroupTokens, kGroupCost>(a, st) : true);
+    if (have) {
+      // join the four waves: maxima and sums of every row, then the values
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        l[t] += __shfl_xor(l[t], 16, 64);
+        l[t] += __shfl_xor(l[t], 32, 64);
+        if (g == 0) {
+          s_m[wave][16 * t + r] = m[t];
+          s_l[wave][16 * t + r] = l[t];
+        }
+      }
+      if (lane == 0) s_bad[wave] = bad;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        __syncthreads();
+        const float top = fmaxf(fmaxf(s_m[0][16 * t + r], s_m[1][16 * t + r]), fmaxf(s_m[2][16 * t + r], s_m[3][16 * t + r]));
+        const float f = __builtin_amdgcn_exp2f(m[t] - top);
+        float* dst = so + (wave * 16 + r) * Shape::kOStride + 4 * g;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) *reinterpret_cast<f32x4_t*>(dst + 16 * c) = o[t][c] * f;
+        __syncthreads();
+        for (int item = tid; item < 16 * (D / 4); item += kThreads) {
+          const int row = item / (D / 4), d = 4 * (item % (D / 4));
+          const int rr = 16 * t + row;
+          f32x4_t sum = *reinterpret_cast<const f32x4_t*>(so + row * Shape::kOStride + d);
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4_t*>(so + (w * 16 + row) * Shape::kOStride + d);
+          if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) {
+            if (kv_sees_nan<FMT, D>(a, done, done.row0 + rr, d, t_begin, t_end)) sum *= as_f(0x7FC00000u);
+          }
+          const float mx = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
+          float total = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) total += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mx);
+          if (whole) {
+            kv_finish4<FMT, D>(a, done, done.row0 + rr, d, sum, mx, total);
+          } else if (done.row0 + rr < done.m * a.group) {
+            put2(part + (int64_t)rr * D + d, sum.x, sum.y);
+            put2(part + (int64_t)rr * D + d + 2, sum.z, sum.w);
+            if (d == 0) put2(part + (int64_t)kRows * D + 2 * rr, mx, total);
+          }
+        }
+      }
+      __syncthreads();
+      if (!whole) kv_join<FMT, D, kRows, kGroupCost, kThreads, 8>(a, done, begins, st.shares, s_most);
+      __syncthreads();
+    }
+    if (!more) return;
     stage_queries<FMT, D, kQ, kRows>(a, kg, rows, sq, s_factor, s_most);
 
     u32x4_t qf[Shape::kQRegs ? kTiles : 1][Shape::kQRegs ? kQ : 1][Shape::kQRegs ? kChunks : 1];
@@ -172,8 +227,6 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
     int all_from, all_to;
     kv_all_see<kRows>(a, u, all_from, all_to);
 
-    f32x4_t o[kTiles][D / 16];
-    float m[kTiles], l[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       m[t] = kNoMax;
@@ -181,8 +234,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) o[t][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-
-    bool bad = false;       // a value that is no finite number was left out
+    bad = false;
     auto step = [&](int grp, Tile& in) {
       const int t0 = first + grp * kGroupTokens;
       const bool edge = t0 + 32 > all_to || t0 < all_from;
@@ -308,59 +360,13 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       if (grp + 1 < mine) step(grp + 1, odd);
     }
 
-    // the next unit's loads set out before this one is finished
-    const KvUnit done = u;
-    const int64_t begins = st.begins;
-    const bool whole = group == 0 && last == u.groups;
-    const int t_begin = u.lo + group * kGroupTokens, t_end = min(u.hi, u.lo + last * kGroupTokens);
-    float* part = kv_partial<D, kRows>(a, blockIdx.x, group == 0);
-    more = take(kv_next<kRows, kGroupTokens, kGroupCost>(a, st));
-
-    // join the four waves: maxima and sums of every row, then the values
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      l[t] += __shfl_xor(l[t], 16, 64);
-      l[t] += __shfl_xor(l[t], 32, 64);
-      if (g == 0) {
-        s_m[wave][16 * t + r] = m[t];
-        s_l[wave][16 * t + r] = l[t];
-      }
-    }
-    if (lane == 0) s_bad[wave] = bad;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      __syncthreads();
-      const float top = fmaxf(fmaxf(s_m[0][16 * t + r], s_m[1][16 * t + r]), fmaxf(s_m[2][16 * t + r], s_m[3][16 * t + r]));
-      const float f = __builtin_amdgcn_exp2f(m[t] - top);
-      float* dst = so + (wave * 16 + r) * Shape::kOStride + 4 * g;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) *reinterpret_cast<f32x4_t*>(dst + 16 * c) = o[t][c] * f;
-      __syncthreads();
-      for (int item = tid; item < 16 * (D / 4); item += kThreads) {
-        const int row = item / (D / 4), d = 4 * (item % (D / 4));
-        const int rr = 16 * t + row;
-        f32x4_t sum = *reinterpret_cast<const f32x4_t*>(so + row * Shape::kOStride + d);
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4_t*>(so + (w * 16 + row) * Shape::kOStride + d);
-        if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) {
-          if (kv_sees_nan<FMT, D>(a, done, done.row0 + rr, d, t_begin, t_end)) sum *= as_f(0x7FC00000u);
-        }
-        const float mx = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
-        float total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) total += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mx);
-        if (whole) {
-          kv_finish4<FMT, D>(a, done, done.row0 + rr, d, sum, mx, total);
-        } else if (done.row0 + rr < done.m * a.group) {
-          put2(part + (int64_t)rr * D + d, sum.x, sum.y);
-          put2(part + (int64_t)rr * D + d + 2, sum.z, sum.w);
-          if (d == 0) put2(part + (int64_t)kRows * D + 2 * rr, mx, total);
-        }
-      }
-    }
-    __syncthreads();
-    if (!whole) kv_join<FMT, D, kRows, kGroupCost, kThreads, 8>(a, done, begins, st.shares, s_most);
-    __syncthreads();
+    done = u;
+    begins = st.begins;
+    whole = group == 0 && last == u.groups;
+    t_begin = u.lo + group * kGroupTokens;
+    t_end = min(u.hi, u.lo + last * kGroupTokens);
+    part = kv_partial<D, kRows>(a, blockIdx.x, group == 0);
+    have = true;
   }
 }
 
@@ -368,17 +374,15 @@ template <int FMT, int D, int kTiles, int kQ, int kP>
 hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   constexpr int kRows = 16 * kTiles;
   KvAttendLaunch b = a;
-  const int64_t numbers = kv_block_numbers<kRows>(b);
-  const int64_t groups = (a.most_tokens + kGroupTokens - 1) / kGroupTokens;
-  const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kGroupCost);
+  const int64_t numbers = kv_block_numbers(b, kRows);
+  const int64_t most = kv_most_groups(b, numbers, kGroupTokens, kGroupCost);
   const int64_t resident = (int64_t)cus * DecodeShape<FMT, D, kTiles, kQ, kP>::kWavesPerSimd;
   const int grid = (int)min(min(most, resident), (int64_t)kMostWorkgroups);
-  b.thirds = resident;
-  b.few_groups = most < INT_MAX;
+  b.thirds = (uint32_t)resident;
   if (a.p.page.d % 32 == 0)
-    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, true>), dim3(grid), dim3(kThreads), 0, st, b, numbers);
+    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, true>), dim3(grid), dim3(kThreads), 0, st, b, (int)numbers);
   else
-    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, false>), dim3(grid), dim3(kThreads), 0, st, b, numbers);
+    hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, false>), dim3(grid), dim3(kThreads), 0, st, b, (int)numbers);
   return hipGetLastError();
 }
 

@@ -10,8 +10,6 @@
 // operand, the left one being the values read transposed.
 #pragma once
 
-#include <limits.h>
-
 #include "fp4q_kv_attend.h"
 
 namespace fp4q {
@@ -102,14 +100,14 @@ __device__ __forceinline__ float wave_queries(const KvAttendLaunch& a, const KvU
 
 template <int FMT, int D, int kW, int kQ, int kP>
 __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesPerSimd)) void kv_prefill_kernel(
-    KvAttendLaunch a, int64_t numbers) {
+    KvAttendLaunch a, int numbers) {
   using Shape = PrefillShape<FMT, D, kW, kQ, kP>;
   using T = KvType<FMT>;
   using Lane = KvLane<FMT, D>;
   constexpr int kRows = Shape::kRows;
   constexpr int kTasks = 8 / kW;       // 16 tokens' keys or values a task: 8 in a step
   __shared__ __align__(16) uint16_t s_kv[2 * Shape::kHalf];
-  __shared__ long long s_scan[kW + 4];
+  __shared__ int s_scan[kW + 6];
   __shared__ int s_bad;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -340,16 +338,14 @@ hipError_t launch_prefill_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   using Shape = PrefillShape<FMT, D, kW, kQ, kP>;
   constexpr int kRows = Shape::kRows;
   KvAttendLaunch b = a;
-  const int64_t numbers = kv_block_numbers<kRows>(b);
-  const int64_t groups = (a.most_tokens + kStepTokens - 1) / kStepTokens;
-  const int64_t most = numbers * a.p.heads * ((groups < 1 ? 1 : groups) + kStepCost);
+  const int64_t numbers = kv_block_numbers(b, kRows);
+  const int64_t most = kv_most_groups(b, numbers, kStepTokens, kStepCost);
   const int64_t resident = (int64_t)cus * (4 * Shape::kWavesPerSimd / kW);
   const int grid = (int)min(min(most, resident), (int64_t)kMostWorkgroups);
-  b.few_groups = most < INT_MAX;
-  hipLaunchKernelGGL((kv_prefill_kernel<FMT, D, kW, kQ, kP>), dim3(grid), dim3(64 * kW), 0, st, b, numbers);
+  hipLaunchKernelGGL((kv_prefill_kernel<FMT, D, kW, kQ, kP>), dim3(grid), dim3(64 * kW), 0, st, b, (int)numbers);
   const hipError_t e = hipGetLastError();
   // (a unit of one step is never shared)
-  if (e != hipSuccess || groups <= 1) return e;
+  if (e != hipSuccess || a.most_tokens <= kStepTokens) return e;
   const int64_t rows = min((int64_t)kRows, (int64_t)a.max_q * a.group);
   hipLaunchKernelGGL((kv_join_kernel<FMT, D, kRows>), dim3(grid, (uint32_t)((rows * (D / 4) + kThreads - 1) / kThreads)),
                      dim3(kThreads), 0, st, a, grid);
