@@ -207,18 +207,45 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
       const int t0 = u.lo + grp * kStepTokens;
       if (t0 >= n) break;                       // (a unit without tokens)
       if (rows && t0 < wu.hi && t0 + kStepTokens > wu.lo) {
+        // LDS reads set out a stage before the products that take them, and the
+        // scheduler may not move them back: left alone it puts each right
+        // before its product, which then waits for it.
         const uint16_t* ks = s_kv + (grp & 1) * Shape::kHalf + col * Shape::kKStride + 8 * half;
-        f32x16_t s[2];
+        const uint16_t* vs = s_kv + (grp & 1) * Shape::kHalf + kStepTokens * Shape::kKStride +
+                             (4 * half + (r >> 2)) * Shape::kVStride + 16 * (g & 1) + 4 * (r & 3);
+        constexpr int kStage = D / 16 < 8 ? D / 16 : 8, kStages = 2 * (D / 16) / kStage;   // key fragments
+        u32x4_t kf[2][kStage];
+        auto read_keys = [&](int stage) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          s[x] = f32x16_t{};
+          for (int i = 0; i < kStage; ++i) {
+            const int f = stage * kStage + i, x = f & 1, c = f >> 1;
+            kf[stage & 1][i] = *reinterpret_cast<const u32x4_t*>(ks + 32 * x * Shape::kKStride + 16 * c);
+          }
+        };
+        u32x4_t vf[2][D / 32];
+        auto read_values = [&](int k) {
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(ks + 32 * x * Shape::kKStride + 16 * c);
+          for (int c = 0; c < D / 32; ++c) {
+            const u32x2_t x0 = read_transposed(vs + 16 * k * Shape::kVStride + 32 * c);
+            const u32x2_t x1 = read_transposed(vs + (16 * k + 8) * Shape::kVStride + 32 * c);
+            vf[k & 1][c] = u32x4_t{x0.x, x0.y, x1.x, x1.y};
+          }
+        };
+        f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
+        read_keys(0);
 #pragma unroll
-            for (int q = 0; q < kQ; ++q) s[x] = T::mfma32(kf, qf[q][c], s[x]);
+        for (int stage = 0; stage < kStages; ++stage) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (stage + 1 < kStages) read_keys(stage + 1);
+          else read_values(0);
+#pragma unroll
+          for (int i = 0; i < kStage; ++i) {
+            const int f = stage * kStage + i, x = f & 1, c = f >> 1;
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) s[x] = T::mfma32(kf[stage & 1][i], qf[q][c], s[x]);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
         // token 32 x + 8 (i / 4) + 4 half + i % 4 of the step
         float y[32];
 #pragma unroll
@@ -258,18 +285,16 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
           for (int q = 0; q < kP; ++q) w[k][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
         }
         // weighted values: element 32 c + 8 (i / 4) + 4 half + i % 4 of the row
-        const uint16_t* vs = s_kv + (grp & 1) * Shape::kHalf + kStepTokens * Shape::kKStride +
-                             (4 * half + (r >> 2)) * Shape::kVStride + 16 * (g & 1) + 4 * (r & 3);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
+        for (int k = 0; k < 4; ++k) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (k + 1 < 4) read_values(k + 1);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const u32x2_t x0 = read_transposed(vs + 16 * k * Shape::kVStride + 32 * c);
-            const u32x2_t x1 = read_transposed(vs + (16 * k + 8) * Shape::kVStride + 32 * c);
-            const u32x4_t vf = {x0.x, x0.y, x1.x, x1.y};
+          for (int q = 0; q < kP; ++q)
 #pragma unroll
-            for (int q = 0; q < kP; ++q) o[c] = T::mfma32(vf, w[k][q], o[c]);
-          }
+            for (int c = 0; c < D / 32; ++c) o[c] = T::mfma32(vf[k & 1][c], w[k][q], o[c]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (grp + 1 < last) {
         put(grp + 1);
