@@ -199,8 +199,10 @@ def kv_cache_read(cache, page_table, cu, *, total, starts=None, rotation=None, o
 
 
 # One zeroed workspace per (device, stream), grown as calls need it: calls on
-# one stream are ordered, and a call leaves its counters zero.
+# one stream are ordered, and a call leaves its counters zero.  Smaller ones
+# are kept too, since captured calls go on using them.
 _workspaces = {}
+_outgrown = []
 
 
 def _grow_workspace(cache, a, stream):
@@ -208,6 +210,9 @@ def _grow_workspace(cache, a, stream):
         raise RuntimeError("fp4q: the workspace of this stream is missing or too small; pass workspace= or make one "
                            "call of this size on the stream before capturing it")
     need = _lib.load().fp4q_kv_attention_workspace_bytes(cache._args, a)
+    old = _workspaces.get((cache._index, stream))
+    if old is not None:
+        _outgrown.append(old)
     ws = _workspaces[(cache._index, stream)] = torch.zeros(need, dtype=torch.uint8, device=cache.device)
     return ws
 

@@ -308,13 +308,20 @@ __device__ __forceinline__ int kv_block_number(const KvAttendLaunch& a, int b) {
   return (int)((uint32_t)(kv_first_query(a, b) * a.group) / kRows) + b;
 }
 
+// Blocks of a sequence of m queries; of more than max_q the blocks past those
+// are left out, so that all ways of counting agree whatever cu_q holds.
+template <int kRows>
+__device__ __forceinline__ int kv_blocks(const KvAttendLaunch& a, int m) {
+  return (int)(((uint32_t)(min(max(m, 0), a.max_q) * a.group) + kRows - 1) / kRows);
+}
+
 template <int kRows, bool kUniform = false>
 __device__ __forceinline__ void kv_sequence(const KvAttendLaunch& a, int b, KvUnit& u) {
   u.b = b;
   u.q0 = kv_first_query<kUniform>(a, b);
   u.m = kv_first_query<kUniform>(a, b + 1) - u.q0;
   u.n = min(max(kUniform ? scalar(a.lens + b) : a.lens[b], 0), (int)a.most_tokens);
-  u.blocks = u.m > 0 ? (int)(((uint32_t)(u.m * a.group) + kRows - 1) / kRows) : 0;
+  u.blocks = kv_blocks<kRows>(a, u.m);
 }
 
 // Queries of the first and last of rows row0 .. row0 + kRows - 1.
@@ -489,7 +496,7 @@ __device__ __forceinline__ bool kv_stretch(const KvAttendLaunch& a, int numbers,
   st.u.q0 = found[2];
   st.u.m = found[3];
   st.u.n = found[4];
-  st.u.blocks = (int)(((uint32_t)(st.u.m * a.group) + kRows - 1) / kRows);
+  st.u.blocks = kv_blocks<kRows>(a, st.u.m);
   kv_block<kRows, kTokens>(a, found[1], st.u);
   const int counted = st.u.groups + kCost;
   st.u.head = found[5] / counted;
@@ -633,8 +640,10 @@ __device__ __forceinline__ void widen_q8(const KvAttendLaunch& a, const RawQ& q,
 // A workgroup's ROWS query rows on their way into LDS: its threads' parts of
 // them as they were loaded, and then as kQ pieces in rows of D + 8 halves,
 // pieces ROWS rows apart, with each row's factor from raw score to exponent of
-// two in factor[].  The factors are not negative: a negative scale goes into
-// the queries' signs.
+// two in factor[].  The factors are positive, so that masked scores stay minus
+// infinity: a negative scale goes into the queries' signs, and a product of
+// zero (a scale of 0; a row of zeros with a small tensor scale) becomes kLeast.
+constexpr float kLeast = 0x1p-126f;
 template <int D, int ROWS>
 struct QueryRows {
   static constexpr int kPer = D / 8, kItems = ROWS * kPer;
@@ -679,7 +688,7 @@ __device__ __forceinline__ void stage_queries(const KvAttendLaunch& a, float kg,
   for (int i = tid; i < ROWS; i += kThreads) {
     float f = base;
     if constexpr (kv_scaled_rows<FMT, kQ>()) f *= as_f((min(max(most[i] >> 23, 9u), 254u) - 8u) << 23);
-    factor[i] = f;
+    factor[i] = larger(f, kLeast);
   }
 #pragma unroll
   for (int k = 0; k < Q::kEach; ++k) {

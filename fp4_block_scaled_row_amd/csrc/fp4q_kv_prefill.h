@@ -95,7 +95,7 @@ __device__ __forceinline__ float wave_queries(const KvAttendLaunch& a, const KvU
 #pragma unroll
     for (int q = 0; q < kQ; ++q) qf[q][c] = u32x4_t{w[0][q], w[1][q], w[2][q], w[3][q]};
   }
-  return factor;
+  return larger(factor, kLeast);
 }
 
 template <int FMT, int D, int kW, int kQ, int kP>
@@ -284,7 +284,11 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
 #pragma unroll
           for (int q = 0; q < kP; ++q) w[k][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
         }
-        // weighted values: element 32 c + 8 (i / 4) + 4 half + i % 4 of the row
+        // weighted values: element 32 c + 8 (i / 4) + 4 half + i % 4 of the row.
+        // Of a SIMD's two waves the one that is at these goes first: its
+        // products fill the other's exponentials (4 x 1000 queries of 40 heads
+        // over to 16000 tokens 775-779 us with this priority, 783-786 without).
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           __builtin_amdgcn_sched_barrier(0);
@@ -295,6 +299,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
             for (int c = 0; c < D / 32; ++c) o[c] = T::mfma32(vf[k & 1][c], w[k][q], o[c]);
         }
         __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(0);
       }
       if (grp + 1 < last) {
         put(grp + 1);
