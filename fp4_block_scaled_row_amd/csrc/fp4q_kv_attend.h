@@ -20,8 +20,9 @@
 // are scaled by a power of two per row that puts the row's largest value in
 // [2^8, 2^9).  The softmax weights enter in kP pieces: one (2^-12 in fp16,
 // 2^-9 in bf16 relative to the weight, below the bf16 output's own rounding)
-// for bf16 outputs, two for fp32 outputs.  Scores, maxima, weights' sums and
-// outputs are held in fp32.
+// for bf16 outputs; for fp32 outputs two in fp16 and three in bf16, whose
+// 16 bits in two left an output's error at 2e-6 of it, twice that of the sum
+// in fp32.  Scores, maxima, weights' sums and outputs are held in fp32.
 //
 // Layout in the matrix instructions.  Scores are formed transposed, keys as
 // the left operand and queries as the right one, so that a lane ends up with

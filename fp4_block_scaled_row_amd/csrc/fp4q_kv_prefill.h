@@ -386,7 +386,7 @@ hipError_t launch_prefill_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
 // and where sequences have at most 128 rows.
 template <int D, int FMT>
 hipError_t launch_prefill_d(const KvAttendLaunch& a, int waves, int cus, hipStream_t st) {
-  if (a.dtype == kF32) return launch_prefill_t<FMT, D, 4, FMT == 1 ? 2 : 3, 2>(a, cus, st);
+  if (a.dtype == kF32) return launch_prefill_t<FMT, D, 4, FMT == 1 ? 2 : 3, FMT == 1 ? 2 : 3>(a, cus, st);
   if constexpr (D <= 128) {
     if (waves == 8) {
       if (kv_rotated_pieces<FMT>(a) == 2) return launch_prefill_t<FMT, D, 8, 2, 1>(a, cus, st);
