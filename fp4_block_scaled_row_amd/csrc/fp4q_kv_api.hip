@@ -5,6 +5,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "fp4q.h"
 #include "fp4q_internal.h"
 #include "fp4q_kv_attend.h"
@@ -118,17 +120,34 @@ fp4q_status check_attention(const fp4q_kv_cache* cache, const fp4q_kv_attention_
   return FP4Q_OK;
 }
 
-// Which kernels: the few-row ones up to 16 query rows of a cache head, up to
-// 32 where those fit their registers (bf16, head_dim to 128); above that the
-// many-row ones, with 32 rows a wave.
+// Which kernels.  The few-row ones take 16 query rows of a cache head in a
+// block (32 where those fit the registers: bf16, head_dim to 128) and read the
+// cache once a block; the many-row ones 32 rows a wave, and turn codes into
+// numbers once for 128 or 256 rows, but need many blocks and long stretches to
+// earn their longer beginning, and a second kernel.  So it goes by the rows and
+// by length: `shorter` with at most 2^16 tokens to pass over in all (sequences x cache heads x
+// tokens of one, as far as the host knows).  Measured, bf16, head_dim 128, NVFP4,
+// 16-row blocks / 32-row blocks / many-row, us:
+//   sequences x heads x tokens    rows 32          rows 64          rows 128
+//         1 x 1 x 2000            16 / 22 / 16     16 / 23 / 17     16 /  - / 18
+//        16 x 1 x 4000            25 / 29 / 30     28 / 32 / 32     30 /  - / 37
+//        16 x 8 x 1000            25 / 27 / 31     31 / 30 / 31     43 /  - / 39
+//        16 x 8 x 8000            60 / 54 / 80    102 / 85 / 84    183 /  - / 99
+// head_dim 64 alike.  With head_dim 256 and fp32 the many-row ones have one wave
+// a SIMD: 16 x 8 x 8000 with 64 rows takes 164 / - / 204 at head_dim 256 and
+// 105 / - / 182 in fp32 at 128.  With head_dim 96, whose codes are loaded 4
+// bytes at a time, further reads cost more: 47 / 34 / 31 at 16 x 8 x 1000 and 64
+// rows, 17 / 22 / 16 at 1 x 1 x 2000.
 struct Plan {
   bool prefill;
   int tiles, waves;
 };
 Plan attend_plan(const KvAttendLaunch& a) {
   const int64_t rows = (int64_t)a.max_q * a.group;
+  const int64_t tokens = a.window > 0 ? std::min(a.most_tokens, (int64_t)a.window + a.max_q) : a.most_tokens;
+  const bool shorter = tokens * a.seqs * a.p.heads <= 1 << 16;
   const bool wide = a.dtype == kBF16 && a.head_dim <= 128;
-  Plan p = {rows > (wide ? 32 : 16), rows <= 16 ? 1 : 2, 4};
+  Plan p = {rows > (a.head_dim == 96 ? 32 : shorter ? 128 : 64), wide && rows > 16 && !shorter ? 2 : 1, 4};
   if (rows > 128 && wide) p.waves = 8;
   return p;
 }

@@ -33,7 +33,8 @@ struct DecodeShape {
   static constexpr int kMax1 = kVBytes > kOBytes ? kVBytes : kOBytes;
   static constexpr int kMain = kQRegs && kQBytes > kMax1 ? kQBytes : kMax1;
   static constexpr int kShared = kMain + (kQRegs ? 0 : kQBytes);
-  static constexpr int kWavesPerSimd = D > 128 ? 1 : (kTiles == 2 || kQ > 1 ? 2 : 3);
+  // as many as the registers allow (head_dim 256 by a hair, up to 9 spilled)
+  static constexpr int kWavesPerSimd = D > 128 ? (kQ > 1 || kP > 1 ? 1 : 2) : (kTiles == 2 || kQ > 1 ? 2 : 3);
 };
 
 template <int FMT, int D, int kTiles, int kQ, int kP, bool kWhole>
