@@ -545,20 +545,22 @@ inline int64_t kv_most_groups(const KvAttendLaunch& a, int64_t numbers, int toke
 // stretch the partial result of the unit it shares with its neighbours: kRows x
 // D weighted values, then each row's maximum and sum.  Units that several
 // workgroups share are joined
-//   - few rows: by whichever of them finishes last, found by counting arrivals
-//     in the record of the workgroup where the unit begins; it clears the
-//     counter again, so that all are zero between calls.  Saves a launch.
+//   - few rows: by whichever of a few neighbours finishes last, found by
+//     counting arrivals in the record of the first of them, then by the last of
+//     a few of those, and so on; each clears its counter again, so that all are
+//     zero between calls.  Saves a launch.
 //   - many rows: by a second kernel with many more workgroups, since one would
 //     take too long over them (a call of 16 units of 64 rows x 256 in 16 pieces
 //     each took 93 us that way, 45 with a second kernel).  The records then
 //     also say which units are shared.
 constexpr int kMostWorkgroups = 1024;      // of a launch
 struct KvShared {
-  uint32_t arrived;
+  uint32_t arrived[5];      // pieces of the unit that begins in the stretch, by level (see kv_join)
+  uint32_t arrived_in[5];   // pieces of a unit that began earlier
   int32_t first;     // 1: the stretch begins with a piece of an earlier unit, 2: with its last one
   int32_t last;      // 1: it ends with the first piece of a unit, sequence b, rows row0 on of `head`
   int32_t b, head, row0;
-  int32_t unused[10];     // (64 bytes: each record in a cache line of its own)
+  int32_t unused[1];      // (64 bytes: each record in a cache line of its own)
 };
 __device__ __forceinline__ KvShared* kv_shared(const KvAttendLaunch& a, int64_t workgroup) {
   return reinterpret_cast<KvShared*>(a.ws) + workgroup;
@@ -775,58 +777,95 @@ __device__ __forceinline__ void kv_finish4(const KvAttendLaunch& a, const KvUnit
 }
 
 // After a workgroup has stored its piece of a shared unit: counts it, and where
-// it is the last one joins the pieces into the output.  kBatch pieces' loads
-// are in flight together.  Every thread of the workgroup calls it; `word`: LDS.
+// it is the last one joins the pieces: kBatch neighbours, their loads in flight
+// together, whose sum is a piece of the next level, until at most 2 kBatch are
+// left, which give the output.  A workgroup reads only about 30 GB/s here; in one
+// level a unit of 16 rows x 128 took 0.27 us a piece.  With levels of 4 a call
+// over 1 x 30000 tokens went from 74 us to 21, one over 2 x 131071 from 75 to 67.5
+// (of 8, with more registers in use: 69 and 71).  Every thread of the workgroup
+// calls it; `word`, `tops`, `totals`: LDS (a word, kRows, kRows).
 template <int FMT, int D, int kRows, int kCost, int kThreadsWg, int kBatch>
 __device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u, int begins, const KvShares& shares,
-                                        unsigned int* word) {
+                                        unsigned int* word, float* tops, float* totals) {
+  constexpr uint32_t kPiece = kRows * (D + 2) * sizeof(float);
   // its first real group and its last one say which workgroups have pieces
   const int w0 = (int)kv_owner(shares, (uint32_t)(begins + kCost));
   const int w1 = (int)kv_owner(shares, (uint32_t)(begins + kCost + u.groups - 1));
-  const int pieces = w1 - w0 + 1;
-  __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t* counter = &kv_shared(a, w0)->arrived;
-    const unsigned int arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
-    if (arrived == (unsigned int)pieces) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *word = arrived;
-  }
-  __syncthreads();
-  if (*word != (unsigned int)pieces) return;
   const int rows = min(kRows, u.m * a.group - u.row0);
-  for (int item = threadIdx.x; item < rows * (D / 4); item += kThreadsWg) {
-    const int rr = item / (D / 4), d = 4 * (item % (D / 4));
-    f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    float top = kNoMax, total = 0.0f;
-    for (int p = 0; p < pieces; p += kBatch) {
-      f32x4_t v[kBatch];
-      float m[kBatch], l[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int q = min(p + i, pieces - 1);
-        const float* part = kv_partial<D, kRows>(a, w0 + q, q == 0);
-        const float2_t x = get2(part + (int64_t)rr * D + d), y = get2(part + (int64_t)rr * D + d + 2);
-        const float2_t ml = get2(part + (int64_t)kRows * D + 2 * rr);
-        v[i] = f32x4_t{x.x, x.y, y.x, y.y};
-        m[i] = p + i < pieces ? ml.x : kNoMax;
-        l[i] = ml.y;
+  // (a level's pieces lie where the first of theirs of the first level lies)
+  int pieces = w1 - w0 + 1, mine = (int)blockIdx.x - w0, stride = 1;
+#pragma unroll 1
+  for (int level = 0;; ++level) {
+    const bool final = pieces <= 2 * kBatch;
+    const int base = final ? 0 : mine / kBatch * kBatch, here = final ? pieces : min(kBatch, pieces - base);
+    if (here > 1) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        KvShared* record = kv_shared(a, w0 + base * stride);
+        uint32_t* counter = base == 0 ? &record->arrived[level] : &record->arrived_in[level];
+        const unsigned int arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+        if (arrived == (unsigned int)here) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *word = arrived;
       }
-      float most = top;
+      __syncthreads();
+      if (*word != (unsigned int)here) return;
+      // (one scalar address and 32-bit offsets, for the sake of registers)
+      const uint8_t* const from = reinterpret_cast<const uint8_t*>(kv_partial<D, kRows>(a, 0, false));
+      const uint32_t first = (uint32_t)(2 * (w0 + base * stride) + (base == 0)) * kPiece;
+      const uint32_t second = (uint32_t)(2 * (w0 + (base + 1) * stride)) * kPiece - first;
+#pragma unroll 1
+      for (int item = threadIdx.x; item < rows * (D / 4); item += kThreadsWg) {
+        const int rr = item / (D / 4), d = 4 * (item % (D / 4));
+        const uint32_t at = 4 * (rr * D + d), at_ml = 4 * (kRows * D + 2 * rr);
+        f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        float top = kNoMax, total = 0.0f;
+        uint32_t piece = first;
+#pragma unroll 1
+        for (int p = 0; p < here; p += kBatch) {
+          float2_t x[kBatch], y[kBatch], ml[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) most = fmaxf(most, m[i]);
-      const float f = __builtin_amdgcn_exp2f(top - most);
-      top = most;
-      sum *= f;
-      total *= f;
+          for (int i = 0; i < kBatch; ++i) {
+            x[i] = get2(reinterpret_cast<const float*>(from + (piece + at)));
+            y[i] = get2(reinterpret_cast<const float*>(from + (piece + at) + 8));
+            ml[i] = get2(reinterpret_cast<const float*>(from + (piece + at_ml)));
+            if (p + i + 1 < here) piece += p + i == 0 ? second : 2 * kPiece * stride;
+          }
+          float most = top;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const float e = p + i < pieces ? __builtin_amdgcn_exp2f(m[i] - top) : 0.0f;
-        sum += v[i] * e;
-        total += l[i] * e;
+          for (int i = 0; i < kBatch; ++i) most = fmaxf(most, ml[i].x);
+          const float f = __builtin_amdgcn_exp2f(top - most);
+          top = most;
+          sum *= f;
+          total *= f;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const float e = p + i < here ? __builtin_amdgcn_exp2f(ml[i].x - top) : 0.0f;
+            sum += f32x4_t{x[i].x, x[i].y, y[i].x, y[i].y} * e;
+            total += ml[i].y * e;
+          }
+        }
+        if (final) {
+          kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, top, total);
+        } else {
+          float* part = kv_partial<D, kRows>(a, w0 + base * stride, base == 0) + rr * D + d;
+          put2(part, sum.x, sum.y);
+          put2(part + 2, sum.z, sum.w);
+          if (d == 0) {
+            tops[rr] = top;
+            totals[rr] = total;
+          }
+        }
       }
+      if (final) return;
+      __syncthreads();      // (the maxima and sums have been read by all)
+      if ((int)threadIdx.x < rows)
+        put2(kv_partial<D, kRows>(a, w0 + base * stride, base == 0) + (int64_t)kRows * D + 2 * threadIdx.x,
+             tops[threadIdx.x], totals[threadIdx.x]);
     }
-    kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, top, total);
+    mine /= kBatch;
+    pieces = (pieces + kBatch - 1) / kBatch;
+    stride *= kBatch;
   }
 }
 
