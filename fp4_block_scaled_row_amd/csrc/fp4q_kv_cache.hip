@@ -126,6 +126,10 @@ __device__ __forceinline__ uint32_t mx_encode_block(const float v[8], uint32_t a
 }
 
 // A thread takes kSlots slots, a workgroup's width apart (all loads first).
+// Large calls: 6760 tokens of 8 heads x 128, bf16, keys rotated, NVFP4, 35 MB in
+// 19 us, 1.9 TB/s, about a third of it the vector instructions and the rest the
+// one round of loads, work and stores that a thread has; addresses held in
+// scalars, and 1, 2 or 8 slots, were no faster.  Small ones by latency, 3 us.
 template <int FMT, int IN, int kSlots>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteLaunch w, float rot_scale, FastDiv row_slots,
                                                             FastDiv heads, uint32_t nslots) {
@@ -241,7 +245,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int64_t t) 
 // run of slots kReadSlots a thread at a time, with the codes of the next step
 // and the page numbers of the one after in flight; it finds its first row's
 // sequence once and goes on from there, the next kAhead sequences' bounds being
-// in LDS.  Bound by the stores.
+// in LDS.  Bound by the stores: 16 sequences of up to 16384 tokens, 8 heads x 128,
+// 932 MB in 195 us, 4.8 TB/s (a large copy reaches 5.1).
 constexpr int kAhead = kThreads;
 
 // p = RN(v g) moved by its last bit towards the exact product where it is a bf16

@@ -270,11 +270,12 @@ fp4q_status fp4q_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *a_co
  * keys and values share theirs.  Format FP4Q_NVFP4 (16-blocks, E4M3 scales,
  * k_global and v_global: device pointers to the tensor scales g, positive and
  * finite) or FP4Q_MXFP4 (32-blocks, E8M0 scales); IF4 is UNSUPPORTED.
- * head_dim: a multiple of 32 up to 1024; page_size: any.  Code planes and
- * code strides are 16-byte aligned, scale planes and strides to the scale
- * bytes of a quarter row where head_dim is a multiple of 128 (else
+ * head_dim: a multiple of 32 up to 1024; page_size: any; num_pages: 1 to
+ * 2^31 - 1; kv_heads: to 4096.  Code planes and code strides are 16-byte
+ * aligned, scale planes and strides to the scale bytes of a quarter row where
+ * head_dim is a multiple of 128, strides are below 2^31 bytes (else
  * FP4Q_ERR_UNSUPPORTED).  A dense [pages][heads][tokens] or
- * [pages][tokens][heads] cache is.
+ * [pages][tokens][heads] cache is all that; planes may pass 4 GiB.
  *
  * Token t of sequence b lies in page page_table[b * table_stride + t /
  * page_size] at offset t % page_size.  A page id outside [0, num_pages) is
@@ -345,7 +346,7 @@ typedef struct {
   int64_t total_q;
   int32_t table_cols;
   int32_t seqs;
-  int32_t max_q;               /* most queries of a sequence, at least (0 or 1 without cu_q) */
+  int32_t max_q;               /* no sequence has more queries (0 or 1 without cu_q); rows past it are left out */
   int32_t q_heads;             /* a multiple of kv_heads: head h reads cache head h / (q_heads / kv_heads) */
   int32_t dtype;               /* FP4Q_F32 or FP4Q_BF16, of q and out */
   int32_t causal;              /* query i of m sees token j <= n - m + i of n; 0: every token */
@@ -369,7 +370,14 @@ size_t fp4q_kv_attention_workspace_bytes(const fp4q_kv_cache *cache, const fp4q_
  * exactly; sums, maxima and outputs are fp32, rounded once.  A query that
  * sees no token, or only scores of minus infinity, gives zeros and a
  * log-sum-exp of minus infinity.  Tokens that a query does not see never
- * reach it, whatever their bytes stand for.  At most 65535 sequences. */
+ * reach it, whatever their bytes stand for; a NaN block of one that it sees
+ * makes a key's row NaN, a value's elements of it.  (An MXFP4 scale byte of
+ * 253 or 254, which fp4q_kv_write does not produce and whose values pass
+ * bf16's range, may count as NaN.)  Sums are taken in an order that the shapes
+ * and lengths fix: a call gives the same bits each time.  At most 65535
+ * sequences, and fewer than 2^31 pieces of work, a piece being 64 tokens for a
+ * block of 16 or more query rows of a cache head (else UNSUPPORTED; table_cols
+ * and max_q count here, not the lengths). */
 fp4q_status fp4q_kv_attention(const fp4q_kv_cache *cache, const fp4q_kv_attention_args *args, void *workspace,
                               size_t workspace_bytes, void *hip_stream);
 

@@ -236,6 +236,21 @@ def test_max_q_is_a_bound(fq, fmt, max_q):  # noqa: F811
         assert np.max(np.abs(out[i:j] - want), initial=0.0) <= 2.0 ** -14 * np.abs(v).max()
 
 
+@pytest.mark.parametrize("fmt,dim,rotate", [("nvfp4", 64, False), ("mxfp4", 96, False), ("nvfp4", 128, True),
+                                            ("mxfp4", 128, True), ("mxfp4", 128, False), ("nvfp4", 256, True),
+                                            ("mxfp4", 256, True), ("nvfp4", 256, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("queries", [3, 8, 11, 16, 27, 32, 50])
+@pytest.mark.parametrize("listed", [0, 140000])
+def test_rows_and_listed_tokens(fq, fmt, dim, rotate, dtype, queries, listed):  # noqa: F811
+    """4 rows a query, few of them to many, and tables that list no more pages than are needed or a long context's:
+    what the choice of kernels goes by."""
+    lens, page = [333, 5, 77], 32
+    case = Case(fq, fmt, dim, 1, lens, page, seed=queries)
+    case.table = np.concatenate([case.table, np.full((3, listed // page), -1, dtype=np.int32)], axis=1)
+    check_attention(case, [queries, min(queries, 2), queries - 1], 4, dtype, rotate=rotate)
+
+
 def test_workspace_serves_any_calls(fq):  # noqa: F811
     """One workspace for calls of both kinds and all sizes, one with more queries than it says among them: each
     result is that with a fresh workspace, and the counters are zero after each."""
