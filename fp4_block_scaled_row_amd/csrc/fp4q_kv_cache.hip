@@ -127,9 +127,10 @@ __device__ __forceinline__ uint32_t mx_encode_block(const float v[8], uint32_t a
 
 // A thread takes kSlots slots, a workgroup's width apart (all loads first).
 // Large calls: 6760 tokens of 8 heads x 128, bf16, keys rotated, NVFP4, 35 MB in
-// 19 us, 1.9 TB/s, about a third of it the vector instructions and the rest the
-// one round of loads, work and stores that a thread has; addresses held in
-// scalars, and 1, 2 or 8 slots, were no faster.  Small ones by latency, 3 us.
+// 19 us, 1.9 TB/s: 178 vector instructions a slot, 8 us of issue, after loads and
+// stores of 7, hardly overlapped (without the encoding 10 us).  Addresses held in
+// scalars, 1, 2 or 8 slots, and workgroups that go on with the next loads in
+// flight were no faster.  Small ones by latency, 3 us.
 template <int FMT, int IN, int kSlots>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteLaunch w, float rot_scale, FastDiv row_slots,
                                                             FastDiv heads, uint32_t nslots) {
