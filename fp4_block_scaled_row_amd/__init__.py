@@ -25,11 +25,13 @@ import torch
 
 from . import _lib
 from ._lib import Fp4qError, load  # noqa: F401
-from ._kv import KvCache, kv_cache, kv_cache_attention, kv_cache_read, kv_cache_write
+from ._kv import (KvCache, kv_cache, kv_cache_attention, kv_cache_attention_workspace_bytes, kv_cache_read,
+                  kv_cache_write)
 
 __all__ = [
     "quantize_mxfp4", "quantize_nvfp4", "silu_mul_fwht_mxfp4", "fwht", "dequantize", "mxfp4_gemm",
     "KvCache", "kv_cache", "kv_cache_write", "kv_cache_read", "kv_cache_attention",
+    "kv_cache_attention_workspace_bytes",
     "workspace_bytes",
     "check_counters", "version", "MxResult", "NvResult", "Fp4qError",
 ]

@@ -13,7 +13,8 @@ import torch
 
 from . import _lib
 
-__all__ = ["KvCache", "kv_cache", "kv_cache_write", "kv_cache_read", "kv_cache_attention"]
+__all__ = ["KvCache", "kv_cache", "kv_cache_write", "kv_cache_read", "kv_cache_attention",
+           "kv_cache_attention_workspace_bytes"]
 
 _FORMATS = {"nvfp4": (_lib.FP4Q_NVFP4, 16), "mxfp4": (_lib.FP4Q_MXFP4, 32)}
 _DTYPES = {torch.float32: _lib.FP4Q_F32, torch.bfloat16: _lib.FP4Q_BF16}
@@ -217,6 +218,18 @@ def _grow_workspace(cache, a, stream):
     return ws
 
 
+def kv_cache_attention_workspace_bytes(q, cache, page_table, *, max_q=1, window=0):
+    """Bytes of the workspace= that kv_cache_attention takes for these
+    arguments (max_q 1 where it is called without cu_q)."""
+    shape, qs, code = _rows(q, "q", cache, 0)
+    seqs, cols, stride = _table(page_table, cache)
+    # (shapes decide; the tensors that are not at hand stand in for each other)
+    at = page_table.data_ptr() or cache.k_codes.data_ptr()
+    a = _lib.KvAttentionArgs(q.data_ptr(), qs[:2], q.data_ptr(), None, at, at, at, stride, shape[0], cols, seqs,
+                             int(max_q), shape[1], code, 1, int(window), _lib.FP4Q_ROT_NONE, 1.0)
+    return _lib.load().fp4q_kv_attention_workspace_bytes(cache._args, a)
+
+
 def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None, scale=None, causal=True, window=0,
                        rotation=None, out=None, return_lse=False, workspace=None):
     """softmax(scale q k^T) v over the cache: q [total, q_heads, head_dim],
@@ -236,7 +249,8 @@ def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None,
     zeros and -inf.  Nothing waits for the GPU: lengths and tables are read
     there, so a captured call may be replayed with others in place.  Calls on
     one stream share a workspace that is kept for it; workspace: another one
-    (a zeroed GPU tensor of fp4q_kv_attention_workspace_bytes bytes)."""
+    (a zeroed GPU tensor of kv_cache_attention_workspace_bytes bytes, for calls
+    on other streams at the same time, replays of captured ones among them)."""
     shape, qs, code = _rows(q, "q", cache, 0)
     seqs, cols, stride = _table(page_table, cache)
     total, q_heads = shape[0], shape[1]

@@ -270,6 +270,24 @@ def test_workspace_serves_any_calls(fq):  # noqa: F811
         assert not bool(shared[:1024 * 64].view(torch.int32)[::16].any())
 
 
+@pytest.mark.parametrize("new,q_heads", SHAPES)
+@pytest.mark.parametrize("window", [0, 30])
+def test_workspace_bytes(fq, new, q_heads, window):  # noqa: F811
+    """A workspace of the size asked for serves; one of 16 bytes less is refused."""
+    case = Case(fq, "mxfp4", 128, 2, [150, 37, 400], 16, seed=3)
+    cache, table = case.cache(), torch.from_numpy(case.table).cuda()
+    n = torch.tensor(case.lens, dtype=torch.int32, device="cuda")
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    q = torch.randn(sum(new), q_heads, 128, device="cuda")
+    need = fq.kv_cache_attention_workspace_bytes(q, cache, table, max_q=max(new), window=window)
+    own = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    kw = dict(cu_q=cu, max_q=max(new), window=window)
+    assert torch.equal(fq.kv_cache_attention(q, cache, table, n, workspace=own, **kw),
+                       fq.kv_cache_attention(q, cache, table, n, **kw))
+    with pytest.raises(RuntimeError):
+        fq.kv_cache_attention(q, cache, table, n, workspace=own[:-16], **kw)
+
+
 # ---- streams and graphs
 
 
