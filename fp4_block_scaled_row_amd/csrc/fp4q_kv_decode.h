@@ -405,7 +405,7 @@ hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
 template <int D, int FMT>
 hipError_t launch_decode_d(const KvAttendLaunch& a, int tiles, int cus, hipStream_t st) {
   if (a.dtype == kF32) return launch_decode_t<FMT, D, 1, FMT == 1 ? 2 : 3, FMT == 1 ? 2 : 3>(a, cus, st);
-  const bool two = kv_rotated_pieces<FMT>(a) == 2;
+  const bool two = kv_bf16_pieces(a) == 2;
   if constexpr (D <= 128) {
     if (tiles == 2) return two ? launch_decode_t<FMT, D, 2, 2, 1>(a, cus, st) : launch_decode_t<FMT, D, 2, 1, 1>(a, cus, st);
   }

@@ -398,11 +398,11 @@ hipError_t launch_prefill_d(const KvAttendLaunch& a, int waves, int cus, hipStre
   if (a.dtype == kF32) return launch_prefill_t<FMT, D, 4, FMT == 1 ? 2 : 3, FMT == 1 ? 2 : 3>(a, cus, st);
   if constexpr (D <= 128) {
     if (waves == 8) {
-      if (kv_rotated_pieces<FMT>(a) == 2) return launch_prefill_t<FMT, D, 8, 2, 1>(a, cus, st);
+      if (kv_bf16_pieces(a) == 2) return launch_prefill_t<FMT, D, 8, 2, 1>(a, cus, st);
       return launch_prefill_t<FMT, D, 8, 1, 1>(a, cus, st);
     }
   }
-  if (kv_rotated_pieces<FMT>(a) == 2) return launch_prefill_t<FMT, D, 4, 2, 1>(a, cus, st);
+  if (kv_bf16_pieces(a) == 2) return launch_prefill_t<FMT, D, 4, 2, 1>(a, cus, st);
   return launch_prefill_t<FMT, D, 4, 1, 1>(a, cus, st);
 }
 

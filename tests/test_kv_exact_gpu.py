@@ -1,0 +1,72 @@
+"""How exact attention over the 4-bit cache is, measured against the outputs' own size: calls as a serving program
+makes them (without the log-sum-exp, keys rotated), contexts so long that outputs are far smaller than the values.
+
+Bounds, in root mean square over a call's outputs and relative to the outputs' own.  A bf16 output's own rounding is
+computed (the 64-bit result rounded).  What comes on top of it may be at most 2^-11: weights are rounded by 2^-12
+of themselves at most (one fp16 piece) with signs of their own, which moves an output by that part of the root of its
+squared terms, about its own size; queries in two pieces move a score s by 2^-17 |s| at most (16 bits, bf16) with |s| to
+2^4, another 2^-13.  An fp32 output: weights and queries of 22 bits or more, scores to 2^3, fp32 sums over up to 40000
+terms with errors of either sign: 2^-22 (1 + 2^3) + 2^-24 * 200, doubled: 2^-15."""
+import numpy as np
+import pytest
+import torch
+
+import kv_ref
+from test_kv_gpu import DT, Case, fq  # noqa: F401  (fq: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+ON_TOP = {"bf16": 2.0 ** -11, "f32": 2.0 ** -15}
+# (lengths, queries, query heads of 2 cache heads): few rows, more of them, many, long contexts
+SHAPES = [([700, 301, 33], [1, 1, 1], 16), ([700, 301, 33], [3, 2, 4], 8), ([300, 87], [40, 33], 8),
+          ([333, 210], [140, 70], 4), ([9001, 40000], [1, 1], 8)]
+
+
+def rms(x):
+    return float(np.sqrt(np.mean(np.square(x))))
+
+
+def call(case, q, new, rotate, **kw):
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    return case.fq.kv_cache_attention(q.cuda(), case.cache(), torch.from_numpy(case.table).cuda(),
+                                      torch.tensor(case.lens, dtype=torch.int32, device="cuda"),
+                                      cu_q=None if max(new) == 1 else cu, max_q=max(new),
+                                      rotation="fwht128" if rotate else None, **kw)
+
+
+def wanted(case, q, new, rotate):
+    qd = kv_ref.rotate(q.double().numpy()) if rotate else q.double().numpy()
+    at = np.concatenate([[0], np.cumsum(new)])
+    return np.concatenate([kv_ref.attention(qd[at[b]:at[b + 1]], *case.tokens(b), case.dim ** -0.5)[0]
+                           for b in range(len(new))])
+
+
+@pytest.mark.parametrize("fmt,dim,rotate", [("nvfp4", 128, True), ("nvfp4", 128, False), ("nvfp4", 256, True),
+                                            ("mxfp4", 128, True), ("mxfp4", 128, False), ("mxfp4", 256, False),
+                                            ("nvfp4", 64, False), ("mxfp4", 96, False)])
+@pytest.mark.parametrize("dtype,q_scale", [("bf16", 1.5), ("bf16", 5.0), ("f32", 1.5)])
+@pytest.mark.parametrize("lens,new,q_heads", SHAPES)
+def test_error_by_the_outputs_own_size(fq, fmt, dim, rotate, dtype, q_scale, lens, new, q_heads):  # noqa: F811
+    if fmt == "mxfp4" and dtype == "bf16":
+        pytest.skip("weights in one bf16 piece")
+    case = Case(fq, fmt, dim, 2, lens, 48, seed=len(new) + dim)
+    q = (q_scale * torch.from_numpy(case.rng.standard_normal((sum(new), q_heads, dim)))).to(DT[dtype])
+    print("attention", fmt, dim, rotate, dtype, q_scale, lens, new, q_heads, flush=True)
+    got = call(case, q, new, rotate).double().cpu().numpy()
+    want = wanted(case, q, new, rotate)
+    own = rms(torch.from_numpy(want).to(DT[dtype]).double().numpy() - want)
+    error, bound = rms(got - want), (own ** 2 + (ON_TOP[dtype] * rms(want)) ** 2) ** 0.5
+    assert error <= bound, "off by %g of the outputs, own rounding %g, bound %g" % tuple(
+        x / rms(want) for x in (error, own, bound))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dim", [128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,new,q_heads", SHAPES)
+def test_log_sum_exps_leave_the_outputs_alone(fq, fmt, dim, dtype, lens, new, q_heads):  # noqa: F811
+    """The same bits whether the log-sum-exp is asked for or not."""
+    case = Case(fq, fmt, dim, 2, lens, 64, seed=3)
+    q = torch.randn(sum(new), q_heads, dim).to(DT[dtype])
+    print("attention", fmt, dim, dtype, lens, new, q_heads, flush=True)
+    assert torch.equal(call(case, q, new, True), call(case, q, new, True, return_lse=True)[0])
