@@ -18,11 +18,15 @@
 // a weight; it takes 190 us where two take 229, 4096 queries of 32 heads over as
 // many tokens); an fp32 one keeps 22 (fp16) or 24 (bf16).  fp16 pieces
 // are scaled by a power of two per row that puts the row's largest value in
-// [2^8, 2^9).  The softmax weights enter in kP pieces: one (2^-12 in fp16,
-// 2^-9 in bf16 relative to the weight, below the bf16 output's own rounding)
-// for bf16 outputs; for fp32 outputs two in fp16 and three in bf16, whose
-// 16 bits in two left an output's error at 2e-6 of it, twice that of the sum
-// in fp32.  Scores, maxima, weights' sums and outputs are held in fp32.
+// [2^8, 2^9).  The softmax weights enter in kP pieces.  For bf16 outputs one
+// in fp16 (2^-12 of the weight, an eighth of the output's own rounding), two in
+// bf16 (2^-17): one bf16 piece (2^-9) is as coarse as that rounding and left
+// outputs a third further off than it.  The many-row kernel, where a second
+// piece makes the call 1.33 times longer, turns MXFP4 values whose scales allow
+// it into fp16 instead (see KvLane::fits_half).  For fp32 outputs two in fp16
+// and three in bf16, whose 16 bits in two left an output's error at 2e-6 of it,
+// twice that of the sum in fp32.  Scores, maxima, weights' sums and outputs are
+// held in fp32.
 //
 // Layout in the matrix instructions.  Scores are formed transposed, keys as
 // the left operand and queries as the right one, so that a lane ends up with
@@ -189,6 +193,27 @@ struct KvLane {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) codes[c] = there ? codes[c] : 0u;
     }
+  }
+  // MXFP4: whether all values are fp16 numbers, 0.5 x 2^-23 to 6 x 2^13, or zeros.
+  __device__ __forceinline__ bool fits_half() const {
+    static_assert(FMT == 0, "NVFP4 values always are");
+    bool fits = true;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const uint32_t b = (scales >> (8 * scale_of(c))) & 0xFFu;
+      fits &= b - 104u <= 36u || ((codes[c] & 0x77777777u) == 0u && b != 255u);
+    }
+    return fits;
+  }
+  // Chunk c of MXFP4 values that fit, in fp16.
+  __device__ __forceinline__ u32x4_t half_values(int c) const {
+    const float sc = e8m0_operand((scales >> (8 * scale_of(c))) & 0xFFu);
+    u32x4_t o;
+    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], sc, 0));
+    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], sc, 1));
+    o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], sc, 2));
+    o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes[c], sc, 3));
+    return o;
   }
   // All scale bytes prepared for values(): NVFP4's as fp16 pairs.
   struct Scales {

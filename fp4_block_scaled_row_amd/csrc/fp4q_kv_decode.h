@@ -41,8 +41,8 @@ struct DecodeShape {
   static constexpr int kMax1 = kVBytes > kOBytes ? kVBytes : kOBytes;
   static constexpr int kMain = kQRegs && kQBytes > kMax1 ? kQBytes : kMax1;
   static constexpr int kShared = kMain + (kQRegs ? 0 : kQBytes);
-  // as many as the registers allow (head_dim 256 by a hair, up to 9 spilled)
-  static constexpr int kWavesPerSimd = D > 128 ? (kQ > 1 || kP > 1 ? 1 : 2) : (kTiles == 2 || kQ > 1 ? 2 : 3);
+  // as many as the registers allow (head_dim 256 by a hair, up to 13 spilled)
+  static constexpr int kWavesPerSimd = D > 128 ? (kQ > 1 ? 1 : 2) : (kTiles == 2 || kQ > 1 ? 2 : 3);
 };
 
 template <int FMT, int D, int kTiles, int kQ, int kP, bool kWhole>
@@ -405,11 +405,12 @@ hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
 template <int D, int FMT>
 hipError_t launch_decode_d(const KvAttendLaunch& a, int tiles, int cus, hipStream_t st) {
   if (a.dtype == kF32) return launch_decode_t<FMT, D, 1, FMT == 1 ? 2 : 3, FMT == 1 ? 2 : 3>(a, cus, st);
+  constexpr int kP = FMT == 1 ? 1 : 2;
   const bool two = kv_bf16_pieces(a) == 2;
   if constexpr (D <= 128) {
-    if (tiles == 2) return two ? launch_decode_t<FMT, D, 2, 2, 1>(a, cus, st) : launch_decode_t<FMT, D, 2, 1, 1>(a, cus, st);
+    if (tiles == 2) return two ? launch_decode_t<FMT, D, 2, 2, kP>(a, cus, st) : launch_decode_t<FMT, D, 2, 1, kP>(a, cus, st);
   }
-  return two ? launch_decode_t<FMT, D, 1, 2, 1>(a, cus, st) : launch_decode_t<FMT, D, 1, 1, 1>(a, cus, st);
+  return two ? launch_decode_t<FMT, D, 1, 2, kP>(a, cus, st) : launch_decode_t<FMT, D, 1, 1, kP>(a, cus, st);
 }
 
 }  // namespace fp4q

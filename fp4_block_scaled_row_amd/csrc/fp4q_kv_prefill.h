@@ -11,17 +11,28 @@
 // Bound by matrix and vector instructions, which overlap only between a SIMD's
 // two waves: 64 tokens x 32 rows x 128 elements are 1024 cycles of the ones and
 // about 1150 of the others (a third of them exponentials) a wave.  4 x 1000
-// queries of 40 heads over up to 16000 tokens, MXFP4: 775 us, 970 TFLOP/s (a
+// queries of 40 heads over up to 16000 tokens, MXFP4: 810 us, 930 TFLOP/s (a
 // large library product reaches 1190); 4096 queries of 32 heads over as many
-// tokens, NVFP4: 190 to 205 us, 670 to 720, where blocks that see half of a step
-// and the ends of blocks weigh more.  Products of the next step's scores between
+// tokens, NVFP4, rotated queries in two pieces, whose second is as much matrix
+// work again as half of the rest: 229 us, 600, where blocks that see half of a
+// step and the ends of blocks weigh more.  Products of the next step's scores between
 // this one's exponentials in an order fixed by the source, with three steps in
-// LDS, were no faster (830 us).
+// LDS, were no faster (830 us for 785).
+//
+// MXFP4 values are fp16 numbers, as NVFP4's are, where a block's largest lies
+// between 2^-23 and 2^16.  So for bf16 outputs a workgroup takes its part of a
+// unit in fp16, with one piece of weights, and if it meets a block that is not,
+// leaves that and begins the part again in bf16 with two.
 #pragma once
 
 #include "fp4q_kv_attend.h"
 
 namespace fp4q {
+
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
 
 constexpr int kStepTokens = 64;
 constexpr int kStepCost = 6;      // steps that beginning and ending a unit takes as long as
@@ -34,6 +45,8 @@ struct PrefillShape {
   // transposed reads take 4 rows of 16 words at once: rows 16 or 48 banks apart
   static constexpr int kVStride = D == 96 ? D : D + 32;
   static constexpr int kHalf = kStepTokens * (kKStride + kVStride);
+  // MXFP4 with bf16 outputs: values in fp16 where all of them fit it
+  static constexpr bool kHalfValues = FMT == 0 && kP == 1;
   // two waves a SIMD where the registers allow it
   static constexpr int kWavesPerSimd = D <= 128 && kQ <= 2 && kP == 1 ? 2 : 1;
 };
@@ -118,6 +131,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
   __shared__ __align__(16) uint16_t s_kv[2 * Shape::kHalf];
   __shared__ int s_scan[kW + 6];
   __shared__ int s_bad;
+  __shared__ int s_misfit[2];      // kHalfValues: a step's values do not fit fp16
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4, col = lane & 31, half = lane >> 5;
@@ -162,7 +176,8 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         there[x] = page && t < n;
       }
     };
-    auto put = [&](int grp) {
+    // (fmt: the values' type, that of a format's products)
+    auto put = [&](int grp, auto fmt) __attribute__((always_inline)) {
       const int t0 = u.lo + grp * kStepTokens;
       const bool edge = t0 + kStepTokens > block_to || t0 < block_from;
       uint16_t* base = s_kv + (grp & 1) * Shape::kHalf;
@@ -174,20 +189,30 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
           const bool left_out = in[x].drop_not_finite();
           if (__any(left_out)) s_bad = 1;
         }
-        const typename Lane::Scales sc = in[x].prepare();
         const int t = 16 * ((task0 + x) >> 1) + r;
         uint16_t* dst = values ? base + kStepTokens * Shape::kKStride + t * Shape::kVStride : base + t * Shape::kKStride;
+        if constexpr (decltype(fmt)::value != FMT) {
+          if (values) {
+            if (__any(!in[x].fits_half())) s_misfit[grp & 1] = 1;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<u32x4_t*>(dst + Lane::element(c, g)) = in[x].half_values(c);
+            continue;
+          }
+        }
+        const typename Lane::Scales sc = in[x].prepare();
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) *reinterpret_cast<u32x4_t*>(dst + Lane::element(c, g)) = in[x].values(c, sc);
       }
     };
-    // (the first loads are on their way while the queries are prepared)
-    if (n > 0) {
-      find(group);
-      fetch(group);
-      find(group + 1);
-    }
-    if (tid == 0) s_bad = 0;
+    auto begin = [&]() {
+      if (n > 0) {
+        find(group);
+        fetch(group);
+        find(group + 1);
+      }
+    };
+    begin();      // (on their way while the queries are prepared)
+    if (tid == 0) s_bad = s_misfit[0] = s_misfit[1] = 0;
     u32x4_t qf[kQ][D / 16];
     const float factor = wave_queries<FMT, D, kQ>(a, u, row0 + col, half, qf);
     int sees_from;
@@ -201,121 +226,150 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
     const bool rows = (int)quotient((uint32_t)row0, a.group_div) < u.m;
 
     f32x16_t o[D / 32];
+    float m, l;
+    // The steps of the workgroup's groups, values and weights in the type of
+    // format fmt, weights in np pieces; false: some values do not fit that type.
+    auto pass = [&](auto fmt, auto np) __attribute__((always_inline)) {
+      constexpr int kWeights = decltype(np)::value;
+      constexpr bool kMayMisfit = decltype(fmt)::value != FMT;
+      using V = KvType<decltype(fmt)::value>;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) o[c] = f32x16_t{};
-    float m = kNoMax, l = 0.0f;
+      for (int c = 0; c < D / 32; ++c) o[c] = f32x16_t{};
+      m = kNoMax;
+      l = 0.0f;
 
-    __syncthreads();
-    if (n > 0) {
-      put(group);
-      fetch(group + 1);
-      find(group + 2);
-    }
-    __syncthreads();
-    for (int grp = group; grp < last; ++grp) {
-      const int t0 = u.lo + grp * kStepTokens;
-      if (t0 >= n) break;                       // (a unit without tokens)
-      if (rows && t0 < wu.hi && t0 + kStepTokens > wu.lo) {
-        // LDS reads set out a stage before the products that take them, and the
-        // scheduler may not move them back: left alone it puts each right
-        // before its product, which then waits for it.
-        const uint16_t* ks = s_kv + (grp & 1) * Shape::kHalf + col * Shape::kKStride + 8 * half;
-        const uint16_t* vs = s_kv + (grp & 1) * Shape::kHalf + kStepTokens * Shape::kKStride +
-                             (4 * half + (r >> 2)) * Shape::kVStride + 16 * (g & 1) + 4 * (r & 3);
-        constexpr int kStage = D / 16 < 8 ? D / 16 : 8, kStages = 2 * (D / 16) / kStage;   // key fragments
-        u32x4_t kf[2][kStage];
-        auto read_keys = [&](int stage) {
-#pragma unroll
-          for (int i = 0; i < kStage; ++i) {
-            const int f = stage * kStage + i, x = f & 1, c = f >> 1;
-            kf[stage & 1][i] = *reinterpret_cast<const u32x4_t*>(ks + 32 * x * Shape::kKStride + 16 * c);
-          }
-        };
-        u32x4_t vf[2][D / 32];
-        auto read_values = [&](int k) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const u32x2_t x0 = read_transposed(vs + 16 * k * Shape::kVStride + 32 * c);
-            const u32x2_t x1 = read_transposed(vs + (16 * k + 8) * Shape::kVStride + 32 * c);
-            vf[k & 1][c] = u32x4_t{x0.x, x0.y, x1.x, x1.y};
-          }
-        };
-        f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
-        read_keys(0);
-#pragma unroll
-        for (int stage = 0; stage < kStages; ++stage) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (stage + 1 < kStages) read_keys(stage + 1);
-          else read_values(0);
-#pragma unroll
-          for (int i = 0; i < kStage; ++i) {
-            const int f = stage * kStage + i, x = f & 1, c = f >> 1;
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) s[x] = T::mfma32(kf[stage & 1][i], qf[q][c], s[x]);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        // token 32 x + 8 (i / 4) + 4 half + i % 4 of the step
-        float y[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = s[i >> 4][i & 15];
-        if (t0 + kStepTokens > all_to || t0 < all_from) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint32_t j = (uint32_t)(t0 + 8 * (i >> 2) + 4 * half + (i & 3) - sees_from);
-            y[i] = j < sees ? y[i] : -INFINITY;
-          }
-        }
-        float most = y[0];
-#pragma unroll
-        for (int i = 1; i < 32; ++i) most = larger(most, y[i]);
-        most *= factor;
-        if (__any(most > m + kRaise)) {
-          const float x = larger(larger(most, __shfl_xor(most, 32, 64)), m);
-          const float f = __builtin_amdgcn_exp2f(m - x);
-          m = x;
-          l *= f;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) o[c] *= f;
-        }
-        const float top = T::kUp - m;
-        u32x4_t w[4][kP];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h[4][kP];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j], factor, top));
-            const float p1 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j + 1], factor, top));
-            l += p0 + p1;
-            pieces<FMT, kP>(p0, p1, h[j]);
-          }
-#pragma unroll
-          for (int q = 0; q < kP; ++q) w[k][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
-        }
-        // weighted values: element 32 c + 8 (i / 4) + 4 half + i % 4 of the row.
-        // Of a SIMD's two waves the one that is at these goes first: its
-        // products fill the other's exponentials (4 x 1000 queries of 40 heads
-        // over to 16000 tokens 775-779 us with this priority, 783-786 without).
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (k + 1 < 4) read_values(k + 1);
-#pragma unroll
-          for (int q = 0; q < kP; ++q)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] = T::mfma32(vf[k & 1][c], w[k][q], o[c]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(0);
-      }
-      if (grp + 1 < last) {
-        put(grp + 1);
-        fetch(grp + 2);
-        find(grp + 3);
+      __syncthreads();
+      if (n > 0) {
+        put(group, fmt);
+        fetch(group + 1);
+        find(group + 2);
       }
       __syncthreads();
+      for (int grp = group; grp < last; ++grp) {
+        const int t0 = u.lo + grp * kStepTokens;
+        if (t0 >= n) break;                       // (a unit without tokens)
+        // (a half's word is written before the barrier that ends the step before,
+        // and again only after the one that ends this step: all waves read the same)
+        const int misfit = kMayMisfit ? s_misfit[grp & 1] : 0;
+        if (rows && t0 < wu.hi && t0 + kStepTokens > wu.lo) {
+          // LDS reads set out a stage before the products that take them, and the
+          // scheduler may not move them back: left alone it puts each right
+          // before its product, which then waits for it.
+          const uint16_t* ks = s_kv + (grp & 1) * Shape::kHalf + col * Shape::kKStride + 8 * half;
+          const uint16_t* vs = s_kv + (grp & 1) * Shape::kHalf + kStepTokens * Shape::kKStride +
+                               (4 * half + (r >> 2)) * Shape::kVStride + 16 * (g & 1) + 4 * (r & 3);
+          constexpr int kStage = D / 16 < 8 ? D / 16 : 8, kStages = 2 * (D / 16) / kStage;   // key fragments
+          u32x4_t kf[2][kStage];
+          auto read_keys = [&](int stage) {
+#pragma unroll
+            for (int i = 0; i < kStage; ++i) {
+              const int f = stage * kStage + i, x = f & 1, c = f >> 1;
+              kf[stage & 1][i] = *reinterpret_cast<const u32x4_t*>(ks + 32 * x * Shape::kKStride + 16 * c);
+            }
+          };
+          u32x4_t vf[2][D / 32];
+          auto read_values = [&](int k) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const u32x2_t x0 = read_transposed(vs + 16 * k * Shape::kVStride + 32 * c);
+              const u32x2_t x1 = read_transposed(vs + (16 * k + 8) * Shape::kVStride + 32 * c);
+              vf[k & 1][c] = u32x4_t{x0.x, x0.y, x1.x, x1.y};
+            }
+          };
+          f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
+          read_keys(0);
+#pragma unroll
+          for (int stage = 0; stage < kStages; ++stage) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (stage + 1 < kStages) read_keys(stage + 1);
+            else read_values(0);
+#pragma unroll
+            for (int i = 0; i < kStage; ++i) {
+              const int f = stage * kStage + i, x = f & 1, c = f >> 1;
+#pragma unroll
+              for (int q = 0; q < kQ; ++q) s[x] = T::mfma32(kf[stage & 1][i], qf[q][c], s[x]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          // token 32 x + 8 (i / 4) + 4 half + i % 4 of the step
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = s[i >> 4][i & 15];
+          if (t0 + kStepTokens > all_to || t0 < all_from) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t j = (uint32_t)(t0 + 8 * (i >> 2) + 4 * half + (i & 3) - sees_from);
+              y[i] = j < sees ? y[i] : -INFINITY;
+            }
+          }
+          float most = y[0];
+#pragma unroll
+          for (int i = 1; i < 32; ++i) most = larger(most, y[i]);
+          most *= factor;
+          if (__any(most > m + kRaise)) {
+            const float x = larger(larger(most, __shfl_xor(most, 32, 64)), m);
+            const float f = __builtin_amdgcn_exp2f(m - x);
+            m = x;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) o[c] *= f;
+          }
+          const float top = V::kUp - m;
+          u32x4_t w[4][kWeights];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4][kWeights];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float p0 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j], factor, top));
+              const float p1 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j + 1], factor, top));
+              l += p0 + p1;
+              pieces<decltype(fmt)::value, kWeights>(p0, p1, h[j]);
+            }
+#pragma unroll
+            for (int q = 0; q < kWeights; ++q) w[k][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
+          }
+          // weighted values: element 32 c + 8 (i / 4) + 4 half + i % 4 of the row.
+          // Of a SIMD's two waves the one that is at these goes first: its
+          // products fill the other's exponentials (4 x 1000 queries of 40 heads
+          // over to 16000 tokens 775-779 us with this priority, 783-786 without).
+          __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (k + 1 < 4) read_values(k + 1);
+#pragma unroll
+            for (int q = 0; q < kWeights; ++q)
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) o[c] = V::mfma32(vf[k & 1][c], w[k][q], o[c]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          __builtin_amdgcn_s_setprio(0);
+        }
+        if (kMayMisfit && __builtin_amdgcn_readfirstlane(misfit)) return false;
+        if (grp + 1 < last) {
+          put(grp + 1, fmt);
+          fetch(grp + 2);
+          find(grp + 3);
+        }
+        __syncthreads();
+      }
+      if constexpr (V::kUp != T::kUp) {      // (weights and sums as the other passes leave them)
+        constexpr float back = 1.0f / (1 << (int)(V::kUp - T::kUp));
+        l *= back;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] *= back;
+      }
+      return true;
+    };
+    if constexpr (Shape::kHalfValues) {
+      if (!pass(Const<1>{}, Const<1>{})) {
+        if (tid == 0) s_bad = 0;      // (read after the passes only)
+        begin();
+        pass(Const<0>{}, Const<2>{});
+      }
+    } else {
+      pass(Const<FMT>{}, Const<kP>{});
     }
 
     l += __shfl_xor(l, 32, 64);

@@ -47,8 +47,6 @@ def wanted(case, q, new, rotate):
 @pytest.mark.parametrize("dtype,q_scale", [("bf16", 1.5), ("bf16", 5.0), ("f32", 1.5)])
 @pytest.mark.parametrize("lens,new,q_heads", SHAPES)
 def test_error_by_the_outputs_own_size(fq, fmt, dim, rotate, dtype, q_scale, lens, new, q_heads):  # noqa: F811
-    if fmt == "mxfp4" and dtype == "bf16":
-        pytest.skip("weights in one bf16 piece")
     case = Case(fq, fmt, dim, 2, lens, 48, seed=len(new) + dim)
     q = (q_scale * torch.from_numpy(case.rng.standard_normal((sum(new), q_heads, dim)))).to(DT[dtype])
     print("attention", fmt, dim, rotate, dtype, q_scale, lens, new, q_heads, flush=True)
@@ -70,3 +68,37 @@ def test_log_sum_exps_leave_the_outputs_alone(fq, fmt, dim, dtype, lens, new, q_
     q = torch.randn(sum(new), q_heads, dim).to(DT[dtype])
     print("attention", fmt, dim, dtype, lens, new, q_heads, flush=True)
     assert torch.equal(call(case, q, new, True), call(case, q, new, True, return_lse=True)[0])
+
+
+# Scale bytes of MXFP4 values by 32-element block: those of fp16 numbers are 104 to 140
+SPANS = {"low edge": [(100, 109)] * 4, "high edge": [(136, 145)] * 4, "far apart": [(20, 24), (122, 127), (60, 66), (180, 184)],
+         "one block": [(122, 127)] * 4, "zeros": [(122, 127)] * 4}
+
+
+@pytest.mark.parametrize("spans", list(SPANS), ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,new,q_heads,page", [([700, 301, 33], [1, 1, 1], 8, 32), ([300, 87], [40, 33], 8, 48),
+                                                   ([333, 2100], [140, 70], 4, 16), ([500, 90], [200, 90], 12, 64)])
+def test_values_of_any_scale(fq, spans, dtype, lens, new, q_heads, page):  # noqa: F811
+    """MXFP4 value blocks at the edges of fp16's range and far outside: as exact as others, each block measured by
+    its own outputs.  One block alone outside of it, far back in one sequence; blocks of zeros with any scale."""
+    case = Case(fq, "mxfp4", 128, 2, lens, page, seed=21)
+    case.planes[3][:] = np.stack([case.rng.integers(*s, case.planes[3].shape[:3]) for s in SPANS[spans]], -1)
+    if spans == "one block":
+        t = lens[0] // 3
+        case.planes[3][case.table[0, t // page], 1, t % page, 2] = 150
+    if spans == "zeros":
+        rows = case.rng.random(case.planes[3].shape) < 0.3
+        case.planes[3][rows] = case.rng.integers(0, 253, int(rows.sum()))
+        codes = case.planes[2].reshape(*rows.shape, 16)
+        codes[rows] &= 0x88
+    q = (1.5 * torch.from_numpy(case.rng.standard_normal((sum(new), q_heads, 128)))).to(DT[dtype])
+    print("attention", spans, dtype, lens, new, q_heads, page, flush=True)
+    got = call(case, q, new, False).double().cpu().numpy().reshape(-1, 4, 32)
+    want = wanted(case, q, new, False).reshape(-1, 4, 32)
+    for j in range(4):
+        g, w = got[:, j], want[:, j]
+        own = rms(torch.from_numpy(w).to(DT[dtype]).double().numpy() - w)
+        error, bound = rms(g - w), (own ** 2 + (ON_TOP[dtype] * rms(w)) ** 2) ** 0.5
+        assert error <= bound, "block %d off by %g of the outputs, own rounding %g, bound %g" % (
+            j, error / rms(w), own / rms(w), bound / rms(w))
