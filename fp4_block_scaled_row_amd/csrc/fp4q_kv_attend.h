@@ -858,14 +858,17 @@ __device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u
           for (int i = 0; i < kBatch; ++i) most = fmaxf(most, ml[i].x);
           const float f = __builtin_amdgcn_exp2f(top - most);
           top = most;
-          sum *= f;
-          total *= f;
+          // (small pieces among themselves before they meet a large one)
+          f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
+          float part_total = 0.0f;
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
             const float e = p + i < here ? __builtin_amdgcn_exp2f(ml[i].x - top) : 0.0f;
-            sum += f32x4_t{x[i].x, x[i].y, y[i].x, y[i].y} * e;
-            total += ml[i].y * e;
+            part += f32x4_t{x[i].x, x[i].y, y[i].x, y[i].y} * e;
+            part_total += ml[i].y * e;
           }
+          sum = sum * f + part;
+          total = total * f + part_total;
         }
         if (final) {
           kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, top, total);
@@ -930,14 +933,17 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(KvAttendLaunch a, int
     for (int i = 0; i < kBatch; ++i) most = fmaxf(most, ml[i].x);
     const float f = __builtin_amdgcn_exp2f(top - most);
     top = most;
-    sum *= f;
-    total *= f;
+    // (small pieces among themselves before they meet a large one)
+    f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
+    float part_total = 0.0f;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const float e = p + i < pieces ? __builtin_amdgcn_exp2f(ml[i].x - top) : 0.0f;
-      sum += v[i] * e;
-      total += ml[i].y * e;
+      part += v[i] * e;
+      part_total += ml[i].y * e;
     }
+    sum = sum * f + part;
+    total = total * f + part_total;
   }
   kv_finish4<FMT, D>(a, u, u.row0 + rr, d, sum, top, total);
 }

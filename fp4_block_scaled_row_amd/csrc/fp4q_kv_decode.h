@@ -340,13 +340,17 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       for (int t = 0; t < kTiles; ++t) {
         const float top = T::kUp - m[t];
         uint32_t h[4][kP];
+        // (a step's weights among themselves first: one rounding a step beside
+        // what may be far larger.  Before their own: the log-sum-exp is held to fp32)
+        float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float p0 = __builtin_amdgcn_exp2f(fmaf(y[t][2 * j], factor[t], top));
           const float p1 = __builtin_amdgcn_exp2f(fmaf(y[t][2 * j + 1], factor[t], top));
-          l[t] += p0 + p1;       // (before rounding: the log-sum-exp is held to fp32)
+          sum += p0 + p1;
           pieces<FMT, kP>(p0, p1, h[j]);
         }
+        l[t] += sum;
 #pragma unroll
         for (int q = 0; q < kP; ++q) w[t][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
       }

@@ -315,6 +315,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
             for (int c = 0; c < D / 32; ++c) o[c] *= f;
           }
           const float top = V::kUp - m;
+          float sum = 0.0f;       // (as in the few-row kernel)
           u32x4_t w[4][kWeights];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -323,12 +324,13 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
             for (int j = 0; j < 4; ++j) {
               const float p0 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j], factor, top));
               const float p1 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j + 1], factor, top));
-              l += p0 + p1;
+              sum += p0 + p1;
               pieces<decltype(fmt)::value, kWeights>(p0, p1, h[j]);
             }
 #pragma unroll
             for (int q = 0; q < kWeights; ++q) w[k][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
           }
+          l += sum;
           // weighted values: element 32 c + 8 (i / 4) + 4 half + i % 4 of the row.
           // Of a SIMD's two waves the one that is at these goes first: its
           // products fill the other's exponentials (4 x 1000 queries of 40 heads

@@ -102,3 +102,63 @@ def test_values_of_any_scale(fq, spans, dtype, lens, new, q_heads, page):  # noq
         error, bound = rms(g - w), (own ** 2 + (ON_TOP[dtype] * rms(w)) ** 2) ** 0.5
         assert error <= bound, "block %d off by %g of the outputs, own rounding %g, bound %g" % (
             j, error / rms(w), own / rms(w), bound / rms(w))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4"])
+@pytest.mark.parametrize("queries", [1, 48])
+@pytest.mark.parametrize("score", [12.0625, 14.125, 20.0])
+def test_many_small_weights_beside_a_large_one(fq, fmt, queries, score):  # noqa: F811
+    """One token scores `score` and has values of zero, 131070 score nothing and have ones: an output is n w / (1 + n w)
+    with w = exp(-score).  All of their weights are rounded alike.  fp32: the exponents, to 32 in powers of two, are
+    rounded by 2^-20, weights to 22 bits down to 2^-43 of the largest, sums of a lane's hundreds of terms by 2^-24 each:
+    2^-19 of the output and 2^17 x 2^-43 of the values, doubled."""
+    n, dim, page = 131071, 64, 64
+    pages = -(-n // page)
+    cache = fq.kv_cache(pages, page, 1, dim, format=fmt)
+    one = 0x38 if fmt == "nvfp4" else 127
+    cache.k_scales.fill_(one)
+    cache.v_scales.fill_(one)
+    cache.v_codes.fill_(0x22)                 # ones
+    cache.k_codes[0, 0, 0, 0] = 0x02          # the first token's first element
+    cache.v_codes[0, 0, 0] = 0
+    q = torch.zeros(queries, 4, dim, device="cuda")
+    q[:, :, 0] = score
+    print("attention", fmt, queries, score, flush=True)
+    out = fq.kv_cache_attention(q, cache, torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                                torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                cu_q=torch.tensor([0, queries], dtype=torch.int32, device="cuda"), max_q=queries, scale=1.0)
+    alike = (n - queries + torch.arange(queries, dtype=torch.float64))[:, None, None] * np.exp(-score)
+    want = alike / (1 + alike)
+    error = (out.double().cpu() - want).abs()
+    print("error", float((error / want).max()), "of the output")
+    assert bool((error <= 2.0 ** -18 * want + 2.0 ** -25).all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4"])
+@pytest.mark.parametrize("queries", [1, 3, 48])
+@pytest.mark.parametrize("score", [12.0625, 14.125])
+@pytest.mark.parametrize("n", [1000, 70000])
+def test_a_large_weight_among_few_small_ones(fq, fmt, queries, score, n):  # noqa: F811
+    """As above with a large one every 64 tokens, so that every part of a context that is summed by itself has one."""
+    dim, page = 64, 64
+    pages = -(-n // page)
+    cache = fq.kv_cache(pages, page, 1, dim, format=fmt)
+    one = 0x38 if fmt == "nvfp4" else 127
+    cache.k_scales.fill_(one)
+    cache.v_scales.fill_(one)
+    cache.v_codes.fill_(0x22)
+    cache.k_codes[:, 0, 5, 0] = 0x02
+    cache.v_codes[:, 0, 5] = 0
+    q = torch.zeros(queries, 4, dim, device="cuda")
+    q[:, :, 0] = score
+    print("attention", fmt, queries, score, n, flush=True)
+    out = fq.kv_cache_attention(q, cache, torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                                torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                cu_q=torch.tensor([0, queries], dtype=torch.int32, device="cuda"), max_q=queries, scale=1.0)
+    seen = n - queries + 1 + torch.arange(queries, dtype=torch.float64)
+    large = torch.floor((seen + 58) / 64)
+    small = ((seen - large) * np.exp(-score))[:, None, None]
+    want = small / (large[:, None, None] + small)
+    error = (out.double().cpu() - want).abs()
+    print("error", float((error / want).max()), "of the output")
+    assert bool((error <= 2.0 ** -18 * want + 2.0 ** -25 * want.new_tensor(64 / 2 ** 17)).all())
