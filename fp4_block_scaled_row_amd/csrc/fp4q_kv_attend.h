@@ -24,8 +24,8 @@
 // outputs a third further off than it.  The many-row kernel, where a second
 // piece makes the call 1.33 times longer, turns MXFP4 values whose scales allow
 // it into fp16 instead (see KvLane::fits_half).  For fp32 outputs two in fp16
-// and three in bf16, whose 16 bits in two left an output's error at 2e-6 of it,
-// twice that of the sum in fp32.  Scores, maxima, weights' sums and outputs are
+// (see weight_pieces) and three in bf16, whose 16 bits in two left an output's
+// error at 2e-6 of it, twice that of the sum in fp32.  Scores, maxima, weights' sums and outputs are
 // held in fp32.
 //
 // Layout in the matrix instructions.  Scores are formed transposed, keys as
@@ -115,6 +115,31 @@ __device__ __forceinline__ void pieces(float a, float b, uint32_t out[N]) {
       b -= KvType<FMT>::hi(out[i]);
     }
   }
+}
+
+// Pieces of a pair of softmax weights.  The second of two fp16 ones is 2^11
+// times as large, so that it holds 11 bits of what the first left down to 2^-36
+// (2^-43 of the largest weight at least; as it is it would end at 2^-25, and a
+// hundred thousand tokens of weight 2^-17 of the largest, whose roundings all go
+// one way, would be off by 3e-5), and meets values 2^-11 times as large: exact in
+// fp16, NVFP4 values being multiples of 2^-10.
+template <int FMT, int N>
+__device__ __forceinline__ void weight_pieces(float a, float b, uint32_t out[N]) {
+  if constexpr (FMT == 1 && N == 2) {
+    out[0] = KvType<1>::pack(a, b);
+    out[1] = KvType<1>::pack((a - KvType<1>::lo(out[0])) * 2048.0f, (b - KvType<1>::hi(out[0])) * 2048.0f);
+  } else {
+    pieces<FMT, N>(a, b, out);
+  }
+}
+// The values that piece q of N meets.
+template <int FMT, int N>
+__device__ __forceinline__ u32x4_t values_of_piece(int q, u32x4_t v) {
+  if (FMT == 1 && N == 2 && q == 1) {
+    const f16x8_t by = (_Float16)(1.0f / 2048.0f);
+    v = __builtin_bit_cast(u32x4_t, __builtin_bit_cast(f16x8_t, v) * by);
+  }
+  return v;
 }
 
 // ----------------------------------------------------------------------------

@@ -348,7 +348,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
           const float p0 = __builtin_amdgcn_exp2f(fmaf(y[t][2 * j], factor[t], top));
           const float p1 = __builtin_amdgcn_exp2f(fmaf(y[t][2 * j + 1], factor[t], top));
           sum += p0 + p1;
-          pieces<FMT, kP>(p0, p1, h[j]);
+          weight_pieces<FMT, kP>(p0, p1, h[j]);
         }
         l[t] += sum;
 #pragma unroll
@@ -361,9 +361,11 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
         const u32x2_t x0 = read_transposed(vp + 16 * c), x1 = read_transposed(vp + 16 * Shape::kVStride + 16 * c);
         const u32x4_t vf = {x0.x, x0.y, x1.x, x1.y};
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+        for (int q = 0; q < kP; ++q) {
+          const u32x4_t vq = values_of_piece<FMT, kP>(q, vf);
 #pragma unroll
-          for (int q = 0; q < kP; ++q) o[t][c] = T::mfma16(vf, w[t][q], o[t][c]);
+          for (int t = 0; t < kTiles; ++t) o[t][c] = T::mfma16(vq, w[t][q], o[t][c]);
+        }
       }
     };
     // (this wave's groups: those that begin before the end)

@@ -325,7 +325,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
               const float p0 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j], factor, top));
               const float p1 = __builtin_amdgcn_exp2f(fmaf(y[8 * k + 2 * j + 1], factor, top));
               sum += p0 + p1;
-              pieces<decltype(fmt)::value, kWeights>(p0, p1, h[j]);
+              weight_pieces<decltype(fmt)::value, kWeights>(p0, p1, h[j]);
             }
 #pragma unroll
             for (int q = 0; q < kWeights; ++q) w[k][q] = u32x4_t{h[0][q], h[1][q], h[2][q], h[3][q]};
@@ -343,7 +343,10 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
 #pragma unroll
             for (int q = 0; q < kWeights; ++q)
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) o[c] = V::mfma32(vf[k & 1][c], w[k][q], o[c]);
+              for (int c = 0; c < D / 32; ++c) {
+                const u32x4_t vq = values_of_piece<decltype(fmt)::value, kWeights>(q, vf[k & 1][c]);
+                o[c] = V::mfma32(vq, w[k][q], o[c]);
+              }
           }
           __builtin_amdgcn_sched_barrier(0);
           __builtin_amdgcn_s_setprio(0);

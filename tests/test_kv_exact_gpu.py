@@ -104,7 +104,7 @@ def test_values_of_any_scale(fq, spans, dtype, lens, new, q_heads, page):  # noq
             j, error / rms(w), own / rms(w), bound / rms(w))
 
 
-@pytest.mark.parametrize("fmt", ["mxfp4"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("queries", [1, 48])
 @pytest.mark.parametrize("score", [12.0625, 14.125, 20.0])
 def test_many_small_weights_beside_a_large_one(fq, fmt, queries, score):  # noqa: F811
@@ -134,7 +134,7 @@ def test_many_small_weights_beside_a_large_one(fq, fmt, queries, score):  # noqa
     assert bool((error <= 2.0 ** -18 * want + 2.0 ** -25).all())
 
 
-@pytest.mark.parametrize("fmt", ["mxfp4"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("queries", [1, 3, 48])
 @pytest.mark.parametrize("score", [12.0625, 14.125])
 @pytest.mark.parametrize("n", [1000, 70000])
