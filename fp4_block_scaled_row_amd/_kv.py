@@ -239,7 +239,8 @@ def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None,
     page_table: int32 [seqs, pages]; seq_lens: int32 [seqs], the tokens in the
     cache, new ones among them.  Without cu_q each sequence has one query;
     with cu_q (int32 [seqs + 1]) sequence b's are rows cu_q[b] to
-    cu_q[b + 1] - 1, at most max_q (default: all rows) in any.  causal: query
+    cu_q[b + 1] - 1, at most max_q (default: all rows) in any; rows from
+    cu_q[seqs] on, and those of a sequence past max_q, are zeros.  causal: query
     i of m sees token j <= n - m + i of the n; window > 0: only the last
     `window` of them.  scale: 1 / sqrt(head_dim) by default.  rotation: as the
     keys were written.

@@ -85,7 +85,8 @@ fp4q_status check_attention(const fp4q_kv_cache* cache, const fp4q_kv_attention_
   if (a->max_q < 0 || (!a->cu_q && (a->total_q != a->seqs || a->max_q > 1))) return FP4Q_ERR_INVALID_ARG;
   // row numbers (query, head of the group) are 31-bit
   if (a->total_q > INT_MAX / a->q_heads || a->seqs > 65535) return FP4Q_ERR_UNSUPPORTED;
-  if (a->total_q > 0 && a->seqs > 0) {
+  if (a->total_q > 0) {
+    if (a->seqs == 0) return FP4Q_ERR_INVALID_ARG;      // (as in a read: rows without a sequence)
     if (!a->q || !a->out || !a->seq_lens || (a->table_cols > 0 && !a->page_table)) return FP4Q_ERR_INVALID_ARG;
     if (a->q_stride[0] < 0 || a->q_stride[1] < 0) return FP4Q_ERR_INVALID_ARG;
     const int64_t esz = a->dtype == FP4Q_F32 ? 4 : 2;
@@ -259,8 +260,7 @@ fp4q_status fp4q_kv_read(const fp4q_kv_cache* cache, const fp4q_kv_read_args* ar
 
 size_t fp4q_kv_attention_workspace_bytes(const fp4q_kv_cache* cache, const fp4q_kv_attention_args* args) {
   KvAttendLaunch l;
-  if (check_attention(cache, args, &l) != FP4Q_OK || l.total_q == 0 || l.seqs == 0 || kv_attend_groups(l) > INT_MAX)
-    return 0;
+  if (check_attention(cache, args, &l) != FP4Q_OK || l.total_q == 0 || kv_attend_groups(l) > INT_MAX) return 0;
   return kv_attend_workspace(l);
 }
 
@@ -269,7 +269,7 @@ fp4q_status fp4q_kv_attention(const fp4q_kv_cache* cache, const fp4q_kv_attentio
   KvAttendLaunch l;
   const fp4q_status st = check_attention(cache, args, &l);
   if (st != FP4Q_OK) return st;
-  if (l.total_q == 0 || l.seqs == 0) return FP4Q_OK;
+  if (l.total_q == 0) return FP4Q_OK;
   if (kv_attend_groups(l) > INT_MAX) return FP4Q_ERR_UNSUPPORTED;
   const size_t need = kv_attend_workspace(l);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return FP4Q_ERR_WORKSPACE;

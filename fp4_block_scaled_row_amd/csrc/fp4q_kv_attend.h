@@ -638,14 +638,41 @@ __device__ __forceinline__ float2_t get2(const float* p) {
   return float2_t{as_f((uint32_t)w), as_f((uint32_t)(w >> 32))};
 }
 
-// Query head and row of q of row rr of a sequence; false: past its queries.
+// Query head and row of q of row rr of a sequence; false: past its queries, or
+// past max_q of them.
 struct KvOutRow {
   int64_t at;     // row of out and lse, [total_q][q_heads]
 };
 __device__ __forceinline__ bool kv_out_row(const KvAttendLaunch& a, int q0, int m, int head, int rr, KvOutRow& o) {
   const int i = (int)quotient((uint32_t)rr, a.group_div);
   o.at = ((int64_t)q0 + i) * ((int64_t)a.p.heads * a.group) + (int64_t)head * a.group + (rr - i * a.group);
-  return i < m;
+  return i < min(m, a.max_q);
+}
+
+// Zeros, and log-sum-exps of minus infinity, for queries [from, to).
+template <int D, int kThreadsWg>
+__device__ __forceinline__ void kv_clear(const KvAttendLaunch& a, int from, int to, int first, int workgroups) {
+  const int64_t per = (int64_t)a.p.heads * a.group, r0 = from * per, r1 = to * per;   // rows of out and lse
+  const int64_t at = (int64_t)first * kThreadsWg + threadIdx.x, step = (int64_t)workgroups * kThreadsWg;
+  const int chunks = D * (a.dtype == kF32 ? 4 : 2) / 16;
+  u32x4_t* out = static_cast<u32x4_t*>(a.out);
+  for (int64_t i = r0 * chunks + at; i < r1 * chunks; i += step) out[i] = u32x4_t{0u, 0u, 0u, 0u};
+  if (a.lse)
+    for (int64_t i = r0 + at; i < r1; i += step) a.lse[i] = -INFINITY;
+}
+// Rows that no unit has, which would be left as they were: queries past the last
+// sequence's (a batch padded to the size of a captured call), shared out over the
+// workgroups, and queries of a sequence past max_q.
+template <int D, int kThreadsWg>
+__device__ __forceinline__ void kv_clear_others(const KvAttendLaunch& a) {
+  if (!a.cu_q) return;      // (as many rows as sequences)
+  const int end = kv_first_query<true>(a, a.seqs);
+  if (end < a.total_q) kv_clear<D, kThreadsWg>(a, end, (int)a.total_q, blockIdx.x, gridDim.x);
+  if (a.max_q >= a.total_q) return;
+  for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
+    const int q0 = kv_first_query<true>(a, b), q1 = kv_first_query<true>(a, b + 1);
+    if (q1 - q0 > a.max_q) kv_clear<D, kThreadsWg>(a, q0 + a.max_q, q1, 0, 1);
+  }
 }
 
 // Pieces of bf16 queries.

@@ -66,6 +66,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   uint16_t* sq = reinterpret_cast<uint16_t*>(s_main + (Shape::kQRegs ? 0 : Shape::kMain));
 
   const float kg = FMT == 1 ? scalar(a.p.kg) : 1.0f;
+  kv_clear_others<D, kThreads>(a);
   KvStretch st;
   if (!kv_stretch<kRows, kGroupTokens, kGroupCost, kThreads, Shape::kWavesPerSimd == 3>(a, numbers, st, s_scan)) return;
   const KvUnit& u = st.u;

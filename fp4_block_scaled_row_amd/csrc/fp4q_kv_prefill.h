@@ -136,6 +136,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4, col = lane & 31, half = lane >> 5;
 
+  kv_clear_others<D, 64 * kW>(a);
   KvStretch st;
   KvShared* shared = kv_shared(a, blockIdx.x);
   if (tid == 0) shared->first = shared->last = 0;

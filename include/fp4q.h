@@ -346,7 +346,7 @@ typedef struct {
   int64_t total_q;
   int32_t table_cols;
   int32_t seqs;
-  int32_t max_q;               /* no sequence has more queries (0 or 1 without cu_q); rows past it are left out */
+  int32_t max_q;               /* no sequence has more queries (0 or 1 without cu_q) */
   int32_t q_heads;             /* a multiple of kv_heads: head h reads cache head h / (q_heads / kv_heads) */
   int32_t dtype;               /* FP4Q_F32 or FP4Q_BF16, of q and out */
   int32_t causal;              /* query i of m sees token j <= n - m + i of n; 0: every token */
@@ -369,7 +369,9 @@ size_t fp4q_kv_attention_workspace_bytes(const fp4q_kv_cache *cache, const fp4q_
  * counts at most table_cols * page_size tokens.  The cache's values enter
  * exactly; sums, maxima and outputs are fp32, rounded once.  A query that
  * sees no token, or only scores of minus infinity, gives zeros and a
- * log-sum-exp of minus infinity.  Tokens that a query does not see never
+ * log-sum-exp of minus infinity, and so do rows of q that no sequence has: from
+ * cu_q[seqs] on (a call of a fixed size with fewer queries), and queries of a
+ * sequence past max_q.  Tokens that a query does not see never
  * reach it, whatever their bytes stand for; a NaN block of one that it sees
  * makes a key's row NaN, a value's elements of it.  (An MXFP4 scale byte of
  * 253 or 254, which fp4q_kv_write does not produce and whose values pass
