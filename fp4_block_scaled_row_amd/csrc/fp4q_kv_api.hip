@@ -19,14 +19,15 @@ namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 fp4q_status hip_status(hipError_t e) { return e == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }
 
-// Bytes that one load of scales takes (see KvLane): what a plane's base and
-// strides have to be multiples of.
+bool attend_dim(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
+
+// Bytes that attention's one load of scales takes (see KvLane), 1, 2 or 4: what a
+// plane's base and strides have to be multiples of.  Writing and reading take a
+// byte at a time, so the head dimensions that attention does not have are free.
 int scale_alignment(int format, int head_dim) {
-  if (head_dim % 128 != 0) return 1;
+  if (!attend_dim(head_dim) || head_dim % 128 != 0) return 1;
   return head_dim / 4 / (format == FP4Q_MXFP4 ? 32 : 16);
 }
-
-bool attend_dim(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
 
 // Checks of a cache and the kernels' view of it.
 fp4q_status check_cache(const fp4q_kv_cache* c, KvPlanes* p) {

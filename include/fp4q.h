@@ -272,8 +272,8 @@ fp4q_status fp4q_mxfp4_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *a_co
  * finite) or FP4Q_MXFP4 (32-blocks, E8M0 scales); IF4 is UNSUPPORTED.
  * head_dim: a multiple of 32 up to 1024; page_size: any; num_pages: 1 to
  * 2^31 - 1; kv_heads: to 4096.  Code planes and code strides are 16-byte
- * aligned, scale planes and strides to the scale bytes of a quarter row where
- * head_dim is a multiple of 128, strides are below 2^31 bytes (else
+ * aligned, with head_dim 128 or 256 scale planes and strides to the scale bytes
+ * of a quarter row (1, 2 or 4), strides are below 2^31 bytes (else
  * FP4Q_ERR_UNSUPPORTED).  A dense [pages][heads][tokens] or
  * [pages][tokens][heads] cache is all that; planes may pass 4 GiB.
  *

@@ -4,7 +4,7 @@ import os
 import pytest
 
 from fp4_block_scaled_row_amd import _lib
-from test_kv_abi import A, attention_args, cache
+from test_kv_abi import A, attention_args, cache, read_args, write_args
 
 
 @pytest.fixture(scope="module")
@@ -18,3 +18,27 @@ def test_queries_without_a_sequence_are_refused(lib):
     """As a read of rows without a sequence is: they would be left as they are."""
     assert lib.fp4q_kv_attention(cache(), attention_args(seqs=0), A, 1 << 40, None) == _lib.FP4Q_ERR_INVALID_ARG
     assert lib.fp4q_kv_attention_workspace_bytes(cache(), attention_args(seqs=0)) == 0
+
+
+@pytest.mark.parametrize("fmt", [_lib.FP4Q_NVFP4, _lib.FP4Q_MXFP4])
+@pytest.mark.parametrize("head_dim", [384, 512, 640, 768, 896, 1024, 32, 64, 96, 160])
+@pytest.mark.parametrize("base", [0x10000, 0x10200, 0x10400, 0x10600, 0x10800, 0x10A00, 0x10E00, 0x10001])
+def test_scale_planes_of_dense_caches_lie_anywhere(lib, fmt, head_dim, base):
+    """Writing and reading take scales a byte at a time: a dense cache is taken wherever its planes lie."""
+    block = 16 if fmt == _lib.FP4Q_NVFP4 else 32
+    row = head_dim // block
+    c = cache(format=fmt, head_dim=head_dim, code_stride=(head_dim * 16, head_dim * 8, head_dim // 2),
+              scale_stride=(row * 32, row * 16, row), k_scales=base, v_scales=base + 0x4000)
+    assert lib.fp4q_kv_write(c, write_args(tokens=0), None) == _lib.FP4Q_OK
+    assert lib.fp4q_kv_read(c, read_args(total=0), None) == _lib.FP4Q_OK
+
+
+@pytest.mark.parametrize("fmt,head_dim,bytes_", [(_lib.FP4Q_NVFP4, 128, 2), (_lib.FP4Q_NVFP4, 256, 4),
+                                                 (_lib.FP4Q_MXFP4, 128, 1), (_lib.FP4Q_MXFP4, 256, 2)])
+def test_scale_planes_that_attention_loads_wide(lib, fmt, head_dim, bytes_):
+    row = head_dim // (16 if fmt == _lib.FP4Q_NVFP4 else 32)
+    for off in (0, 1, 2, 4):
+        c = cache(format=fmt, head_dim=head_dim, code_stride=(head_dim * 16, head_dim * 8, head_dim // 2),
+                  scale_stride=(row * 32, row * 16, row), k_scales=A + off)
+        want = _lib.FP4Q_OK if off % bytes_ == 0 else _lib.FP4Q_ERR_UNSUPPORTED
+        assert lib.fp4q_kv_attention(c, attention_args(total_q=0), None, 0, None) == want
