@@ -73,9 +73,9 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 
   // Codes of 2 x 16 tokens a lane, those of two groups in flight, and the page
   // numbers of the group after them.
-  //   kWhole: pages are multiples of 32 tokens, so that a wave's 32 tokens lie
-  // in one page: its number and their place are scalars, the lanes' offsets
-  // constants.  Tokens past the end are in the page too and are read.
+  //   kWhole (see kv_whole_tiles): pages are multiples of 32 tokens, so that a
+  // wave's 32 tokens lie in one page: its number and their place are scalars, the
+  // lanes' offsets 32-bit constants.  Tokens past the end are in the page too and are read.
   //   Other pages: every lane finds its token's page.  No branches: tokens past
   // the end are looked for at the last one's place.
   //   Pages that are none are read at page 0 and then zeroed.
@@ -386,6 +386,12 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   }
 }
 
+// Whether a wave's 32 tokens lie in one page and at 32-bit offsets from its
+// start: 31 token strides and a row.
+inline bool kv_whole_tiles(const KvPlanes& p) {
+  return p.page.d % 32 == 0 && p.code_stride[2] <= UINT32_MAX / 32 && p.scale_stride[2] <= UINT32_MAX / 32;
+}
+
 template <int FMT, int D, int kTiles, int kQ, int kP>
 hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   constexpr int kRows = 16 * kTiles;
@@ -400,7 +406,7 @@ hipError_t launch_decode_t(const KvAttendLaunch& a, int cus, hipStream_t st) {
   const int64_t wanted = a.most_tokens > 2 * kJoin * kGroupTokens ? (most + 1) / 2 : most;
   const int grid = (int)min(min(wanted, resident), (int64_t)kMostWorkgroups);
   b.thirds = (uint32_t)resident;
-  if (a.p.page.d % 32 == 0)
+  if (kv_whole_tiles(a.p))
     hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, true>), dim3(grid), dim3(kThreads), 0, st, b, (int)numbers);
   else
     hipLaunchKernelGGL((kv_decode_kernel<FMT, D, kTiles, kQ, kP, false>), dim3(grid), dim3(kThreads), 0, st, b, (int)numbers);
