@@ -627,12 +627,15 @@ inline size_t kv_workspace_bytes(int64_t workgroups, int64_t rows, int64_t head_
 // Partial results are written and read by relaxed atomics of agent scope, which
 // go past the caches that the chip's parts do not share; a workgroup counts its
 // arrival after its own have completed (vmcnt 0 of every wave, then a barrier).
+// The wait is an asm statement that clobbers memory: the builtin counts as
+// touching none, so that the compiler would be free to move stores past it.
 // Agent fences, which write back and invalidate whole L2 caches, made a call
 // over a batch of 64 four times longer.
 __device__ __forceinline__ void put2(float* p, float a, float b) {
   const uint64_t w = (uint64_t)as_u(a) | ((uint64_t)as_u(b) << 32);
   __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void wait_for_own_stores() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ float2_t get2(const float* p) {
   const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return float2_t{as_f((uint32_t)w), as_f((uint32_t)(w >> 32))};
@@ -873,7 +876,7 @@ __device__ __forceinline__ void kv_join(const KvAttendLaunch& a, const KvUnit& u
     const bool final = pieces <= 2 * kBatch;
     const int base = final ? 0 : mine / kBatch * kBatch, here = final ? pieces : min(kBatch, pieces - base);
     if (here > 1) {
-      __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt 0
+      wait_for_own_stores();
       __syncthreads();
       if (threadIdx.x == 0) {
         KvShared* record = kv_shared(a, w0 + base * stride);
