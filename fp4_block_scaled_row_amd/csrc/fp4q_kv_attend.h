@@ -199,17 +199,25 @@ struct KvLane {
   // MXFP4 253 and more, which no finite input is stored with (its largest
   // exponent less 2 is 252) and whose values pass bf16's range.
   static __device__ __forceinline__ bool not_finite(uint32_t b) { return FMT == 0 ? b >= 253u : (b & 0x7Fu) == 0x7Fu; }
-  // Makes such blocks zero and says whether there were any.
-  __device__ __forceinline__ bool drop_not_finite() {
-    uint32_t keep = 0xFFFFFFFFu;
+  // The block that scale byte i is of.
+  static __device__ __forceinline__ int block(int i, int g) {
+    return kRun ? g * (D / 4) / kBlock + i : (FMT == 0 ? i : 2 * i + (g >> 1));
+  }
+  // Makes such blocks zero and says which there were (bit i: scale byte i).
+  __device__ __forceinline__ uint32_t drop_not_finite() {
+    uint32_t keep = 0xFFFFFFFFu, dropped = 0u;
 #pragma unroll
-    for (int i = 0; i < kScales; ++i) keep &= not_finite((scales >> (8 * i)) & 0xFFu) ? ~(0xFFu << (8 * i)) : 0xFFFFFFFFu;
+    for (int i = 0; i < kScales; ++i) {
+      const bool drop = not_finite((scales >> (8 * i)) & 0xFFu);
+      keep &= drop ? ~(0xFFu << (8 * i)) : 0xFFFFFFFFu;
+      dropped |= drop ? 1u << i : 0u;
+    }
     scales &= keep;
     if constexpr (FMT == 0) {      // (scale byte 0 is 2^-127, not 0)
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) codes[c] = (keep >> (8 * scale_of(c))) & 1u ? codes[c] : 0u;
     }
-    return keep != 0xFFFFFFFFu;
+    return dropped;
   }
   // Zeros in place of what was loaded (a token that is not there).
   __device__ __forceinline__ void keep_if(bool there) {
@@ -807,28 +815,43 @@ __device__ __forceinline__ void kv_all_see(const KvAttendLaunch& a, const KvUnit
   from = a.window > 0 && past + i1 + 1 > a.window ? past + i1 + 1 - a.window : 0;
 }
 
-// Values that are no finite numbers, in a tile that some rows see only in
-// part, enter the products as zeros: 0 times NaN must not reach the rows that
-// do not see them.  Where that happened the rows that do see one are made NaN
-// here, element d .. d + 3 of row rr at a time, by going through the scale
-// bytes of tokens [t0, t1) again.
-template <int FMT, int D>
-__device__ __forceinline__ bool kv_sees_nan(const KvAttendLaunch& a, const KvUnit& u, int rr, int d, int t0, int t1) {
-  int from;
-  uint32_t count;
-  kv_sees(a, u, rr, from, count);
-  const KvHead planes = kv_head(a.p, u.head);
-  const int32_t* table = a.table + u.b * a.table_stride;
-  bool nan = false;
-  for (int t = max(t0, from); t < t1 && (uint32_t)(t - from) < count; ++t) {
-    const uint32_t col = quotient((uint32_t)t, a.p.page);
-    const int32_t page = table[col];
-    if ((uint32_t)page >= (uint32_t)a.p.num_pages) continue;
-    const KvAt at = kv_at(a.p, (uint32_t)page, (uint32_t)t - col * a.p.page.d);
-    nan |= KvLane<FMT, D>::not_finite(planes.vs[at.scale + d / KvLane<FMT, D>::kBlock]);
+// Values that are no finite numbers, in a tile that some rows see only in part,
+// enter the products as zeros: 0 times NaN must not reach the rows that do not
+// see them.  Their tokens and blocks (a bit each) are noted where they are left
+// out, and the rows that do see one made NaN at the end.  Such tiles are the ones
+// at either end of a block's tokens: of a window's beginnings, which spread over
+// kRows tokens at most, with the rest of two tiles, and of the rows' last tokens.
+template <int kRows, int kTile>
+struct NotedNans {
+  static constexpr int kMost = 2 * kRows + 4 * kTile;
+  int count;
+  int token[kMost];
+  uint32_t blocks[kMost];
+
+  // The lane's part (group g of the token's row) of what was left out.
+  template <int FMT, int D>
+  __device__ __forceinline__ void note(int t, int g, uint32_t dropped) {
+    uint32_t b = 0u;
+#pragma unroll
+    for (int i = 0; i < KvLane<FMT, D>::kScales; ++i) b |= ((dropped >> i) & 1u) << KvLane<FMT, D>::block(i, g);
+    b |= __shfl_xor((int)b, 16, 64);
+    b |= __shfl_xor((int)b, 32, 64);
+    if (g != 0 || b == 0u) return;
+    const int at = atomicAdd(&count, 1);
+    if (at >= kMost) return;
+    token[at] = t;
+    blocks[at] = b;
   }
-  return nan;
-}
+  // The noted blocks that row rr sees.
+  __device__ __forceinline__ uint32_t seen(const KvAttendLaunch& a, const KvUnit& u, int rr) const {
+    int from;
+    uint32_t sees, b = 0u;
+    kv_sees(a, u, rr, from, sees);
+#pragma unroll 1
+    for (int i = 0; i < min(count, kMost); ++i) b |= (uint32_t)(token[i] - from) < sees ? blocks[i] : 0u;
+    return b;
+  }
+};
 
 // Stores 4 consecutive elements of an output row.
 __device__ __forceinline__ void store_out4(const KvAttendLaunch& a, int64_t o, f32x4_t v) {

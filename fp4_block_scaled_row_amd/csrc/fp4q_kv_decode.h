@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   __shared__ float s_factor[kRows];
   __shared__ uint32_t s_most[kRows];
   __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
-  __shared__ int s_bad[kWaves];
+  __shared__ NotedNans<kRows, 32> s_nans;
   __shared__ int s_scan[kWaves + 6];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -159,12 +159,11 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
   // One unit a turn; it is finished in the next turn, when the next unit's loads
   // are on their way.
   KvUnit done = {};
-  int begins = 0, t_begin = 0, t_end = 0;
+  int begins = 0;
   bool have = false, whole = false;
   float* part = nullptr;
   f32x4_t o[kTiles][D / 16];
   float m[kTiles], l[kTiles];
-  bool bad = false;       // a value that is no finite number was left out
   for (;;) {
     const bool more = take(have ? kv_next<kRows, kGroupTokens, kGroupCost>(a, st) : true);
     if (have) {
@@ -178,7 +177,6 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
           s_l[wave][16 * t + r] = l[t];
         }
       }
-      if (lane == 0) s_bad[wave] = bad;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
         __syncthreads();
@@ -194,9 +192,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
           f32x4_t sum = *reinterpret_cast<const f32x4_t*>(so + row * Shape::kOStride + d);
 #pragma unroll
           for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4_t*>(so + (w * 16 + row) * Shape::kOStride + d);
-          if (s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]) {
-            if (kv_sees_nan<FMT, D>(a, done, done.row0 + rr, d, t_begin, t_end)) sum *= as_f(0x7FC00000u);
-          }
+          if (s_nans.count && (s_nans.seen(a, done, done.row0 + rr) >> (d / Lane::kBlock)) & 1u) sum *= as_f(0x7FC00000u);
           const float mx = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
           float total = 0.0f;
 #pragma unroll
@@ -215,6 +211,7 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       __syncthreads();
     }
     if (!more) return;
+    if (tid == 0) s_nans.count = 0;
     stage_queries<FMT, D, kQ, kRows>(a, kg, rows, sq, s_factor, s_most);
 
     u32x4_t qf[Shape::kQRegs ? kTiles : 1][Shape::kQRegs ? kQ : 1][Shape::kQRegs ? kChunks : 1];
@@ -244,7 +241,6 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) o[t][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    bad = false;
     auto step = [&](int grp, Tile& in) {
       const int t0 = first + grp * kGroupTokens;
       const bool edge = t0 + 32 > all_to || t0 < all_from;
@@ -258,8 +254,10 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
       if (edge) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const bool left_out = in.v[x].drop_not_finite() && t0 + 16 * x + r < n;
-          bad |= __any(left_out) != 0;
+          const int t = t0 + 16 * x + r;
+          uint32_t dropped = in.v[x].drop_not_finite();
+          if (t >= n) dropped = 0u;
+          if (__any(dropped != 0u)) s_nans.template note<FMT, D>(t, g, dropped);
         }
       }
       // scores of 32 tokens x 16 rows, transposed: token 16 x + 4 g + i, row r
@@ -379,8 +377,6 @@ __global__ __launch_bounds__(kThreads, (DecodeShape<FMT, D, kTiles, kQ, kP>::kWa
     done = u;
     begins = st.begins;
     whole = group == 0 && last == u.groups;
-    t_begin = u.lo + group * kGroupTokens;
-    t_end = min(u.hi, u.lo + last * kGroupTokens);
     part = kv_partial<D, kRows>(a, blockIdx.x, group == 0);
     have = true;
   }

@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
   constexpr int kTasks = 8 / kW;       // 16 tokens' keys or values a task: 8 in a step
   __shared__ __align__(16) uint16_t s_kv[2 * Shape::kHalf];
   __shared__ int s_scan[kW + 6];
-  __shared__ int s_bad;
+  __shared__ NotedNans<kRows, kStepTokens> s_nans;
   __shared__ int s_misfit[2];      // kHalfValues: a step's values do not fit fp16
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -187,8 +187,8 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         const bool values = (task0 + x) & 1;
         in[x].keep_if(there[x]);
         if (values && edge) {
-          const bool left_out = in[x].drop_not_finite();
-          if (__any(left_out)) s_bad = 1;
+          const uint32_t dropped = in[x].drop_not_finite();
+          if (__any(dropped != 0u)) s_nans.template note<FMT, D>(t0 + 16 * ((task0 + x) >> 1) + r, g, dropped);
         }
         const int t = 16 * ((task0 + x) >> 1) + r;
         uint16_t* dst = values ? base + kStepTokens * Shape::kKStride + t * Shape::kVStride : base + t * Shape::kKStride;
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
       }
     };
     begin();      // (on their way while the queries are prepared)
-    if (tid == 0) s_bad = s_misfit[0] = s_misfit[1] = 0;
+    if (tid == 0) s_nans.count = s_misfit[0] = s_misfit[1] = 0;
     u32x4_t qf[kQ][D / 16];
     const float factor = wave_queries<FMT, D, kQ>(a, u, row0 + col, half, qf);
     int sees_from;
@@ -370,7 +370,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
     };
     if constexpr (Shape::kHalfValues) {
       if (!pass(Const<1>{}, Const<1>{})) {
-        if (tid == 0) s_bad = 0;      // (read after the passes only)
+        if (tid == 0) s_nans.count = 0;      // (noted again; read after the passes only)
         begin();
         pass(Const<0>{}, Const<2>{});
       }
@@ -381,23 +381,15 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
     l += __shfl_xor(l, 32, 64);
     const bool whole = group == 0 && last == u.groups;
     const int rr = 32 * wave + col;
-    if (s_bad) {
-      const int t1 = min(u.hi, u.lo + last * kStepTokens);
+    if (s_nans.count) {
+      const uint32_t nan = s_nans.seen(a, u, u.row0 + rr);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const int d = 32 * c + 2 * i + 4 * half;
-          const float f = kv_sees_nan<FMT, D>(a, u, u.row0 + rr, d, u.lo + group * kStepTokens, t1) ? as_f(0x7FC00000u) : 1.0f;
-          o[c] = f32x16_t{i == 0 ? o[c][0] * f : o[c][0],    i == 0 ? o[c][1] * f : o[c][1],
-                          i == 0 ? o[c][2] * f : o[c][2],    i == 0 ? o[c][3] * f : o[c][3],
-                          i == 4 ? o[c][4] * f : o[c][4],    i == 4 ? o[c][5] * f : o[c][5],
-                          i == 4 ? o[c][6] * f : o[c][6],    i == 4 ? o[c][7] * f : o[c][7],
-                          i == 8 ? o[c][8] * f : o[c][8],    i == 8 ? o[c][9] * f : o[c][9],
-                          i == 8 ? o[c][10] * f : o[c][10],  i == 8 ? o[c][11] * f : o[c][11],
-                          i == 12 ? o[c][12] * f : o[c][12], i == 12 ? o[c][13] * f : o[c][13],
-                          i == 12 ? o[c][14] * f : o[c][14], i == 12 ? o[c][15] * f : o[c][15]};
-        }
+      for (int c = 0; c < D / 32; ++c) {
+        // (elements 0 to 7 of a lane's 16 are in the lower half of the 32)
+        const float f0 = (nan >> (32 * c / Lane::kBlock)) & 1u ? as_f(0x7FC00000u) : 1.0f;
+        const float f1 = (nan >> ((32 * c + 16) / Lane::kBlock)) & 1u ? as_f(0x7FC00000u) : 1.0f;
+        o[c] *= f32x16_t{f0, f0, f0, f0, f0, f0, f0, f0, f1, f1, f1, f1, f1, f1, f1, f1};
+      }
     }
     if (whole) {
 #pragma unroll
@@ -428,7 +420,7 @@ __global__ __launch_bounds__(64 * kW, (PrefillShape<FMT, D, kW, kQ, kP>::kWavesP
         if (half == 0) *reinterpret_cast<float2_t*>(part + (int64_t)kRows * D + 2 * rr) = float2_t{m, l};
       }
     }
-    __syncthreads();      // (everyone has read s_bad)
+    __syncthreads();      // (everyone has read s_nans)
   } while (kv_next<kRows, kStepTokens, kStepCost>(a, st));
 }
 
