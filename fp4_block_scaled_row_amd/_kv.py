@@ -133,6 +133,12 @@ def _index(t, what, cache, dtype, dims):
     return t.shape
 
 
+def _int32(x):
+    """x as far as 32 bits go (ctypes would keep its low bits); what is negative
+    stays so."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 def _table(page_table, cache):
     """Sequences, pages a sequence and the row stride of a page table."""
     seqs, cols = _index(page_table, "page_table", cache, torch.int32, 2)
@@ -226,7 +232,7 @@ def kv_cache_attention_workspace_bytes(q, cache, page_table, *, max_q=1, window=
     # (shapes decide; the tensors that are not at hand stand in for each other)
     at = page_table.data_ptr() or cache.k_codes.data_ptr()
     a = _lib.KvAttentionArgs(q.data_ptr(), qs[:2], q.data_ptr(), None, at, at, at, stride, shape[0], cols, seqs,
-                             int(max_q), shape[1], code, 1, int(window), _lib.FP4Q_ROT_NONE, 1.0)
+                             _int32(max_q), shape[1], code, 1, _int32(window), _lib.FP4Q_ROT_NONE, 1.0)
     return _lib.load().fp4q_kv_attention_workspace_bytes(cache._args, a)
 
 
@@ -266,7 +272,7 @@ def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None,
         if _index(cu_q, "cu_q", cache, torch.int32, 1)[0] != seqs + 1:
             raise ValueError("fp4q: cu_q must have one entry more than there are sequences")
         cu = cu_q.data_ptr()
-        max_q = total if max_q is None else int(max_q)
+        max_q = total if max_q is None else _int32(max_q)
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=cache.device)
     elif out.get_device() != cache._index or out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
@@ -274,7 +280,7 @@ def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None,
     lse = torch.empty((total, q_heads), dtype=torch.float32, device=cache.device) if return_lse else None
     a = _lib.KvAttentionArgs(q.data_ptr(), qs[:2], out.data_ptr(), lse.data_ptr() if return_lse else None, cu,
                              seq_lens.data_ptr(), page_table.data_ptr(), stride, total, cols, seqs, max_q, q_heads,
-                             code, 1 if causal else 0, int(window), _rotation(rotation),
+                             code, 1 if causal else 0, _int32(window), _rotation(rotation),
                              cache.head_dim ** -0.5 if scale is None else float(scale))
     run, stream = _lib.load().fp4q_kv_attention, _raw_stream(cache._index)
     if workspace is not None:

@@ -2,8 +2,9 @@
 import os
 
 import pytest
+import torch
 
-from fp4_block_scaled_row_amd import _lib
+from fp4_block_scaled_row_amd import _kv, _lib
 from test_kv_abi import A, attention_args, cache, read_args, write_args
 
 
@@ -42,3 +43,53 @@ def test_scale_planes_that_attention_loads_wide(lib, fmt, head_dim, bytes_):
                   scale_stride=(row * 32, row * 16, row), k_scales=A + off)
         want = _lib.FP4Q_OK if off % bytes_ == 0 else _lib.FP4Q_ERR_UNSUPPORTED
         assert lib.fp4q_kv_attention(c, attention_args(total_q=0), None, 0, None) == want
+
+
+class Handle:
+    """What the Python entry points look at of a cache, on the CPU; calls to the library are recorded, not made."""
+    head_dim, kv_heads, page_size, device, _index, _args = 128, 2, 16, torch.device("cpu"), -1, None
+
+
+class Recorder:
+    def __init__(self, calls):
+        self.calls = calls
+
+    def fp4q_kv_attention(self, cache, a, *rest):
+        self.calls.append(a)
+        return 0
+
+    def fp4q_kv_attention_workspace_bytes(self, cache, a):
+        self.calls.append(a)
+        return 64
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    made = []
+    monkeypatch.setattr(_kv._lib, "load", lambda: Recorder(made))
+    monkeypatch.setattr(_kv, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(_kv, "_call", lambda cache, function, *args: function(*args))
+    monkeypatch.setattr(_kv, "_workspaces", {(-1, 0): torch.zeros(64, dtype=torch.uint8)})
+    return made
+
+
+def attention(**kw):
+    q, table = torch.zeros(6, 8, 128), torch.zeros(2, 4, dtype=torch.int32)
+    cu = torch.tensor([0, 3, 6], dtype=torch.int32)
+    return _kv.kv_cache_attention(q, Handle(), table, torch.zeros(2, dtype=torch.int32), cu_q=cu, **kw)
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1])
+def test_numbers_past_32_bits_do_not_wrap(calls, value):
+    """A window or a bound on the queries that is as good as none must not become a small one, or none at all."""
+    attention(window=value, max_q=value)
+    assert calls[-1].window == 2 ** 31 - 1 and calls[-1].max_q >= 6
+    _kv.kv_cache_attention_workspace_bytes(torch.zeros(6, 8, 128), Handle(), torch.zeros(2, 4, dtype=torch.int32),
+                                           max_q=value, window=value)
+    assert calls[-1].window == 2 ** 31 - 1 and calls[-1].max_q >= 6
+
+
+@pytest.mark.parametrize("value", [-1, -2 ** 31 - 1, -2 ** 32])
+def test_negative_numbers_stay_negative(calls, value):
+    attention(window=value, max_q=value)       # (for the library to refuse)
+    assert calls[-1].window < 0 and calls[-1].max_q < 0
