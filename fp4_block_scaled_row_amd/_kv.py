@@ -284,8 +284,9 @@ def kv_cache_attention(q, cache, page_table, seq_lens, *, cu_q=None, max_q=None,
                              cache.head_dim ** -0.5 if scale is None else float(scale))
     run, stream = _lib.load().fp4q_kv_attention, _raw_stream(cache._index)
     if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("fp4q: the workspace must be a contiguous GPU tensor")
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != cache._index \
+                or not workspace.is_contiguous():
+            raise ValueError("fp4q: the workspace must be a contiguous tensor on the cache's device")
         status = _call(cache, run, cache._args, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                        stream)
     else:
