@@ -83,7 +83,7 @@ def kv_cache(num_pages, page_size, kv_heads, head_dim, *, format="nvfp4", k_glob
     planes = [torch.zeros((num_pages, kv_heads, page_size, w), dtype=torch.uint8, device=device) for w in widths]
     if format == "mxfp4":
         return KvCache(format, *planes)
-    scales = [g if isinstance(g, torch.Tensor) else torch.full((1,), float(g), device=device)
+    scales = [g if isinstance(g, torch.Tensor) else torch.full((1,), float(g), dtype=torch.float32, device=device)
               for g in (k_global, v_global)]
     return KvCache(format, *planes, *scales)
 
