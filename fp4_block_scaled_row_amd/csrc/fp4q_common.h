@@ -201,30 +201,6 @@ __device__ __forceinline__ uint32_t e2m1_sr_mag_f32(float a, uint32_t u, bool no
 }
 
 // ----------------------------------------------------------------------------
-// bf16 bits of vs * g rounded once: the fp32 product to nearest-even, a product
-// exactly on a bf16 midpoint decided by its rounding error (an FMA; fp64 below
-// 2^-100, where that error could underflow).
-__device__ __forceinline__ uint32_t bf16_of_product(float vs, float g) {
-  const float av = fabsf(vs);
-  const float a = av * g;
-  const uint32_t b = as_u(a);
-  const uint32_t hi = b >> 16;
-  uint32_t r = (b + 0x7FFFu + (hi & 1u)) >> 16;
-  if ((b & 0xFFFFu) == 0x8000u) {   // on a bf16 midpoint: which side is the exact product?
-    int side;
-    if (a >= 0x1p-100f) {
-      const float e = fmaf(av, g, -a);
-      side = e > 0.0f ? 1 : (e < 0.0f ? -1 : 0);
-    } else {
-      const double ex = (double)av * (double)g;
-      side = ex > (double)a ? 1 : (ex < (double)a ? -1 : 0);
-    }
-    r = side > 0 ? hi + 1u : (side < 0 ? hi : hi + (hi & 1u));
-  }
-  return r | ((as_u(vs) >> 31) << 15);
-}
-
-// ----------------------------------------------------------------------------
 // E4M3 (FN flavour: bias 7, subnormals k 2^-9, max 448 = 0x7E, 0x7F NaN).
 // Value of magnitude byte c (0..127) by the hardware conversion
 // (v_cvt_f32_fp8, one instruction, no branch): e4m3_value_hw for bytes

@@ -26,6 +26,26 @@ namespace {
 
 constexpr int kUnroll = 8;
 
+__device__ __forceinline__ uint32_t bf16_of_product(float vs, float g) {
+  const float av = fabsf(vs);
+  const float a = av * g;
+  const uint32_t b = as_u(a);
+  const uint32_t hi = b >> 16;
+  uint32_t r = (b + 0x7FFFu + (hi & 1u)) >> 16;
+  if ((b & 0xFFFFu) == 0x8000u) {   // on a bf16 midpoint: which side is the exact product?
+    int side;
+    if (a >= 0x1p-100f) {
+      const float e = fmaf(av, g, -a);
+      side = e > 0.0f ? 1 : (e < 0.0f ? -1 : 0);
+    } else {
+      const double ex = (double)av * (double)g;
+      side = ex > (double)a ? 1 : (ex < (double)a ? -1 : 0);
+    }
+    r = side > 0 ? hi + 1u : (side < 0 ? hi : hi + (hi & 1u));
+  }
+  return r | ((as_u(vs) >> 31) << 15);
+}
+
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 // Output bits (fp32, or bf16 in the low half) of k * 6 * s_c * g / 7 rounded

@@ -169,7 +169,7 @@ int64_t kv_attend_groups(const KvAttendLaunch& a) {
   const Plan p = attend_plan(a);
   KvAttendLaunch b = a;
   const int64_t numbers = kv_block_numbers(b, p.prefill ? 32 * p.waves : 16 * p.tiles);
-  // (the smaller of the two kernels' steps, the larger of their costs)
+  // (the smaller of the two kernels' steps; more than a unit costs in either)
   return kv_most_groups(b, numbers, 64, 16);
 }
 

@@ -130,7 +130,8 @@ __device__ __forceinline__ uint32_t mx_encode_block(const float v[8], uint32_t a
 // 19 us, 1.9 TB/s: 178 vector instructions a slot, 8 us of issue, after loads and
 // stores of 7, hardly overlapped (without the encoding 10 us).  Addresses held in
 // scalars, 1, 2 or 8 slots, and workgroups that go on with the next loads in
-// flight were no faster.  Small ones by latency, 3 us.
+// flight were no faster; a table of the scales' factors, whose set-up only this
+// instance (four slots) would pay, has not been tried.  Small ones by latency, 3 us.
 template <int FMT, int IN, int kSlots>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteLaunch w, float rot_scale, FastDiv row_slots,
                                                             FastDiv heads, uint32_t nslots) {
@@ -247,7 +248,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int64_t t) 
 // and the page numbers of the one after in flight; it finds its first row's
 // sequence once and goes on from there, the next kAhead sequences' bounds being
 // in LDS.  Bound by the stores: 16 sequences of up to 16384 tokens, 8 heads x 128,
-// 932 MB in 195 us, 4.8 TB/s (a large copy reaches 5.1).
+// 932 MB in 195 us, 4.8 TB/s (the library's copies and dequantizations of such
+// sizes reach 6.1 to 6.4).
 constexpr int kAhead = kThreads;
 
 // p = RN(v g) moved by its last bit towards the exact product where it is a bf16

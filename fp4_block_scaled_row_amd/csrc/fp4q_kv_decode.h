@@ -12,11 +12,15 @@
 // are in flight while one is worked on: a group takes a wave about 1.2 us, a
 // load from HBM about as long under load.
 //
-// Bound by HBM in large calls: 64 sequences of up to 8192 tokens, 8 heads of
-// 128, NVFP4, 380 MB in 83 to 89 us, 4.3 to 4.6 TB/s (a large copy reaches 5.1);
-// MXFP4, 2 x 131071 tokens, 273 MB in 67.5 us, 4.0 TB/s, of which the joins and
-// the uneven ends of the workgroups are about 15.  Small ones by the chain of
-// lengths, page numbers, codes, products and joins: 1 x 1023 tokens 11 us.
+// Large calls: 64 sequences of up to 8192 tokens, 8 heads of 128, NVFP4, 380 MB
+// in 82 us, 4.6 TB/s (a large copy reaches 6.4), 87 to 91 with rotated queries,
+// whose two pieces leave two waves a SIMD instead of three; of that call the
+// vector units issue 43 % of the time and the matrix units work 16 %, so it is
+// neither's issue nor the memory's rate alone but latency that more waves would
+// hide.  MXFP4, 2 x 131071 tokens, 273 MB in 56 us (partly from the Infinity
+// Cache) to 64; CUs are busy 73 to 84 % of it, joins and the uneven ends of the
+// workgroups are the rest.  Small ones by the chain of lengths, page numbers,
+// codes, products and joins: 1 x 1023 tokens 11 us.
 #pragma once
 
 #include "fp4q_kv_attend.h"
@@ -41,7 +45,8 @@ struct DecodeShape {
   static constexpr int kMax1 = kVBytes > kOBytes ? kVBytes : kOBytes;
   static constexpr int kMain = kQRegs && kQBytes > kMax1 ? kQBytes : kMax1;
   static constexpr int kShared = kMain + (kQRegs ? 0 : kQBytes);
-  // as many as the registers allow (head_dim 256 by a hair, up to 13 spilled)
+  // as many as the registers allow: by a hair, 4 to 13 of them spilled with
+  // head_dim 256 and 5 to 28 with 32 rows of 128 in two pieces
   static constexpr int kWavesPerSimd = D > 128 ? (kQ > 1 ? 1 : 2) : (kTiles == 2 || kQ > 1 ? 2 : 3);
 };
 

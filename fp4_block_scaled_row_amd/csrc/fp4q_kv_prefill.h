@@ -9,13 +9,14 @@
 // operand, the left one being the values read transposed.
 //
 // Bound by matrix and vector instructions, which overlap only between a SIMD's
-// two waves: 64 tokens x 32 rows x 128 elements are 1024 cycles of the ones and
-// about 1150 of the others (a third of them exponentials) a wave.  4 x 1000
-// queries of 40 heads over up to 16000 tokens, MXFP4: 810 us, 930 TFLOP/s (a
-// large library product reaches 1190); 4096 queries of 32 heads over as many
-// tokens, NVFP4, rotated queries in two pieces, whose second is as much matrix
-// work again as half of the rest: 229 us, 600, where blocks that see half of a
-// step and the ends of blocks weigh more.  Products of the next step's scores between
+// two waves (42 % and 44 % of the cycles in the first of the calls below, 47 % and
+// 44 % in the second): 64 tokens x 32 rows x 128 elements are 1024 cycles of the
+// ones and about 1150 of the others (a third of them exponentials) a wave.
+// 4 x 1000 queries of 40 heads over up to 16000 tokens, MXFP4: 810 us, 930
+// TFLOP/s (a large library product reaches 1190); 4096 queries of 32 heads over
+// as many tokens, NVFP4, rotated, so that queries in two pieces make the first
+// product twice as long: 230 us, 600, where blocks that see half of a step and
+// the ends of blocks weigh more too.  Products of the next step's scores between
 // this one's exponentials in an order fixed by the source, with three steps in
 // LDS, were no faster (830 us for 785).
 //
@@ -100,7 +101,7 @@ __device__ __forceinline__ float wave_queries(const KvAttendLaunch& a, const KvU
     }
   }
   float factor = fabsf(a.scale) * kLog2e * (FMT == 1 ? *a.p.kg : 1.0f), up = a.scale < 0.0f ? -1.0f : 1.0f;
-  if constexpr (kv_scaled_rows<FMT, kQ>()) {
+  if constexpr (kv_scaled_rows<FMT>()) {
     uint32_t most = 0u;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) most = max(most, abs_max_bits8(v[c]));
