@@ -58,6 +58,23 @@ def test_error_by_the_outputs_own_size(fq, fmt, dim, rotate, dtype, q_scale, len
         x / rms(want) for x in (error, own, bound))
 
 
+@pytest.mark.parametrize("fmt,dim,rotate", [("nvfp4", 128, True), ("nvfp4", 128, False), ("mxfp4", 128, True), ("mxfp4", 256, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [32, 64])
+@pytest.mark.parametrize("lens,new,q_heads", [SHAPES[0], SHAPES[1], ([20000], [1], 32), ([900] * 24, [1] * 24, 32)])
+def test_error_with_pages_of_whole_tiles(fq, fmt, dim, rotate, dtype, page, lens, new, q_heads):  # noqa: F811
+    """As above where a wave's 32 tokens lie in one page, up to 32 rows a cache head."""
+    case = Case(fq, fmt, dim, 1 if len(lens) == 1 else 2, lens, page, seed=page + dim)
+    q = (1.5 * torch.from_numpy(case.rng.standard_normal((sum(new), q_heads, dim)))).to(DT[dtype])
+    print("attention", fmt, dim, rotate, dtype, page, lens, new, q_heads, flush=True)
+    got = call(case, q, new, rotate).double().cpu().numpy()
+    want = wanted(case, q, new, rotate)
+    own = rms(torch.from_numpy(want).to(DT[dtype]).double().numpy() - want)
+    error, bound = rms(got - want), (own ** 2 + (ON_TOP[dtype] * rms(want)) ** 2) ** 0.5
+    assert error <= bound, "off by %g of the outputs, own rounding %g, bound %g" % tuple(
+        x / rms(want) for x in (error, own, bound))
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("dim", [128, 256])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
