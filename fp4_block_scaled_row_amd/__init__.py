@@ -18,12 +18,17 @@ Formats (pages cited by title and section):
   * Paged key/value cache in NVFP4 or MXFP4: quantizing new tokens into it,
     reading it back, attention over it (section 3, the rotated
     NVFP4 KV cache).
+  * Linear layers over 4-bit weights with activations of 8, 16 or 32 bits, the
+    gated pair of a feed-forward block, root-mean-square norm with the residual
+    and MXFP8 output, and their gradients.
 """
 from collections import namedtuple
 
 import torch
 
 from . import _lib
+from ._ffn import (Fp4Weight, Mx8Result, NormResult, fp4_gated, fp4_gated_backward, fp4_linear, fp4_linear_backward,
+                   fp4_weight, rms_norm, rms_norm_backward)
 from ._lib import Fp4qError, load  # noqa: F401
 from ._kv import (KvCache, kv_cache, kv_cache_attention, kv_cache_attention_workspace_bytes, kv_cache_read,
                   kv_cache_write)
@@ -32,6 +37,8 @@ __all__ = [
     "quantize_mxfp4", "quantize_nvfp4", "silu_mul_fwht_mxfp4", "fwht", "dequantize", "mxfp4_gemm",
     "KvCache", "kv_cache", "kv_cache_write", "kv_cache_read", "kv_cache_attention",
     "kv_cache_attention_workspace_bytes",
+    "Fp4Weight", "fp4_weight", "fp4_linear", "fp4_linear_backward", "fp4_gated", "fp4_gated_backward",
+    "Mx8Result", "NormResult", "rms_norm", "rms_norm_backward",
     "workspace_bytes",
     "check_counters", "version", "MxResult", "NvResult", "Fp4qError",
 ]
@@ -246,11 +253,11 @@ def fwht(x, transform_size=None, random_signs=False, seed=0, out=None):
 
 def dequantize(fmt, codes, scales, global_scale=None, out_dtype=torch.float32, out=None):
     """Reconstruct [rows, cols] from packed codes and block scales.  fmt is
-    "mxfp4", "nvfp4" or "if4" (the latter two need the fp32 global_scale tensor)."""
-    f = {"mxfp4": _lib.FP4Q_MXFP4, "nvfp4": _lib.FP4Q_NVFP4, "if4": _lib.FP4Q_IF4}[fmt]
-    rows, half = codes.shape
-    cols = half * 2
-    block = 32 if f == _lib.FP4Q_MXFP4 else 16
+    "mxfp4", "nvfp4" or "if4" (the latter two need the fp32 global_scale tensor),
+    or "mxfp8" (codes [rows, cols], E4M3)."""
+    f = {"mxfp4": _lib.FP4Q_MXFP4, "nvfp4": _lib.FP4Q_NVFP4, "if4": _lib.FP4Q_IF4, "mxfp8": _lib.FP4Q_MXFP8}[fmt]
+    rows, cols = codes.shape[0], codes.shape[1] * (1 if fmt == "mxfp8" else 2)
+    block = 32 if fmt in ("mxfp4", "mxfp8") else 16
     _check_buf(codes, None, torch.uint8, "codes")
     _check_buf(scales, (rows, cols // block), torch.uint8, "scales")
     if global_scale is not None:

@@ -14,17 +14,20 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("FP4Q_LIB") or os.path.join(HERE, "libfp4q.so")
 
 FP4Q_OK, FP4Q_ERR_INVALID_ARG, FP4Q_ERR_UNSUPPORTED, FP4Q_ERR_WORKSPACE, FP4Q_ERR_NONFINITE, FP4Q_ERR_HIP = range(6)
-FP4Q_F32, FP4Q_BF16 = 0, 1
-FP4Q_MXFP4, FP4Q_NVFP4, FP4Q_IF4 = 0, 1, 2
+FP4Q_F32, FP4Q_BF16, FP4Q_E4M3 = 0, 1, 2
+FP4Q_MXFP4, FP4Q_NVFP4, FP4Q_IF4, FP4Q_MXFP8 = 0, 1, 2, 4
 FP4Q_SCALE_OCP_MAX, FP4Q_SCALE_MANUAL, FP4Q_SCALE_NV_MAX6, FP4Q_SCALE_FOUR_OVER_SIX, FP4Q_SCALE_IF4 = 0, 1, 2, 3, 4
 FP4Q_ROUND_RNE, FP4Q_ROUND_STOCHASTIC = 0, 1
 FP4Q_ROT_NONE, FP4Q_ROT_FWHT_ROW, FP4Q_ROT_RHT16, FP4Q_ROT_FWHT128 = 0, 1, 2, 3
+FP4Q_LINEAR, FP4Q_GATED, FP4Q_LINEAR_BACKWARD = 0, 1, 2
 
 EXPORTED = [
     "fp4q_workspace_bytes", "fp4q_quantize_mxfp4", "fp4q_quantize_nvfp4", "fp4q_quantize_nvfp4_noalloc",
     "fp4q_silu_mul_fwht_mxfp4", "fp4q_fwht",
     "fp4q_dequantize", "fp4q_mxfp4_gemm",
     "fp4q_kv_write", "fp4q_kv_read", "fp4q_kv_attention", "fp4q_kv_attention_workspace_bytes",
+    "fp4q_linear", "fp4q_gated", "fp4q_linear_backward", "fp4q_linear_workspace_bytes", "fp4q_gated_grad",
+    "fp4q_rms_norm", "fp4q_rms_norm_backward", "fp4q_rms_norm_backward_workspace_bytes",
     "fp4q_check_counters", "fp4q_status_string", "fp4q_version",
 ]
 
@@ -81,6 +84,47 @@ class KvAttentionArgs(C.Structure):
     ]
 
 
+class WeightArgs(C.Structure):
+    _fields_ = [
+        ("format", C.c_int32), ("n", C.c_int64), ("k", C.c_int64),
+        ("codes", C.c_void_p), ("scales", C.c_void_p), ("global_scale", C.c_void_p),
+    ]
+
+
+class LinearArgs(C.Structure):
+    _fields_ = [
+        ("x", C.c_void_p), ("x_scales", C.c_void_p), ("rows", C.c_int64), ("x_stride", C.c_int64),
+        ("x_dtype", C.c_int32), ("out_dtype", C.c_int32),
+        ("bias", C.c_void_p), ("out", C.c_void_p), ("products", C.c_void_p), ("products_dtype", C.c_int32),
+    ]
+
+
+class GatedGradArgs(C.Structure):
+    _fields_ = [
+        ("dh", C.c_void_p), ("products", C.c_void_p), ("dproducts", C.c_void_p),
+        ("rows", C.c_int64), ("f", C.c_int64), ("dh_stride", C.c_int64), ("dtype", C.c_int32),
+        ("products_dtype", C.c_int32),
+    ]
+
+
+class RmsNormArgs(C.Structure):
+    _fields_ = [
+        ("x", C.c_void_p), ("residual", C.c_void_p), ("x_stride", C.c_int64), ("residual_stride", C.c_int64),
+        ("weight", C.c_void_p), ("y", C.c_void_p), ("summed", C.c_void_p), ("rstd", C.c_void_p),
+        ("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("d", C.c_int64),
+        ("dtype", C.c_int32), ("weight_dtype", C.c_int32), ("eps", C.c_float),
+    ]
+
+
+class RmsNormGradArgs(C.Structure):
+    _fields_ = [
+        ("dy", C.c_void_p), ("s", C.c_void_p), ("ds", C.c_void_p),
+        ("dy_stride", C.c_int64), ("s_stride", C.c_int64), ("ds_stride", C.c_int64),
+        ("weight", C.c_void_p), ("rstd", C.c_void_p), ("dx", C.c_void_p), ("dw", C.c_void_p),
+        ("rows", C.c_int64), ("d", C.c_int64), ("dtype", C.c_int32), ("weight_dtype", C.c_int32),
+    ]
+
+
 class Fp4qError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -129,6 +173,20 @@ def load():
         lib.fp4q_kv_attention_workspace_bytes.restype = C.c_size_t
         lib.fp4q_kv_attention.argtypes = [kvp, C.POINTER(KvAttentionArgs), vp, C.c_size_t, vp]
         lib.fp4q_kv_attention.restype = C.c_int
+        wp, lp = C.POINTER(WeightArgs), C.POINTER(LinearArgs)
+        for call in (lib.fp4q_linear, lib.fp4q_gated, lib.fp4q_linear_backward):
+            call.argtypes = [wp, lp, vp, C.c_size_t, vp]
+            call.restype = C.c_int
+        lib.fp4q_linear_workspace_bytes.argtypes = [wp, lp, i32]
+        lib.fp4q_linear_workspace_bytes.restype = C.c_size_t
+        lib.fp4q_gated_grad.argtypes = [C.POINTER(GatedGradArgs), vp]
+        lib.fp4q_gated_grad.restype = C.c_int
+        lib.fp4q_rms_norm.argtypes = [C.POINTER(RmsNormArgs), vp]
+        lib.fp4q_rms_norm.restype = C.c_int
+        lib.fp4q_rms_norm_backward.argtypes = [C.POINTER(RmsNormGradArgs), vp, C.c_size_t, vp]
+        lib.fp4q_rms_norm_backward.restype = C.c_int
+        lib.fp4q_rms_norm_backward_workspace_bytes.argtypes = [C.POINTER(RmsNormGradArgs)]
+        lib.fp4q_rms_norm_backward_workspace_bytes.restype = C.c_size_t
         lib.fp4q_check_counters.argtypes = [vp]
         lib.fp4q_check_counters.restype = C.c_int
         lib.fp4q_status_string.argtypes = [C.c_int]

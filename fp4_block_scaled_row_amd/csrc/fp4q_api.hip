@@ -10,6 +10,7 @@
 
 #include "fp4q.h"
 #include "fp4q_common.h"
+#include "fp4q_ffn.h"
 #include "fp4q_internal.h"
 
 namespace fp4q {
@@ -284,15 +285,20 @@ fp4q_status fp4q_fwht(int64_t rows, int64_t d, int64_t in_row_stride, int32_t in
 fp4q_status fp4q_dequantize(int32_t format, int64_t rows, int64_t cols, int32_t block_size, const uint8_t* codes,
                             const uint8_t* scales, const float* global_scale, int32_t out_dtype, void* out,
                             void* hip_stream) {
-  if (format != FP4Q_MXFP4 && format != FP4Q_NVFP4 && format != FP4Q_IF4) return FP4Q_ERR_INVALID_ARG;
+  if (format != FP4Q_MXFP4 && format != FP4Q_NVFP4 && format != FP4Q_IF4 && format != FP4Q_MXFP8)
+    return FP4Q_ERR_INVALID_ARG;
   if (rows < 0 || cols < 0) return FP4Q_ERR_INVALID_ARG;
   if (out_dtype != FP4Q_F32 && out_dtype != FP4Q_BF16) return FP4Q_ERR_INVALID_ARG;
-  if (block_size != (format == FP4Q_MXFP4 ? 32 : 16)) return FP4Q_ERR_UNSUPPORTED;
+  if (block_size != (format == FP4Q_MXFP4 || format == FP4Q_MXFP8 ? 32 : 16)) return FP4Q_ERR_UNSUPPORTED;
   if (cols % block_size != 0) return FP4Q_ERR_INVALID_ARG;
   if (rows * cols == 0) return FP4Q_OK;
   if (!codes || !scales || !out) return FP4Q_ERR_INVALID_ARG;
-  if (format != FP4Q_MXFP4 && !global_scale) return FP4Q_ERR_INVALID_ARG;
+  if ((format == FP4Q_NVFP4 || format == FP4Q_IF4) && !global_scale) return FP4Q_ERR_INVALID_ARG;
   if (!aligned(codes, 4) || !aligned(out, 16)) return FP4Q_ERR_UNSUPPORTED;
+  if (format == FP4Q_MXFP8) {
+    const Dequant8Launch d8 = {codes, scales, rows, cols, out_dtype == FP4Q_F32 ? kF32 : kBF16, out};
+    return hip_status(launch_dequant8(d8, static_cast<hipStream_t>(hip_stream)));
+  }
   DequantLaunch dl;
   dl.format = format == FP4Q_MXFP4 ? 0 : (format == FP4Q_NVFP4 ? 1 : 2);
   dl.rows = rows;

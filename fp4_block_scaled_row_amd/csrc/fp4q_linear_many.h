@@ -1,0 +1,374 @@
+// fp4q_linear_many.h -- products of many rows of activations with a 4-bit
+// weight: y = x W^T, h = SiLU(x Wg^T) * (x Wu^T) and dx = dy W, in tiles.
+//
+// A workgroup computes BM rows of activations by BN outputs in stages of 64 of
+// the contraction.  A stage's activations go to LDS as bf16 (fp32 ones as three
+// planes of pieces), its weights as the codes they are, an eighth of the bytes
+// of x: each wave turns the codes that it needs into bf16 in registers.  Loads of
+// a stage are in flight while the one before it is multiplied.
+//
+// v_mfma_f32_16x16x32_bf16, weights as the left operand, so that a lane ends up
+// with consecutive outputs of one row.  The order of the contraction inside a
+// stage is free:
+//  - y = x W^T (contraction over k): lane group g = lane / 16 takes k = 16 g .. +
+//    15 of the stage, 8 bytes of codes with one scale, in two instructions.
+//  - dx = dy W (contraction over the weight's rows): a lane needs 8 rows' codes
+//    of one column.  It reads 4 bytes, 8 columns, of each of those rows, whose
+//    scales differ, converts them row by row, and pairs neighbouring rows'
+//    values: instruction j then takes columns 8 r + j, r = lane mod 16, and a
+//    lane's outputs are 8 consecutive columns again.
+#pragma once
+
+#include "fp4q_ffn.h"
+
+namespace fp4q {
+
+constexpr int kStage = 64;
+enum ManyMode { kForward = 0, kGated = 1, kTransposed = 2 };
+
+// What a launch of the tile kernel adds to the call: how the contraction is
+// parted, and where parts go.
+struct ManyArgs {
+  LinearLaunch l;
+  int tiles_m, tiles_n, ntiles;
+  int splits, stages, per_split;   // stages of the contraction, of one part
+};
+
+template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
+struct ManyTile {
+  static constexpr int kThreads = 64 * WM * WN;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  static constexpr int P = kPieces<XT>;
+  static constexpr int kBlock = FMT == 0 ? 32 : 16;
+  static constexpr bool kT = MODE == kTransposed;
+  static constexpr int kXBytes = P * BM * 2 * kStage;
+  // codes: rows of 32 bytes; transposed, rows of BN / 2 with a pad each 8 rows
+  // that spreads the 4 lane groups' reads over the banks
+  static constexpr int kWPitch = kT ? BN / 2 : kStage / 2;
+  static constexpr int kWBytes = kT ? kStage * kWPitch + kStage / 8 * 64 : BN * kWPitch;
+  // scales: by row; transposed, by block of columns, a byte for each row
+  static constexpr int kSPitch = kT ? kStage + 8 : kStage / kBlock;
+  static constexpr int kSBytes = kT ? BN / kBlock * kSPitch : BN * kSPitch;
+  static constexpr int kBuf = (kXBytes + kWBytes + kSBytes + 15) / 16 * 16;
+  static constexpr int kXPer = BM * 8 / kThreads;                                // 8-element pieces a thread
+  static constexpr int kWPer = (kT ? kStage * (BN / 32) : BN * 2) / kThreads;    // 16-byte pieces
+  static_assert(kXPer * kThreads == BM * 8 && kWPer >= 1, "whole pieces");
+  static_assert(!kT || TN == 128, "a wave takes 8 columns a lane");
+  static_assert(MODE != kGated || FN % 2 == 0, "both factors in a wave");
+};
+
+template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void many_kernel(ManyArgs a) {
+  using T = ManyTile<FMT, XT, MODE, BM, BN, WM, WN>;
+  constexpr int kElem = XT == kXF32 ? 4 : XT == kXBF16 ? 2 : 1;
+  constexpr int P = T::P, FM = T::FM, FN = T::FN;
+  __shared__ __align__(16) uint8_t s_buf[2][T::kBuf];
+  const LinearLaunch& l = a.l;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int wm = wave / WN, wn = wave % WN;
+
+  // workgroup w runs on XCD w mod 8: each XCD walks a contiguous range of tiles,
+  // in groups of 4 tile rows column by column, so that its L2 serves both sides
+  const int w = blockIdx.x, per = (a.ntiles + 7) / 8;
+  const int tile = (w % 8) * per + w / 8;
+  if (tile >= a.ntiles || w / 8 >= per) return;
+  const int group = tile / (4 * a.tiles_n), first = group * 4;
+  const int gsize = min(a.tiles_m - first, 4), in_g = tile - group * 4 * a.tiles_n;
+  const int64_t m0 = (int64_t)(first + in_g % gsize) * BM;
+  const int64_t half = l.w.n / 2;
+  const int64_t o0 = (int64_t)(in_g / gsize) * (MODE == kGated ? BN / 2 : BN);   // first output column
+
+  const int64_t K = l.w.k, srow = K / T::kBlock;
+  const int64_t len = T::kT ? l.w.n : K;                // of the contraction
+  const int s0 = blockIdx.y * a.per_split, s1 = min(a.stages, s0 + a.per_split);
+
+  // ---- loads of a stage: global memory to registers, registers to LDS
+  uint32_t xr[T::kXPer][XT == kXF32 ? 8 : XT == kXBF16 ? 4 : 3];
+  u32x4_t wr[T::kWPer];
+  uint32_t wsr[T::kWPer];
+  auto load_x = [&](int64_t at) {
+#pragma unroll
+    for (int i = 0; i < T::kXPer; ++i) {
+      const int q = tid + i * T::kThreads, row = q >> 3;
+      const int64_t kk = at + (q & 7) * 8, m = min(m0 + row, l.rows - 1);
+      const uint8_t* p = static_cast<const uint8_t*>(l.x) + (m * l.x_stride + kk) * kElem;
+      if (kk + 8 <= len) {
+        if constexpr (XT == kXF32) {
+          const u32x4_t v = load_any<u32x4_t>(p), u = load_any<u32x4_t>(p + 16);
+          xr[i][0] = v.x; xr[i][1] = v.y; xr[i][2] = v.z; xr[i][3] = v.w;
+          xr[i][4] = u.x; xr[i][5] = u.y; xr[i][6] = u.z; xr[i][7] = u.w;
+        } else if constexpr (XT == kXBF16) {
+          const u32x4_t v = load_any<u32x4_t>(p);
+          xr[i][0] = v.x; xr[i][1] = v.y; xr[i][2] = v.z; xr[i][3] = v.w;
+        } else {
+          const u32x2_t v = load_any<u32x2_t>(p);
+          xr[i][0] = v.x; xr[i][1] = v.y;
+          xr[i][2] = l.x_scales[m * (K / 32) + (kk >> 5)];
+        }
+      } else {   // the end of a row; only rows of gradients end inside a piece
+#pragma unroll
+        for (int e = 0; e < (XT == kXF32 ? 8 : XT == kXBF16 ? 4 : 3); ++e) xr[i][e] = 0u;
+        if constexpr (XT == kXF32) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (kk + e < len) xr[i][e] = load_any<uint32_t>(p + 4 * e);
+        } else if constexpr (XT == kXBF16) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (kk + e < len) xr[i][e >> 1] |= (uint32_t)load_any<uint16_t>(p + 2 * e) << (16 * (e & 1));
+        }
+      }
+    }
+  };
+  auto load_w = [&](int64_t at) {
+#pragma unroll
+    for (int i = 0; i < T::kWPer; ++i) {
+      const int q = tid + i * T::kThreads;
+      wr[i] = u32x4_t{0u, 0u, 0u, 0u};
+      wsr[i] = 0u;
+      int64_t n, k;
+      if constexpr (T::kT) {
+        n = at + q / (BN / 32);
+        k = o0 + (q % (BN / 32)) * 32;
+        if (n >= l.w.n) continue;                       // rows that the contraction does not have
+      } else {
+        const int row = q >> 1;
+        k = at + (q & 1) * 32;
+        if constexpr (MODE == kGated) {
+          const int f = (row % T::TN) / 16;
+          n = min(o0 + (row / T::TN) * (T::TN / 2) + (f % (FN / 2)) * 16 + (row & 15), half - 1) + (f >= FN / 2 ? half : 0);
+        } else {
+          n = min(o0 + row, l.w.n - 1);
+        }
+      }
+      const uint8_t* c = l.w.codes + n * (K / 2) + (k >> 1);
+      const uint8_t* s = l.w.scales + n * srow + k / T::kBlock;
+      if (k + 32 <= K) {
+        wr[i] = load_any<u32x4_t>(c);
+        wsr[i] = FMT == 0 ? *s : load_any<uint16_t>(s);
+      } else if (FMT == 1 && k + 16 <= K) {
+        const u32x2_t v = load_any<u32x2_t>(c);
+        wr[i].x = v.x;
+        wr[i].y = v.y;
+        wsr[i] = *s;
+      }
+    }
+  };
+  auto commit = [&](uint8_t* buf) {
+    uint8_t* bw = buf + T::kXBytes;
+    uint8_t* bs = bw + T::kWBytes;
+#pragma unroll
+    for (int i = 0; i < T::kXPer; ++i) {
+      const int q = tid + i * T::kThreads, row = q >> 3, ch = (q & 7) ^ (row & 7);
+      u32x4_t o[P];
+      if constexpr (XT == kXF32) split8(xr[i], o);
+      else if constexpr (XT == kXBF16) o[0] = u32x4_t{xr[i][0], xr[i][1], xr[i][2], xr[i][3]};
+      else o[0] = e4m3_values8(u32x2_t{xr[i][0], xr[i][1]}, xr[i][2]);
+#pragma unroll
+      for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4_t*>(buf + (p * BM + row) * 128 + ch * 16) = o[p];
+    }
+#pragma unroll
+    for (int i = 0; i < T::kWPer; ++i) {
+      const int q = tid + i * T::kThreads;
+      if constexpr (T::kT) {
+        const int n = q / (BN / 32), pc = q % (BN / 32);
+        *reinterpret_cast<u32x4_t*>(bw + n * T::kWPitch + (n >> 3) * 64 + pc * 16) = wr[i];
+        if constexpr (FMT == 0) {
+          bs[pc * T::kSPitch + n] = (uint8_t)wsr[i];
+        } else {
+          bs[2 * pc * T::kSPitch + n] = (uint8_t)wsr[i];
+          bs[(2 * pc + 1) * T::kSPitch + n] = (uint8_t)(wsr[i] >> 8);
+        }
+      } else {
+        *reinterpret_cast<u32x4_t*>(bw + q * 16) = wr[i];
+        if constexpr (FMT == 0) bs[q] = (uint8_t)wsr[i];
+        else *reinterpret_cast<uint16_t*>(bs + 2 * q) = (uint16_t)wsr[i];
+      }
+    }
+  };
+
+  f32x4_t acc[FN][FM];
+#pragma unroll
+  for (int n = 0; n < FN; ++n)
+#pragma unroll
+    for (int m = 0; m < FM; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto multiply = [&](const uint8_t* buf) {
+    const uint8_t* bw = buf + T::kXBytes;
+    const uint8_t* bs = bw + T::kWBytes;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      u32x4_t wf[FN];
+      if constexpr (T::kT) {
+        const uint8_t* c0 = bw + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * 64 + 4 * r;
+        const u32x2_t sb = *reinterpret_cast<const u32x2_t*>(
+            bs + (wn * (128 / T::kBlock) + 8 * r / T::kBlock) * T::kSPitch + 32 * t + 8 * g);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {     // rows i and i + 1 of this lane's 8
+          const uint32_t ca = *reinterpret_cast<const uint32_t*>(c0 + i * T::kWPitch);
+          const uint32_t cb = *reinterpret_cast<const uint32_t*>(c0 + (i + 1) * T::kWPitch);
+          const uint32_t sw = i < 4 ? sb.x : sb.y;
+          const float sa = scale_operand<FMT>((sw >> (8 * (i & 3))) & 0xFFu);
+          const float sc = scale_operand<FMT>((sw >> (8 * (i & 3) + 8)) & 0xFFu);
+          const u32x4_t va = weights8<FMT>(ca, sa), vb = weights8<FMT>(cb, sc);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            wf[2 * j][i >> 1] = __builtin_amdgcn_perm(vb[j], va[j], 0x05040100u);
+            wf[2 * j + 1][i >> 1] = __builtin_amdgcn_perm(vb[j], va[j], 0x07060302u);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+          const int row = wn * T::TN + 16 * n + r;
+          const uint32_t c = *reinterpret_cast<const uint32_t*>(bw + row * T::kWPitch + 8 * g + 4 * t);
+          const uint32_t s = bs[row * T::kSPitch + (FMT == 0 ? g >> 1 : g)];
+          wf[n] = weights8<FMT>(c, scale_operand<FMT>(s));
+        }
+      }
+      // this lane's 8 of the contraction: chunk 4 t + g where groups take runs of
+      // 8 (transposed), 2 g + t where they take runs of 16
+      const int chunk = T::kT ? 4 * t + g : 2 * g + t;
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+        const int row = wm * T::TM + 16 * m + r;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const u32x4_t xf = *reinterpret_cast<const u32x4_t*>(buf + (p * BM + row) * 128 + ((chunk ^ (row & 7)) * 16));
+#pragma unroll
+          for (int n = 0; n < FN; ++n) acc[n][m] = mfma16(wf[n], xf, acc[n][m]);
+        }
+      }
+    }
+  };
+
+  if (s0 < s1) {
+    load_x((int64_t)s0 * kStage);
+    load_w((int64_t)s0 * kStage);
+    commit(s_buf[0]);
+    __syncthreads();
+    for (int s = s0; s < s1; ++s) {
+      const int b = (s - s0) & 1;
+      if (s + 1 < s1) {
+        load_x((int64_t)(s + 1) * kStage);
+        load_w((int64_t)(s + 1) * kStage);
+      }
+      multiply(s_buf[b]);
+      if (s + 1 < s1) commit(s_buf[b ^ 1]);
+      __syncthreads();
+    }
+  }
+
+  // ---- results
+  const int64_t cols = T::kT ? K : l.w.n;               // of the sums
+  // 4 consecutive outputs, or the first `count`
+  auto put4 = [&](void* to, int64_t at, f32x4_t v, int count, int bf16) {
+    if (bf16) {
+      __bf16* o = static_cast<__bf16*>(to) + at;
+      if (count >= 4) {
+        store_any(o, u32x2_t{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
+      } else {
+        for (int i = 0; i < count; ++i) o[i] = (__bf16)v[i];
+      }
+    } else {
+      float* o = static_cast<float*>(to) + at;
+      if (count >= 4) {
+        store_any(o, v);
+      } else {
+        for (int i = 0; i < count; ++i) o[i] = v[i];
+      }
+    }
+  };
+  const float tensor = FMT == 1 ? *l.w.g : 1.0f;
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const int64_t row = m0 + wm * T::TM + 16 * m + r;
+    if (row >= l.rows) continue;
+    if constexpr (T::kT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t k = o0 + wn * 128 + 8 * (4 * g + i);
+        if (k >= K) continue;                           // (K is a multiple of 8)
+        const f32x4_t a0 = {acc[0][m][i], acc[1][m][i], acc[2][m][i], acc[3][m][i]};
+        const f32x4_t a1 = {acc[4][m][i], acc[5][m][i], acc[6][m][i], acc[7][m][i]};
+        if (a.splits > 1) {
+          float* o = l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + k;
+          store_any(o, a0);
+          store_any(o + 4, a1);
+        } else {
+          put4(l.out, row * K + k, a0 * tensor, 4, l.out_bf16);
+          put4(l.out, row * K + k + 4, a1 * tensor, 4, l.out_bf16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < (MODE == kGated ? FN / 2 : FN); ++n) {
+        const int64_t side = MODE == kGated ? half : l.w.n;
+        const int64_t col = o0 + wn * (MODE == kGated ? T::TN / 2 : T::TN) + 16 * n + 4 * g;
+        const int count = (int)min(side - col, (int64_t)4);
+        if (count <= 0) continue;
+        f32x4_t v = acc[n][m], u = acc[MODE == kGated ? n + FN / 2 : n][m];
+        if (a.splits > 1) {
+          float* o = l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + col;
+          for (int i = 0; i < count; ++i) o[i] = v[i];
+          if constexpr (MODE == kGated)
+            for (int i = 0; i < count; ++i) o[half + i] = u[i];
+          continue;
+        }
+        v *= tensor;
+        if constexpr (MODE == kGated) {
+          u *= tensor;
+          if (l.products) {
+            put4(l.products, row * l.w.n + col, v, count, l.products_bf16);
+            put4(l.products, row * l.w.n + half + col, u, count, l.products_bf16);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
+          put4(l.out, row * half + col, v, count, l.out_bf16);
+        } else {
+          if (l.bias) {
+            for (int i = 0; i < count; ++i)
+              v[i] += l.out_bf16 ? (float)static_cast<const __bf16*>(l.bias)[col + i]
+                                 : static_cast<const float*>(l.bias)[col + i];
+          }
+          put4(l.out, row * l.w.n + col, v, count, l.out_bf16);
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
+hipError_t launch_many_t(const ManyArgs& a, hipStream_t s) {
+  using T = ManyTile<FMT, XT, MODE, BM, BN, WM, WN>;
+  hipLaunchKernelGGL((many_kernel<FMT, XT, MODE, BM, BN, WM, WN>), dim3((a.ntiles + 7) / 8 * 8, a.splits),
+                     dim3(T::kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+// Instances, by format and direction (fp4q_linear_many_*.hip); `size`: 0 the
+// small tiles, 1 the large ones.
+struct ManySize {
+  int bm, bn;
+};
+hipError_t launch_many_mx(const ManyArgs& a, int size, hipStream_t s);
+hipError_t launch_many_nv(const ManyArgs& a, int size, hipStream_t s);
+hipError_t launch_many_back_mx(const ManyArgs& a, int size, hipStream_t s);
+hipError_t launch_many_back_nv(const ManyArgs& a, int size, hipStream_t s);
+
+// Tiles: of 8 waves where there are enough of them, of 4 waves else.  fp32
+// activations take three times the LDS and half the rows.
+constexpr ManySize many_size(int x_type, int size) {
+  return size == 0 ? ManySize{64, 128} : x_type == kXF32 ? ManySize{128, 256} : ManySize{256, 256};
+}
+
+template <int FMT, int XT, int MODE>
+hipError_t launch_many_size(const ManyArgs& a, int size, hipStream_t s) {
+  constexpr bool t = MODE == kTransposed;
+  if (size == 0) return launch_many_t<FMT, XT, MODE, 64, 128, t ? 4 : 2, t ? 1 : 2>(a, s);
+  constexpr int BM = many_size(XT, 1).bm;
+  return launch_many_t<FMT, XT, MODE, BM, 256, t ? 4 : 2, t ? 2 : 4>(a, s);
+}
+
+}  // namespace fp4q

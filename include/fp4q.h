@@ -82,8 +82,10 @@ typedef enum {
   FP4Q_ERR_HIP = 5           /* a HIP launch or runtime call failed */
 } fp4q_status;
 
-enum { FP4Q_F32 = 0, FP4Q_BF16 = 1 };                       /* element types */
-enum { FP4Q_MXFP4 = 0, FP4Q_NVFP4 = 1, FP4Q_IF4 = 2 };      /* formats (IF4: dequantize only) */
+enum { FP4Q_F32 = 0, FP4Q_BF16 = 1,                         /* element types */
+       FP4Q_E4M3 = 2 };                                     /* (activations of linear layers: MXFP8 blocks) */
+enum { FP4Q_MXFP4 = 0, FP4Q_NVFP4 = 1, FP4Q_IF4 = 2,        /* formats (IF4: dequantize only) */
+       FP4Q_MXFP8 = 4 };                                    /* (fp4q_rms_norm's output; dequantize) */
 enum {
   FP4Q_SCALE_OCP_MAX = 0,        /* MX: e = floor(log2(amax/4)), clamp [-127,127], amax 0 -> 0 */
   FP4Q_SCALE_MANUAL = 1,         /* MX: e = manual_exponent for every block, in [-127, 127]   */
@@ -237,7 +239,8 @@ fp4q_status fp4q_fwht(int64_t rows, int64_t d, int64_t in_row_stride, int32_t in
  * blocks as NV.  A NaN scale code (low 7 bits 0x7F for NV and IF4) gives NaN
  * for its block.  format FP4Q_MXFP4 (block 32), FP4Q_NVFP4 or FP4Q_IF4
  * (block 16, global_scale: device pointer to g); out_dtype FP4Q_F32 or
- * FP4Q_BF16; out is [rows][cols]. */
+ * FP4Q_BF16; out is [rows][cols].  FP4Q_MXFP8 (block 32): codes are [rows][cols]
+ * E4M3 bytes, value * 2^(b-127), exact (rounded where bf16 is subnormal). */
 fp4q_status fp4q_dequantize(int32_t format, int64_t rows, int64_t cols, int32_t block_size,
                             const uint8_t *codes, const uint8_t *scales,
                             const float *global_scale, int32_t out_dtype, void *out,
@@ -382,6 +385,117 @@ size_t fp4q_kv_attention_workspace_bytes(const fp4q_kv_cache *cache, const fp4q_
  * and max_q count here, not the lengths). */
 fp4q_status fp4q_kv_attention(const fp4q_kv_cache *cache, const fp4q_kv_attention_args *args, void *workspace,
                               size_t workspace_bytes, void *hip_stream);
+
+/* Linear layers over 4-bit weights ("Sub-4-Bit Microscaling", section 3: the
+ * projections around the online SiLU_and_Mul rotation; section 2: weights in 4
+ * bits with activations of more), and the norm in front of them.
+ *
+ * A weight [n][k] is the planes that fp4q_quantize_mxfp4 or
+ * fp4q_quantize_nvfp4 (policies NV_MAX6 and FOUR_OVER_SIX) writes for it: codes
+ * [n][k / 2], scales [n][k / block].  n and k: to 2^31 - 1; k a multiple of the
+ * block.  Any n, any alignment.  FP4Q_IF4 is UNSUPPORTED. */
+typedef struct {
+  int32_t format;              /* FP4Q_MXFP4 or FP4Q_NVFP4 */
+  int64_t n, k;
+  const uint8_t *codes, *scales;
+  const float *global_scale;   /* NVFP4: device pointer to the tensor scale g */
+} fp4q_weight;
+
+typedef struct {
+  const void *x;               /* [rows][x_stride] of x_dtype */
+  const uint8_t *x_scales;     /* FP4Q_E4M3: [rows][k / 32] E8M0 bytes; x_stride is then k, k a multiple of 32 */
+  int64_t rows;
+  int64_t x_stride;            /* elements, >= 0 */
+  int32_t x_dtype;             /* FP4Q_F32, FP4Q_BF16 or FP4Q_E4M3 */
+  int32_t out_dtype;           /* FP4Q_F32 or FP4Q_BF16 */
+  const void *bias;            /* fp4q_linear: [n] of out_dtype, or NULL */
+  void *out;                   /* dense, of out_dtype */
+  void *products;              /* fp4q_gated: [rows][n] of products_dtype, or NULL */
+  int32_t products_dtype;      /* FP4Q_F32 or FP4Q_BF16 (looked at with products) */
+} fp4q_linear_args;
+
+enum { FP4Q_LINEAR = 0, FP4Q_GATED = 1, FP4Q_LINEAR_BACKWARD = 2 };
+
+/* Bytes of device workspace that a call of this kind uses (0 for arguments it
+ * would refuse; most calls use none), 16-byte aligned.  Its contents before and
+ * after a call mean nothing; calls that overlap on the GPU need one each. */
+size_t fp4q_linear_workspace_bytes(const fp4q_weight *weight, const fp4q_linear_args *args, int32_t kind);
+
+/* out [rows][n] = x W^T + bias.  Weights and activations enter exactly, sums are
+ * fp32 in an order that the shapes fix (a call gives the same bits each time),
+ * the tensor scale and the bias are applied in fp32, and the result is rounded
+ * once.  A NaN scale makes its terms NaN. */
+fp4q_status fp4q_linear(const fp4q_weight *weight, const fp4q_linear_args *args, void *workspace,
+                        size_t workspace_bytes, void *hip_stream);
+
+/* out [rows][n / 2] = SiLU(g) * u, SiLU(g) = g / (1 + e^-g), with [g | u] = x W^T:
+ * the weight's first n / 2 rows give g, the others u (n even).  `products`
+ * receives [g | u] for the backward pass: the fp32 sums that the result is
+ * computed from, or their rounding to bf16. */
+fp4q_status fp4q_gated(const fp4q_weight *weight, const fp4q_linear_args *args, void *workspace,
+                       size_t workspace_bytes, void *hip_stream);
+
+/* out [rows][k] = x W, x [rows][x_stride] being the gradient of a linear layer's
+ * output (FP4Q_F32 or FP4Q_BF16, row length n). */
+fp4q_status fp4q_linear_backward(const fp4q_weight *weight, const fp4q_linear_args *args, void *workspace,
+                                 size_t workspace_bytes, void *hip_stream);
+
+typedef struct {
+  const void *dh;              /* [rows][dh_stride]: gradient of fp4q_gated's out, row length f */
+  const void *products;        /* [rows][2 f], as fp4q_gated wrote them */
+  void *dproducts;             /* [rows][2 f] of dtype: their gradients (may be `products`, of the same type) */
+  int64_t rows, f;
+  int64_t dh_stride;           /* elements, >= 0 */
+  int32_t dtype;               /* FP4Q_F32 or FP4Q_BF16, of dh and dproducts */
+  int32_t products_dtype;
+} fp4q_gated_grad_args;
+
+/* dproducts = [dh u s (1 + g (1 - s)) | dh g s], s = 1 / (1 + e^-g): what
+ * fp4q_linear_backward turns into the gradient of x, and x and it into that of
+ * adapters.  In fp32, rounded once. */
+fp4q_status fp4q_gated_grad(const fp4q_gated_grad_args *args, void *hip_stream);
+
+typedef struct {
+  const void *x, *residual;    /* [rows][stride] of dtype; residual may be NULL */
+  int64_t x_stride, residual_stride;   /* elements, >= 0 */
+  const void *weight;          /* [d] of weight_dtype */
+  void *y;                     /* [rows][d] of dtype, or NULL with codes */
+  void *summed;                /* with residual: [rows][d] of dtype (may be x or residual where those are dense) */
+  float *rstd;                 /* [rows] or NULL */
+  uint8_t *codes, *scales;     /* MXFP8 output: [rows][d] E4M3, [rows][d / 32] E8M0; NULL with y */
+  int64_t rows, d;             /* d to 32768; a multiple of 32 for MXFP8 */
+  int32_t dtype, weight_dtype; /* FP4Q_F32 or FP4Q_BF16 */
+  float eps;                   /* >= 0, finite */
+} fp4q_rms_norm_args;
+
+/* s = x + residual rounded to dtype (x without one), r = 1 / sqrt(mean(s^2) +
+ * eps), y = s r weight in fp32, rounded once to dtype or to MXFP8: blocks of 32
+ * with the scale 2^(floor(log2(largest)) - 8) (the OCP max rule for E4M3;
+ * exponents clamp at -127, an all-zero block has 2^0), elements rounded to
+ * nearest even, past 448 to 448; a block with an infinity or NaN gets the NaN
+ * scale and zero codes. */
+fp4q_status fp4q_rms_norm(const fp4q_rms_norm_args *args, void *hip_stream);
+
+typedef struct {
+  const void *dy, *s, *ds;     /* [rows][stride] of dtype: gradient of y, the normed rows, and the gradient that */
+                               /* reaches s by other ways (added to dx), or NULL */
+  int64_t dy_stride, s_stride, ds_stride;
+  const void *weight;          /* [d] of weight_dtype */
+  const float *rstd;           /* [rows], as fp4q_rms_norm wrote them */
+  void *dx;                    /* [rows][d] of dtype */
+  void *dw;                    /* [d] of weight_dtype */
+  int64_t rows, d;
+  int32_t dtype, weight_dtype;
+} fp4q_rms_norm_grad_args;
+
+/* Bytes of device workspace, 16-byte aligned, contents of no meaning. */
+size_t fp4q_rms_norm_backward_workspace_bytes(const fp4q_rms_norm_grad_args *args);
+
+/* With h = s r and g = dy weight: dx = r (g - h mean(g h)) + ds, the gradient of
+ * s (and so of x and of residual), and dw = sum over rows of dy h, in an order
+ * that the shapes fix.  fp32, rounded once. */
+fp4q_status fp4q_rms_norm_backward(const fp4q_rms_norm_grad_args *args, void *workspace, size_t workspace_bytes,
+                                   void *hip_stream);
 
 /* Host-side check of counters copied back from the device: FP4Q_ERR_NONFINITE
  * when counters[2] != 0, else FP4Q_OK (NULL -> FP4Q_ERR_INVALID_ARG). */
