@@ -30,7 +30,7 @@ ManyArgs many_args(const LinearLaunch& l, int size) {
 }
 
 Plan plan(const LinearLaunch& l) {
-  Plan p = {!l.transposed && l.rows <= 64, 1, 1};
+  Plan p = {!l.transposed && l.rows <= (l.x_type == kXF32 ? 16 : 64), 1, 1};
   if (p.few) return p;
   const int cus = device_cu_count();
   const ManyArgs large = many_args(l, 1);
