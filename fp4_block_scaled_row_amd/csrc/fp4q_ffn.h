@@ -155,6 +155,36 @@ __device__ __forceinline__ u32x4_t weights8(uint32_t codes, float s) {
   return o;
 }
 
+// N codes (2 or 4) of one row and N of the next, each row with its own scale: pair
+// j is column j's two values.
+template <int FMT, int N>
+__device__ __forceinline__ void weight_pairs(uint32_t ca, float sa, uint32_t cb, float sb, uint32_t (&o)[N]) {
+  if constexpr (FMT == 0) {
+    const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ca, sa, 0));
+    const uint32_t b0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cb, sb, 0));
+    o[0] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+    o[1] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+    if constexpr (N == 4) {
+      const uint32_t a1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ca, sa, 1));
+      const uint32_t b1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cb, sb, 1));
+      o[2] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+      o[3] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+    }
+  } else {
+    const float one = e8m0_operand(127u);
+    const float2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ca, one, 0);
+    const float2_t b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cb, one, 0);
+    o[0] = high_halves(as_u(a0.x * sa), as_u(b0.x * sb));
+    o[1] = high_halves(as_u(a0.y * sa), as_u(b0.y * sb));
+    if constexpr (N == 4) {
+      const float2_t a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ca, one, 1);
+      const float2_t b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cb, one, 1);
+      o[2] = high_halves(as_u(a1.x * sa), as_u(b1.x * sb));
+      o[3] = high_halves(as_u(a1.y * sa), as_u(b1.y * sb));
+    }
+  }
+}
+
 // Eight E4M3 codes with one E8M0 scale as bf16 pairs.
 __device__ __forceinline__ u32x4_t e4m3_values8(u32x2_t codes, uint32_t scale) {
   const float s = e8m0_operand(scale);

@@ -13,10 +13,15 @@
 //  - y = x W^T (contraction over k): lane group g = lane / 16 takes k = 16 g .. +
 //    15 of the stage, 8 bytes of codes with one scale, in two instructions.
 //  - dx = dy W (contraction over the weight's rows): a lane needs 8 rows' codes
-//    of one column.  It reads 4 bytes, 8 columns, of each of those rows, whose
-//    scales differ, converts them row by row, and pairs neighbouring rows'
-//    values: instruction j then takes columns 8 r + j, r = lane mod 16, and a
-//    lane's outputs are 8 consecutive columns again.
+//    of one column.  It reads those of FN neighbouring columns (2 bytes for 4) of
+//    each of the rows, whose scales differ, converts them row by row, and pairs
+//    neighbouring rows' values: instruction j then takes columns FN r + j, r =
+//    lane mod 16, and a lane's outputs are consecutive columns again.
+//
+// One wave has all BM rows of its columns, so that no code is converted twice in a
+// workgroup; two workgroups of 4 waves a CU overlap one's conversions with the
+// other's products.  (A workgroup of 8 waves on 256 x 256, which converted twice
+// (forward) or four times (back): dx of 1024 rows, k and n 8192, NVFP4 392 us.)
 #pragma once
 
 #include "fp4q_ffn.h"
@@ -45,6 +50,7 @@ struct ManyTile {
   // codes: rows of 32 bytes; transposed, rows of BN / 2 with a pad each 8 rows
   // that spreads the 4 lane groups' reads over the banks
   static constexpr int kWPitch = kT ? BN / 2 : kStage / 2;
+  static constexpr int kColBytes = FN / 2;               // transposed: codes of a lane's columns in a row
   static constexpr int kWBytes = kT ? kStage * kWPitch + kStage / 8 * 64 : BN * kWPitch;
   // scales: by row; transposed, by block of columns, a byte for each row
   static constexpr int kSPitch = kT ? kStage + 8 : kStage / kBlock;
@@ -53,12 +59,12 @@ struct ManyTile {
   static constexpr int kXPer = BM * 8 / kThreads;                                // 8-element pieces a thread
   static constexpr int kWPer = (kT ? kStage * (BN / 32) : BN * 2) / kThreads;    // 16-byte pieces
   static_assert(kXPer * kThreads == BM * 8 && kWPer >= 1, "whole pieces");
-  static_assert(!kT || TN == 128, "a wave takes 8 columns a lane");
+  static_assert(!kT || FN == 2 || FN == 4, "a lane takes 2 or 4 neighbouring columns");
   static_assert(MODE != kGated || FN % 2 == 0, "both factors in a wave");
 };
 
 template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void many_kernel(ManyArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
   using T = ManyTile<FMT, XT, MODE, BM, BN, WM, WN>;
   constexpr int kElem = XT == kXF32 ? 4 : XT == kXBF16 ? 2 : 1;
   constexpr int P = T::P, FM = T::FM, FN = T::FN;
@@ -201,22 +207,26 @@ __global__ __launch_bounds__(64 * WM * WN) void many_kernel(ManyArgs a) {
     for (int t = 0; t < 2; ++t) {
       u32x4_t wf[FN];
       if constexpr (T::kT) {
-        const uint8_t* c0 = bw + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * 64 + 4 * r;
+        const uint8_t* c0 = bw + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * (T::TN / 2) + T::kColBytes * r;
         const u32x2_t sb = *reinterpret_cast<const u32x2_t*>(
-            bs + (wn * (128 / T::kBlock) + 8 * r / T::kBlock) * T::kSPitch + 32 * t + 8 * g);
+            bs + ((wn * T::TN + FN * r) / T::kBlock) * T::kSPitch + 32 * t + 8 * g);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {     // rows i and i + 1 of this lane's 8
-          const uint32_t ca = *reinterpret_cast<const uint32_t*>(c0 + i * T::kWPitch);
-          const uint32_t cb = *reinterpret_cast<const uint32_t*>(c0 + (i + 1) * T::kWPitch);
+          uint32_t ca, cb;
+          if constexpr (FN == 4) {
+            ca = *reinterpret_cast<const uint16_t*>(c0 + i * T::kWPitch);
+            cb = *reinterpret_cast<const uint16_t*>(c0 + (i + 1) * T::kWPitch);
+          } else {
+            ca = c0[i * T::kWPitch];
+            cb = c0[(i + 1) * T::kWPitch];
+          }
           const uint32_t sw = i < 4 ? sb.x : sb.y;
           const float sa = scale_operand<FMT>((sw >> (8 * (i & 3))) & 0xFFu);
           const float sc = scale_operand<FMT>((sw >> (8 * (i & 3) + 8)) & 0xFFu);
-          const u32x4_t va = weights8<FMT>(ca, sa), vb = weights8<FMT>(cb, sc);
+          uint32_t o[FN];
+          weight_pairs<FMT, FN>(ca, sa, cb, sc, o);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            wf[2 * j][i >> 1] = __builtin_amdgcn_perm(vb[j], va[j], 0x05040100u);
-            wf[2 * j + 1][i >> 1] = __builtin_amdgcn_perm(vb[j], va[j], 0x07060302u);
-          }
+          for (int j = 0; j < FN; ++j) wf[j][i >> 1] = o[j];
         }
       } else {
 #pragma unroll
@@ -286,20 +296,15 @@ __global__ __launch_bounds__(64 * WM * WN) void many_kernel(ManyArgs a) {
     const int64_t row = m0 + wm * T::TM + 16 * m + r;
     if (row >= l.rows) continue;
     if constexpr (T::kT) {
+      // columns FN (4 g + i) + j of the wave's: 4 FN consecutive ones a lane, by fours
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t k = o0 + wn * 128 + 8 * (4 * g + i);
+      for (int q = 0; q < FN; ++q) {
+        const int64_t k = o0 + wn * T::TN + FN * 4 * g + 4 * q;
         if (k >= K) continue;                           // (K is a multiple of 8)
-        const f32x4_t a0 = {acc[0][m][i], acc[1][m][i], acc[2][m][i], acc[3][m][i]};
-        const f32x4_t a1 = {acc[4][m][i], acc[5][m][i], acc[6][m][i], acc[7][m][i]};
-        if (a.splits > 1) {
-          float* o = l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + k;
-          store_any(o, a0);
-          store_any(o + 4, a1);
-        } else {
-          put4(l.out, row * K + k, a0 * tensor, 4, l.out_bf16);
-          put4(l.out, row * K + k + 4, a1 * tensor, 4, l.out_bf16);
-        }
+        const f32x4_t v = {acc[(4 * q) % FN][m][4 * q / FN], acc[(4 * q + 1) % FN][m][(4 * q + 1) / FN],
+                           acc[(4 * q + 2) % FN][m][(4 * q + 2) / FN], acc[(4 * q + 3) % FN][m][(4 * q + 3) / FN]};
+        if (a.splits > 1) store_any(l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + k, v);
+        else put4(l.out, row * K + k, v * tensor, 4, l.out_bf16);
       }
     } else {
 #pragma unroll
@@ -357,18 +362,17 @@ hipError_t launch_many_nv(const ManyArgs& a, int size, hipStream_t s);
 hipError_t launch_many_back_mx(const ManyArgs& a, int size, hipStream_t s);
 hipError_t launch_many_back_nv(const ManyArgs& a, int size, hipStream_t s);
 
-// Tiles: of 8 waves where there are enough of them, of 4 waves else.  fp32
-// activations take three times the LDS and half the rows.
+// Tiles: large ones where there are enough of them.  fp32 activations take three
+// times the LDS and half the rows.
 constexpr ManySize many_size(int x_type, int size) {
-  return size == 0 ? ManySize{64, 128} : x_type == kXF32 ? ManySize{128, 256} : ManySize{256, 256};
+  return size == 0 ? ManySize{64, 128} : x_type == kXF32 ? ManySize{64, 256} : ManySize{128, 256};
 }
 
 template <int FMT, int XT, int MODE>
 hipError_t launch_many_size(const ManyArgs& a, int size, hipStream_t s) {
-  constexpr bool t = MODE == kTransposed;
-  if (size == 0) return launch_many_t<FMT, XT, MODE, 64, 128, t ? 4 : 2, t ? 1 : 2>(a, s);
+  if (size == 0) return launch_many_t<FMT, XT, MODE, 64, 128, 1, 4>(a, s);
   constexpr int BM = many_size(XT, 1).bm;
-  return launch_many_t<FMT, XT, MODE, BM, 256, t ? 4 : 2, t ? 2 : 4>(a, s);
+  return launch_many_t<FMT, XT, MODE, BM, 256, 1, 4>(a, s);
 }
 
 }  // namespace fp4q
