@@ -30,7 +30,7 @@ from . import _lib
 from ._ffn import (Fp4Weight, Mx8Result, NormResult, fp4_gated, fp4_gated_backward, fp4_linear, fp4_linear_backward,
                    fp4_weight, rms_norm, rms_norm_backward)
 from ._lib import Fp4qError, load  # noqa: F401
-from ._kv import (KvCache, kv_cache, kv_cache_attention, kv_cache_attention_workspace_bytes, kv_cache_read,
+from ._kv import (KvCache, _raw_stream, kv_cache, kv_cache_attention, kv_cache_attention_workspace_bytes, kv_cache_read,
                   kv_cache_write)
 
 __all__ = [
@@ -56,7 +56,7 @@ def _ptr(t):
 
 
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _in_dtype(x):

@@ -73,18 +73,20 @@ def fp4_weight(quantized):
 
 
 def _rows(t, what, index, cols):
-    """Checks a [rows, cols] tensor of fp32 or bf16 with contiguous rows; its rows, row stride and dtype code."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+    """Checks a [rows, cols] tensor of fp32 or bf16 with contiguous rows on device `index`; its rows, row stride and
+    dtype code."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or index < 0:
         raise ValueError("fp4q: %s must be a GPU tensor on the other operands' device" % what)
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("fp4q: %s must be float32 or bfloat16, got %s" % (what, t.dtype))
-    if t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError("fp4q: %s must be [rows, %d], got %s" % (what, cols, tuple(t.shape)))
-    rows, (stride, inner) = t.shape[0], t.stride()
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError("fp4q: %s must be [rows, %d], got %s" % (what, cols, tuple(shape)))
+    stride, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError("fp4q: rows of %s must be contiguous (stride(1) == 1)" % what)
-    return rows, stride, code
+    return shape[0], stride, code
 
 
 def _out_dtype(dtype):
@@ -98,7 +100,7 @@ def _buffer(t, what, shape, dtype, device):
     """A dense buffer of this shape and dtype: t after checks, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or tuple(t.shape) != shape \
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device \
             or not t.is_contiguous():
         raise ValueError("fp4q: %s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, shape, device))
     return t
@@ -216,8 +218,7 @@ def fp4_gated_backward(dh, products, w):
 
 
 def _vector(t, what, d, index):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index or tuple(t.shape) != (d,) \
-            or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.shape != (d,) or not t.is_contiguous():
         raise ValueError("fp4q: %s must be a contiguous [%d] tensor on x's device" % (what, d))
     code = _DTYPES.get(t.dtype)
     if code is None:
@@ -238,30 +239,31 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, quantize=None, return_rstd=F
     itself, which updates a residual stream in place."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
         raise ValueError("fp4q: x must be a 2-D GPU tensor")
-    index, (rows, d) = x.get_device(), x.shape
-    _, stride, code = _rows(x, "x", index, d)
+    index, d, device = x.get_device(), x.shape[1], x.device
+    rows, stride, code = _rows(x, "x", index, d)
     w_code = _vector(weight, "weight", d, index)
     r_stride = 0
     if residual is not None:
         r_rows, r_stride, r_code = _rows(residual, "residual", index, d)
         if r_rows != rows or r_code != code:
             raise ValueError("fp4q: residual must have x's shape and dtype")
-        summed = _buffer(summed, "summed", (rows, d), x.dtype, x.device)
+        summed = torch.empty_like(x) if summed is None and x.is_contiguous() else \
+            _buffer(summed, "summed", (rows, d), x.dtype, device)
     elif summed is not None:
         raise ValueError("fp4q: without a residual there is no sum to write")
     if quantize is None:
-        out = _buffer(out, "out", (rows, d), x.dtype, x.device)
+        out = _buffer(out, "out", (rows, d), x.dtype, device)
         y, codes, scales = out.data_ptr(), None, None
     elif quantize == "mxfp8":
         if d % 32:
             raise ValueError("fp4q: MXFP8 rows are multiples of 32, got %d" % d)
         c, s = (None, None) if out is None else out
-        out = Mx8Result(_buffer(c, "out.codes", (rows, d), torch.uint8, x.device),
-                        _buffer(s, "out.scales", (rows, d // 32), torch.uint8, x.device))
+        out = Mx8Result(_buffer(c, "out.codes", (rows, d), torch.uint8, device),
+                        _buffer(s, "out.scales", (rows, d // 32), torch.uint8, device))
         y, codes, scales = None, out.codes.data_ptr(), out.scales.data_ptr()
     else:
         raise ValueError("fp4q: quantize is None or 'mxfp8', got %r" % (quantize,))
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if return_rstd else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=device) if return_rstd else None
     a = _lib.RmsNormArgs(x.data_ptr(), None if residual is None else residual.data_ptr(), stride, r_stride,
                          weight.data_ptr(), y, None if summed is None else summed.data_ptr(),
                          None if rstd is None else rstd.data_ptr(), codes, scales, rows, d, code, w_code, float(eps))
@@ -279,8 +281,8 @@ def rms_norm_backward(dy, s, weight, rstd, *, dsummed=None):
     weight's dtype."""
     if not isinstance(dy, torch.Tensor) or not dy.is_cuda or dy.dim() != 2:
         raise ValueError("fp4q: dy must be a 2-D GPU tensor")
-    index, (rows, d) = dy.get_device(), dy.shape
-    _, stride, code = _rows(dy, "dy", index, d)
+    index, d, device = dy.get_device(), dy.shape[1], dy.device
+    rows, stride, code = _rows(dy, "dy", index, d)
     strides = [stride, 0, 0]
     for i, (what, t) in enumerate((("s", s), ("dsummed", dsummed))):
         if t is None and i == 1:
@@ -289,14 +291,14 @@ def rms_norm_backward(dy, s, weight, rstd, *, dsummed=None):
         if t_rows != rows or t_code != code:
             raise ValueError("fp4q: %s must have dy's shape and dtype" % what)
     w_code = _vector(weight, "weight", d, index)
-    _buffer(rstd, "rstd", (rows,), torch.float32, dy.device)
-    dx = torch.empty((rows, d), dtype=dy.dtype, device=dy.device)
+    _buffer(rstd, "rstd", (rows,), torch.float32, device)
+    dx = torch.empty((rows, d), dtype=dy.dtype, device=device)
     dw = torch.empty_like(weight)
     a = _lib.RmsNormGradArgs(dy.data_ptr(), s.data_ptr(), None if dsummed is None else dsummed.data_ptr(), *strides,
                              weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), rows, d, code, w_code)
     lib = _lib.load()
     need = _call(index, lib.fp4q_rms_norm_backward_workspace_bytes, a)
-    ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     status = _call(index, lib.fp4q_rms_norm_backward, a, ws.data_ptr() if need else None, need, _raw_stream(index))
     if status:
         _lib.check(status, "fp4q_rms_norm_backward")
