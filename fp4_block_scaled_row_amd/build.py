@@ -22,7 +22,7 @@ ARCH = "gfx950"
 
 SOURCES = ["fp4q_api.hip", "fp4q_mx.hip", "fp4q_nv.hip", "fp4q_nv_resident.hip", "fp4q_fwht.hip", "fp4q_gemm.hip",
            "fp4q_dequant.hip", "fp4q_ffn_api.hip", "fp4q_linear.hip", "fp4q_linear_few.hip", "fp4q_linear_many_mx.hip",
-           "fp4q_linear_many_nv.hip", "fp4q_linear_many_back_mx.hip", "fp4q_linear_many_back_nv.hip", "fp4q_norm.hip",
+           "fp4q_linear_many_nv.hip", "fp4q_linear_many_back_mx.hip", "fp4q_linear_many_back_nv.hip", "fp4q_linear_mx8.hip", "fp4q_norm.hip",
            "fp4q_kv_api.hip", "fp4q_kv_cache.hip",
            *["fp4q_kv_%s_%s%d.hip" % (kind, fmt, dim)
              for dim in (256, 128, 96, 64) for kind in ("decode", "prefill") for fmt in ("mx", "nv")]]

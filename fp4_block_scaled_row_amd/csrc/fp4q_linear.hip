@@ -9,14 +9,14 @@ namespace fp4q {
 namespace {
 
 struct Plan {
-  bool few;
+  bool few, mx8;
   int size, splits;
 };
 
 ManyArgs many_args(const LinearLaunch& l, int size) {
   ManyArgs a;
   a.l = l;
-  const ManySize t = many_size(l.x_type, size);
+  const ManySize t = size < 0 ? ManySize{256, 256} : many_size(l.x_type, size);
   const int64_t out = l.transposed ? l.w.k : l.gated ? l.w.n / 2 : l.w.n;
   const int64_t bn = l.gated ? t.bn / 2 : t.bn;
   const int64_t tm = (l.rows + t.bm - 1) / t.bm, tn = (out + bn - 1) / bn;
@@ -30,9 +30,18 @@ ManyArgs many_args(const LinearLaunch& l, int size) {
 }
 
 Plan plan(const LinearLaunch& l) {
-  Plan p = {!l.transposed && l.rows <= (l.x_type == kXF32 ? 16 : 64), 1, 1};
+  Plan p = {!l.transposed && l.rows <= (l.x_type == kXF32 ? 16 : 64), false, 1, 1};
   if (p.few) return p;
   const int cus = device_cu_count();
+  // Block-scaled products from a quarter as many tiles as CUs on (its offsets within
+  // 256 rows are 31-bit).  Measured, MXFP4, us, there / converted to bf16:
+  //   k, n        rows 256       512          1024         2048
+  //   8192, 8192  88 /  69    90 / 106     92 / 163    114 / 253
+  //   4096, 4096  45 /  34    45 /  43     51 /  58     53 /  87
+  //   8192, 1024  79 /  29    79 /  33     90 /  43     91 /  69
+  p.mx8 = l.x_type == kXE4M3 && l.w.format == 0 && l.w.k > 0 && l.w.k % 128 == 0 && l.w.k <= 1 << 22 &&
+          many_args(l, -1).ntiles >= cus / 4;
+  if (p.mx8) return p;
   const ManyArgs large = many_args(l, 1);
   if (large.ntiles >= cus) return p;
   p.size = 0;
@@ -170,13 +179,14 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradLaunch l) {
 
 size_t linear_workspace(const LinearLaunch& l) {
   const Plan p = plan(l);
-  if (p.few || p.splits <= 1) return 0;
+  if (p.splits <= 1) return 0;
   return (size_t)p.splits * l.rows * (l.transposed ? l.w.k : l.w.n) * sizeof(float);
 }
 
 hipError_t launch_linear(const LinearLaunch& l, hipStream_t s) {
   const Plan p = plan(l);
   if (p.few) return launch_linear_few(l, s);
+  if (p.mx8) return launch_mx8(many_args(l, -1), s);
   ManyArgs a = many_args(l, p.size);
   a.splits = p.splits;
   a.per_split = (a.stages + p.splits - 1) / p.splits;

@@ -361,6 +361,7 @@ hipError_t launch_many_mx(const ManyArgs& a, int size, hipStream_t s);
 hipError_t launch_many_nv(const ManyArgs& a, int size, hipStream_t s);
 hipError_t launch_many_back_mx(const ManyArgs& a, int size, hipStream_t s);
 hipError_t launch_many_back_nv(const ManyArgs& a, int size, hipStream_t s);
+hipError_t launch_mx8(const ManyArgs& a, hipStream_t s);   // tiles of 256 x 256
 
 // Tiles: large ones where there are enough of them.  fp32 activations take three
 // times the LDS and half the rows.
