@@ -41,7 +41,7 @@ struct ManyArgs {
 
 template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
 struct ManyTile {
-  static constexpr int kThreads = 64 * WM * WN;
+  static constexpr int kThreads = 64 * WM * WN, kWavesM = WM;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   static constexpr int P = kPieces<XT>;
   static constexpr int kBlock = FMT == 0 ? 32 : 16;
@@ -62,6 +62,147 @@ struct ManyTile {
   static_assert(!kT || FN == 2 || FN == 4, "a lane takes 2 or 4 neighbouring columns");
   static_assert(MODE != kGated || FN % 2 == 0, "both factors in a wave");
 };
+
+// Where in LDS the 16-byte chunk `chunk` of a row's 8 lies, by the row: 16 rows'
+// reads of one chunk meet all banks.
+__device__ __forceinline__ int x_chunk(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
+// acc += a stage's products, from its buffer in LDS.
+template <class T, int FMT>
+__device__ __forceinline__ void many_multiply(const uint8_t* buf, f32x4_t (&acc)[T::FN][T::FM], int wm, int wn, int r,
+                                              int g) {
+  constexpr int P = T::P, FM = T::FM, FN = T::FN, BM = T::TM * T::kWavesM;
+  const uint8_t* bw = buf + T::kXBytes;
+  const uint8_t* bs = bw + T::kWBytes;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    u32x4_t wf[FN];
+    if constexpr (T::kT) {
+      const uint8_t* c0 = bw + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * (T::TN / 2) + T::kColBytes * r;
+      const u32x2_t sb = *reinterpret_cast<const u32x2_t*>(
+          bs + ((wn * T::TN + FN * r) / T::kBlock) * T::kSPitch + 32 * t + 8 * g);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {     // rows i and i + 1 of this lane's 8
+        uint32_t ca, cb;
+        if constexpr (FN == 4) {
+          ca = *reinterpret_cast<const uint16_t*>(c0 + i * T::kWPitch);
+          cb = *reinterpret_cast<const uint16_t*>(c0 + (i + 1) * T::kWPitch);
+        } else {
+          ca = c0[i * T::kWPitch];
+          cb = c0[(i + 1) * T::kWPitch];
+        }
+        const uint32_t sw = i < 4 ? sb.x : sb.y;
+        const float sa = scale_operand<FMT>((sw >> (8 * (i & 3))) & 0xFFu);
+        const float sc = scale_operand<FMT>((sw >> (8 * (i & 3) + 8)) & 0xFFu);
+        uint32_t o[FN];
+        weight_pairs<FMT, FN>(ca, sa, cb, sc, o);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) wf[j][i >> 1] = o[j];
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        const int row = wn * T::TN + 16 * n + r;
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(bw + row * T::kWPitch + 8 * g + 4 * t);
+        const uint32_t s = bs[row * T::kSPitch + (FMT == 0 ? g >> 1 : g)];
+        wf[n] = weights8<FMT>(c, scale_operand<FMT>(s));
+      }
+    }
+    // this lane's 8 of the contraction: chunk 4 t + g where groups take runs of
+    // 8 (transposed), 2 g + t where they take runs of 16
+    const int chunk = T::kT ? 4 * t + g : 2 * g + t;
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      const int row = wm * T::TM + 16 * m + r;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const u32x4_t xf = *reinterpret_cast<const u32x4_t*>(buf + (p * BM + row) * 128 + x_chunk(row, chunk) * 16);
+#pragma unroll
+        for (int n = 0; n < FN; ++n) acc[n][m] = mfma16(wf[n], xf, acc[n][m]);
+      }
+    }
+  }
+}
+
+// The sums to where they belong: outputs, or parts of sums.
+template <class T, int FMT, int MODE>
+__device__ __forceinline__ void many_results(const ManyArgs& a, const f32x4_t (&acc)[T::FN][T::FM], int64_t m0, int64_t o0,
+                                             int wm, int wn, int r, int g) {
+  constexpr int FM = T::FM, FN = T::FN;
+  const LinearLaunch& l = a.l;
+  const int64_t K = l.w.k, half = l.w.n / 2;
+  const int64_t cols = T::kT ? K : l.w.n;               // of the sums
+  // 4 consecutive outputs, or the first `count`
+  auto put4 = [&](void* to, int64_t at, f32x4_t v, int count, int bf16) {
+    if (bf16) {
+      __bf16* o = static_cast<__bf16*>(to) + at;
+      if (count >= 4) {
+        store_any(o, u32x2_t{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
+      } else {
+        for (int i = 0; i < count; ++i) o[i] = (__bf16)v[i];
+      }
+    } else {
+      float* o = static_cast<float*>(to) + at;
+      if (count >= 4) {
+        store_any(o, v);
+      } else {
+        for (int i = 0; i < count; ++i) o[i] = v[i];
+      }
+    }
+  };
+  const float tensor = FMT == 1 ? *l.w.g : 1.0f;
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const int64_t row = m0 + wm * T::TM + 16 * m + r;
+    if (row >= l.rows) continue;
+    if constexpr (T::kT) {
+      // columns FN (4 g + i) + j of the wave's: 4 FN consecutive ones a lane, by fours
+#pragma unroll
+      for (int q = 0; q < FN; ++q) {
+        const int64_t k = o0 + wn * T::TN + FN * 4 * g + 4 * q;
+        if (k >= K) continue;                           // (K is a multiple of 8)
+        const f32x4_t v = {acc[(4 * q) % FN][m][4 * q / FN], acc[(4 * q + 1) % FN][m][(4 * q + 1) / FN],
+                           acc[(4 * q + 2) % FN][m][(4 * q + 2) / FN], acc[(4 * q + 3) % FN][m][(4 * q + 3) / FN]};
+        if (a.splits > 1) store_any(l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + k, v);
+        else put4(l.out, row * K + k, v * tensor, 4, l.out_bf16);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < (MODE == kGated ? FN / 2 : FN); ++n) {
+        const int64_t side = MODE == kGated ? half : l.w.n;
+        const int64_t col = o0 + wn * (MODE == kGated ? T::TN / 2 : T::TN) + 16 * n + 4 * g;
+        const int count = (int)min(side - col, (int64_t)4);
+        if (count <= 0) continue;
+        f32x4_t v = acc[n][m], u = acc[MODE == kGated ? n + FN / 2 : n][m];
+        if (a.splits > 1) {
+          float* o = l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + col;
+          for (int i = 0; i < count; ++i) o[i] = v[i];
+          if constexpr (MODE == kGated)
+            for (int i = 0; i < count; ++i) o[half + i] = u[i];
+          continue;
+        }
+        v *= tensor;
+        if constexpr (MODE == kGated) {
+          u *= tensor;
+          if (l.products) {
+            put4(l.products, row * l.w.n + col, v, count, l.products_bf16);
+            put4(l.products, row * l.w.n + half + col, u, count, l.products_bf16);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
+          put4(l.out, row * half + col, v, count, l.out_bf16);
+        } else {
+          if (l.bias) {
+            for (int i = 0; i < count; ++i)
+              v[i] += l.out_bf16 ? (float)static_cast<const __bf16*>(l.bias)[col + i]
+                                 : static_cast<const float*>(l.bias)[col + i];
+          }
+          put4(l.out, row * l.w.n + col, v, count, l.out_bf16);
+        }
+      }
+    }
+  }
+}
 
 template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
@@ -166,7 +307,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
     uint8_t* bs = bw + T::kWBytes;
 #pragma unroll
     for (int i = 0; i < T::kXPer; ++i) {
-      const int q = tid + i * T::kThreads, row = q >> 3, ch = (q & 7) ^ (row & 7);
+      const int q = tid + i * T::kThreads, row = q >> 3, ch = x_chunk(row, q & 7);
       u32x4_t o[P];
       if constexpr (XT == kXF32) split8(xr[i], o);
       else if constexpr (XT == kXBF16) o[0] = u32x4_t{xr[i][0], xr[i][1], xr[i][2], xr[i][3]};
@@ -200,59 +341,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
 #pragma unroll
     for (int m = 0; m < FM; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto multiply = [&](const uint8_t* buf) {
-    const uint8_t* bw = buf + T::kXBytes;
-    const uint8_t* bs = bw + T::kWBytes;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      u32x4_t wf[FN];
-      if constexpr (T::kT) {
-        const uint8_t* c0 = bw + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * (T::TN / 2) + T::kColBytes * r;
-        const u32x2_t sb = *reinterpret_cast<const u32x2_t*>(
-            bs + ((wn * T::TN + FN * r) / T::kBlock) * T::kSPitch + 32 * t + 8 * g);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {     // rows i and i + 1 of this lane's 8
-          uint32_t ca, cb;
-          if constexpr (FN == 4) {
-            ca = *reinterpret_cast<const uint16_t*>(c0 + i * T::kWPitch);
-            cb = *reinterpret_cast<const uint16_t*>(c0 + (i + 1) * T::kWPitch);
-          } else {
-            ca = c0[i * T::kWPitch];
-            cb = c0[(i + 1) * T::kWPitch];
-          }
-          const uint32_t sw = i < 4 ? sb.x : sb.y;
-          const float sa = scale_operand<FMT>((sw >> (8 * (i & 3))) & 0xFFu);
-          const float sc = scale_operand<FMT>((sw >> (8 * (i & 3) + 8)) & 0xFFu);
-          uint32_t o[FN];
-          weight_pairs<FMT, FN>(ca, sa, cb, sc, o);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) wf[j][i >> 1] = o[j];
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < FN; ++n) {
-          const int row = wn * T::TN + 16 * n + r;
-          const uint32_t c = *reinterpret_cast<const uint32_t*>(bw + row * T::kWPitch + 8 * g + 4 * t);
-          const uint32_t s = bs[row * T::kSPitch + (FMT == 0 ? g >> 1 : g)];
-          wf[n] = weights8<FMT>(c, scale_operand<FMT>(s));
-        }
-      }
-      // this lane's 8 of the contraction: chunk 4 t + g where groups take runs of
-      // 8 (transposed), 2 g + t where they take runs of 16
-      const int chunk = T::kT ? 4 * t + g : 2 * g + t;
-#pragma unroll
-      for (int m = 0; m < FM; ++m) {
-        const int row = wm * T::TM + 16 * m + r;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const u32x4_t xf = *reinterpret_cast<const u32x4_t*>(buf + (p * BM + row) * 128 + ((chunk ^ (row & 7)) * 16));
-#pragma unroll
-          for (int n = 0; n < FN; ++n) acc[n][m] = mfma16(wf[n], xf, acc[n][m]);
-        }
-      }
-    }
-  };
-
   if (s0 < s1) {
     load_x((int64_t)s0 * kStage);
     load_w((int64_t)s0 * kStage);
@@ -264,84 +352,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
         load_x((int64_t)(s + 1) * kStage);
         load_w((int64_t)(s + 1) * kStage);
       }
-      multiply(s_buf[b]);
+      many_multiply<T, FMT>(s_buf[b], acc, wm, wn, r, g);
       if (s + 1 < s1) commit(s_buf[b ^ 1]);
       __syncthreads();
     }
   }
 
-  // ---- results
-  const int64_t cols = T::kT ? K : l.w.n;               // of the sums
-  // 4 consecutive outputs, or the first `count`
-  auto put4 = [&](void* to, int64_t at, f32x4_t v, int count, int bf16) {
-    if (bf16) {
-      __bf16* o = static_cast<__bf16*>(to) + at;
-      if (count >= 4) {
-        store_any(o, u32x2_t{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
-      } else {
-        for (int i = 0; i < count; ++i) o[i] = (__bf16)v[i];
-      }
-    } else {
-      float* o = static_cast<float*>(to) + at;
-      if (count >= 4) {
-        store_any(o, v);
-      } else {
-        for (int i = 0; i < count; ++i) o[i] = v[i];
-      }
-    }
-  };
-  const float tensor = FMT == 1 ? *l.w.g : 1.0f;
-#pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    const int64_t row = m0 + wm * T::TM + 16 * m + r;
-    if (row >= l.rows) continue;
-    if constexpr (T::kT) {
-      // columns FN (4 g + i) + j of the wave's: 4 FN consecutive ones a lane, by fours
-#pragma unroll
-      for (int q = 0; q < FN; ++q) {
-        const int64_t k = o0 + wn * T::TN + FN * 4 * g + 4 * q;
-        if (k >= K) continue;                           // (K is a multiple of 8)
-        const f32x4_t v = {acc[(4 * q) % FN][m][4 * q / FN], acc[(4 * q + 1) % FN][m][(4 * q + 1) / FN],
-                           acc[(4 * q + 2) % FN][m][(4 * q + 2) / FN], acc[(4 * q + 3) % FN][m][(4 * q + 3) / FN]};
-        if (a.splits > 1) store_any(l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + k, v);
-        else put4(l.out, row * K + k, v * tensor, 4, l.out_bf16);
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < (MODE == kGated ? FN / 2 : FN); ++n) {
-        const int64_t side = MODE == kGated ? half : l.w.n;
-        const int64_t col = o0 + wn * (MODE == kGated ? T::TN / 2 : T::TN) + 16 * n + 4 * g;
-        const int count = (int)min(side - col, (int64_t)4);
-        if (count <= 0) continue;
-        f32x4_t v = acc[n][m], u = acc[MODE == kGated ? n + FN / 2 : n][m];
-        if (a.splits > 1) {
-          float* o = l.partials + ((int64_t)blockIdx.y * l.rows + row) * cols + col;
-          for (int i = 0; i < count; ++i) o[i] = v[i];
-          if constexpr (MODE == kGated)
-            for (int i = 0; i < count; ++i) o[half + i] = u[i];
-          continue;
-        }
-        v *= tensor;
-        if constexpr (MODE == kGated) {
-          u *= tensor;
-          if (l.products) {
-            put4(l.products, row * l.w.n + col, v, count, l.products_bf16);
-            put4(l.products, row * l.w.n + half + col, u, count, l.products_bf16);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
-          put4(l.out, row * half + col, v, count, l.out_bf16);
-        } else {
-          if (l.bias) {
-            for (int i = 0; i < count; ++i)
-              v[i] += l.out_bf16 ? (float)static_cast<const __bf16*>(l.bias)[col + i]
-                                 : static_cast<const float*>(l.bias)[col + i];
-          }
-          put4(l.out, row * l.w.n + col, v, count, l.out_bf16);
-        }
-      }
-    }
-  }
+  many_results<T, FMT, MODE>(a, acc, m0, o0, wm, wn, r, g);
 }
 
 template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   __shared__ __align__(16) uint8_t s_b1[kBuf8];
   __shared__ __align__(16) uint8_t s_b2[kBuf8];
   const LinearLaunch& l = a.l;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // (one a wave: descriptors go by it)
   const int wx = wave >> 1, ww = wave & 1;          // this wave's quarter of x's rows, half of the weight's
 
   const int w = blockIdx.x, per = (a.ntiles + 7) / 8;
@@ -128,30 +128,30 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   // (16 bits a read: pairs of reads made into one lose what tells the compiler which
   // loads into LDS they have to wait for, and wait for all)
   auto read_scales = [&](const uint8_t* buf) {
-    const uint8_t* p = buf + kCodes8 + (lane & 31) * 4 + (lane >> 5) * 2;
+    const int p = kCodes8 + (lane & 31) * 4 + (lane >> 5) * 2;
 #pragma unroll
-    for (int u = 0; u < kSubX; ++u) xe[u] = *reinterpret_cast<const uint16_t*>(p + (64 * wx + 32 * u) * 4);
+    for (int u = 0; u < kSubX; ++u) xe[u] = *reinterpret_cast<const uint16_t*>(buf + (p + (64 * wx + 32 * u) * 4));
 #pragma unroll
-    for (int u = 0; u < kSubW; ++u) we[u] = *reinterpret_cast<const uint16_t*>(p + (kTile8 + 128 * ww + 32 * u) * 4);
+    for (int u = 0; u < kSubW; ++u) we[u] = *reinterpret_cast<const uint16_t*>(buf + (p + (kTile8 + 128 * ww + 32 * u) * 4));
   };
-  // (the lane's part of the addresses is made anew each time: kept, those of three
-  // buffers would take more registers than there are)
+  // The lane's offsets are hidden from the compiler: it would keep those of three
+  // buffers in more registers than there are, and it tells which loads into LDS a
+  // read has to wait for only where the read's address is a step or two from the
+  // buffer's (else it waits for all, which took 110 us for 106).
   auto read = [&](const uint8_t* buf, int kk) {
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    const int part = 2 * kk + (ln >> 5);            // this lane's 32 of the stage's k
-    const uint8_t* xp = buf + (64 * wx + (ln & 31)) * kK8;
-    const uint8_t* wp = buf + kXBytes8 + (128 * ww + (ln & 31)) * (kK8 / 2) + (part ^ ((ln >> 2) & 3)) * 16;
-    const int c0 = ((2 * part) ^ ((ln >> 1) & 7)) * 16, c1 = c0 ^ 16;
+    const int part = 2 * kk + (lane >> 5);          // this lane's 32 of the stage's k
+    int x0 = (64 * wx + (lane & 31)) * kK8 + ((2 * part) ^ ((lane >> 1) & 7)) * 16, x1 = x0 ^ 16;
+    int w0 = kXBytes8 + (128 * ww + (lane & 31)) * (kK8 / 2) + (part ^ ((lane >> 2) & 3)) * 16;
+    asm volatile("" : "+v"(x0), "+v"(x1), "+v"(w0));
 #pragma unroll
     for (int u = 0; u < kSubX; ++u) {
-      const uint4 v0 = *reinterpret_cast<const uint4*>(xp + 32 * u * kK8 + c0);
-      const uint4 v1 = *reinterpret_cast<const uint4*>(xp + 32 * u * kK8 + c1);
+      const u32x4_t v0 = *reinterpret_cast<const u32x4_t*>(buf + (x0 + 32 * u * kK8));
+      const u32x4_t v1 = *reinterpret_cast<const u32x4_t*>(buf + (x1 + 32 * u * kK8));
       xv[u] = v8i_t{(int)v0.x, (int)v0.y, (int)v0.z, (int)v0.w, (int)v1.x, (int)v1.y, (int)v1.z, (int)v1.w};
     }
 #pragma unroll
     for (int u = 0; u < kSubW; ++u) {
-      const uint4 c = *reinterpret_cast<const uint4*>(wp + 32 * u * (kK8 / 2));
+      const u32x4_t c = *reinterpret_cast<const u32x4_t*>(buf + (w0 + 32 * u * (kK8 / 2)));
       wv[u] = v8i_t{(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
     }
   };
