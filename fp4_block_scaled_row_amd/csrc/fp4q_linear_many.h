@@ -24,6 +24,8 @@
 // (forward) or four times (back): dx of 1024 rows, k and n 8192, NVFP4 392 us.)
 #pragma once
 
+#include <type_traits>
+
 #include "fp4q_ffn.h"
 
 namespace fp4q {
@@ -68,14 +70,16 @@ struct ManyTile {
 __device__ __forceinline__ int x_chunk(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
 // acc += a stage's products, from its buffer in LDS.
+// (half: of its first or second 32 of the contraction alone, or both, -1.)
 template <class T, int FMT>
 __device__ __forceinline__ void many_multiply(const uint8_t* buf, f32x4_t (&acc)[T::FN][T::FM], int wm, int wn, int r,
-                                              int g) {
+                                              int g, int half = -1) {
   constexpr int P = T::P, FM = T::FM, FN = T::FN, BM = T::TM * T::kWavesM;
   const uint8_t* bw = buf + T::kXBytes;
   const uint8_t* bs = bw + T::kWBytes;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int i = 0; i < (half < 0 ? 2 : 1); ++i) {
+    const int t = half < 0 ? i : half;
     u32x4_t wf[FN];
     if constexpr (T::kT) {
       const uint8_t* c0 = bw + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * (T::TN / 2) + T::kColBytes * r;
@@ -361,6 +365,186 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
   many_results<T, FMT, MODE>(a, acc, m0, o0, wm, wn, r, g);
 }
 
+// ----------------------------------------------------------------------------
+// The same tile for bf16 rows that are whole 16-byte pieces and stages.  x and
+// codes go straight into LDS, into a ring of three buffers, two stages ahead.
+// Eight waves: four side by side as above, and those twice, each four with one half
+// of a stage's contraction, so that every SIMD has two waves on one tile and still
+// no code is converted twice.  At the end the two fours exchange halves of their
+// rows' sums.  (Two workgroups of four waves a CU need twice the tiles: dx of 1024
+// rows, k and n 8192, took 207 us, or 151 in two parts with a join.)
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0,
+                                           (int)(bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF), 0x00020000);
+}
+// Until at most N loads are on their way, and every LDS access is done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+template <int FMT, int MODE>
+__global__ __launch_bounds__(512) void ring_kernel(ManyArgs a) {
+  constexpr int BM = 128, BN = 256;
+  using T = ManyTile<FMT, kXBF16, MODE, BM, BN, 1, 4>;
+  using H = ManyTile<FMT, kXBF16, MODE, BM / 2, BN, 1, 4>;     // what a wave stores
+  // separate objects, so that reads of one are not ordered after loads into others
+  __shared__ __align__(16) uint8_t s_b0[T::kBuf];
+  __shared__ __align__(16) uint8_t s_b1[T::kBuf];
+  __shared__ __align__(16) uint8_t s_b2[T::kBuf];
+  const LinearLaunch& l = a.l;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4, wn = wave & 3, part = wave >> 2;
+
+  const int w = blockIdx.x, per = (a.ntiles + 7) / 8;
+  const int tile = (w % 8) * per + w / 8;
+  if (tile >= a.ntiles || w / 8 >= per) return;
+  const int group = tile / (4 * a.tiles_n), first = group * 4;
+  const int gsize = min(a.tiles_m - first, 4), in_g = tile - group * 4 * a.tiles_n;
+  const int64_t m0 = (int64_t)(first + in_g % gsize) * BM;
+  const int64_t half = l.w.n / 2;
+  const int64_t o0 = (int64_t)(in_g / gsize) * (MODE == kGated ? BN / 2 : BN);
+  const int64_t K = l.w.k, kb = K / 2, srow = K / T::kBlock;
+  const int s0 = blockIdx.y * a.per_split, s1 = min(a.stages, s0 + a.per_split);
+
+  f32x4_t acc[T::FN][T::FM];
+#pragma unroll
+  for (int n = 0; n < T::FN; ++n)
+#pragma unroll
+    for (int m = 0; m < T::FM; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // Offsets within a tile are below 2^31 (rows of at most 2^22 elements); rows past
+  // the ends read the last one, columns past the end what lies there (zeros past
+  // the plane's), and their results are not stored.
+  const uint8_t* x = static_cast<const uint8_t*>(l.x) + m0 * l.x_stride * 2;
+  int x_off[2], w_off;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {                     // 8 rows of x a load, 128 bytes each
+    const int row = (wave * 2 + i) * 8 + (lane >> 3);
+    x_off[i] = (int)((min(m0 + row, l.rows - 1) - m0) * l.x_stride * 2) + x_chunk(row, lane & 7) * 16;
+  }
+  // row of the weight that local row i is (of the forward directions), from its side's first
+  auto w_row = [&](int i) {
+    if constexpr (MODE == kGated) return min(o0 + (i >> 6) * 32 + (i & 31), half - 1) - o0;
+    else return min(o0 + i, l.w.n - 1) - o0;
+  };
+  auto w_side = [&](int i) { return MODE == kGated && (i & 32) ? o0 + half : o0; };
+  // 32 rows' 32 bytes a load, or 8 rows' 128
+  if constexpr (T::kT) w_off = (int)((wave * 8 + (lane >> 3)) * kb) + (lane & 7) * 16;
+  else w_off = (int)(w_row(wave * 32 + (lane >> 1)) * kb) + (lane & 1) * 16;
+  auto issue = [&](int st, uint8_t* buf) {
+    const __amdgpu_buffer_rsrc_t xb = buffer_of(x + (int64_t)st * (kStage * 2), 0x7FFFFFFF);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void_t*)(buf + (wave * 2 + i) * 1024), 16, x_off[i], 0, 0, 0);
+    const int64_t at = T::kT ? (int64_t)st * kStage * kb + o0 / 2 : w_side(wave * 32) * kb + (int64_t)st * (kStage / 2);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(l.w.codes + at, l.w.n * kb - at),
+                                             (lds_void_t*)(buf + T::kXBytes + wave * (T::kT ? 1024 + 64 : 1024)), 16,
+                                             w_off, 0, 0, 0);
+  };
+  // Scales go through a register: a row's two halves in two threads; transposed, an
+  // eighth of a row's blocks in each of eight, to the places of their blocks.
+  constexpr int kHave = T::kT ? BN / T::kBlock / 8 : kStage / T::kBlock / 2;    // 1 or 2 bytes
+  using scale_t = typename std::conditional<kHave == 1, uint8_t, uint16_t>::type;
+  int s_off;                                        // from the tile's first scale (transposed: the stage's)
+  bool s_in = true;
+  if constexpr (T::kT) {
+    const int col = (tid & 7) * kHave;
+    s_in = o0 / T::kBlock + col < srow;             // (K is a multiple of 64: both are there or not)
+    s_off = (tid >> 3) * (int)srow + col;
+  } else {
+    s_off = (int)((w_side(tid >> 1) - o0 + w_row(tid >> 1)) * srow) + (tid & 1) * kHave;
+  }
+  uint32_t s_next;
+  auto load_scales = [&](int st) {
+    const uint8_t* p = l.w.scales + (T::kT ? (int64_t)st * kStage * srow + o0 / T::kBlock
+                                           : o0 * srow + (int64_t)st * (kStage / T::kBlock));
+    s_next = 0u;
+    if (s_in) s_next = load_any<scale_t>(p + s_off);
+  };
+  auto store_scales = [&](uint8_t* buf) {
+    uint8_t* bs = buf + T::kXBytes + T::kWBytes;
+    if constexpr (T::kT) {
+#pragma unroll
+      for (int i = 0; i < kHave; ++i) bs[((tid & 7) * kHave + i) * T::kSPitch + (tid >> 3)] = (uint8_t)(s_next >> (8 * i));
+    } else {
+      *reinterpret_cast<scale_t*>(bs + tid * kHave) = (scale_t)s_next;
+    }
+  };
+  // As the block-scaled kernel's step: wait until only the next stage's loads are on
+  // their way, meet, ask for the stage after the next, which goes where the one
+  // before lay, and multiply.  Scales are written there before: beside a stage that
+  // is on its way the write would wait for it.  No branch, so that the compiler's
+  // counts stay exact.
+  auto step = [&](int st, const uint8_t* cur, uint8_t* fill) {
+    wait_loads<4>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    store_scales(fill);
+    load_scales(min(st + 3, s1 - 1));
+    issue(min(st + 2, s1 - 1), fill);
+    __builtin_amdgcn_sched_barrier(0);
+    // (the lane's part of the addresses is made anew each time: kept for three
+    // buffers, it would take more registers than there are)
+    int rr = r, gg = g;
+    asm volatile("" : "+v"(rr), "+v"(gg));
+    many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, part);
+  };
+  if (s0 < s1) {
+    load_scales(s0);
+    store_scales(s_b0);
+    load_scales(min(s0 + 1, s1 - 1));
+    store_scales(s_b1);
+    issue(s0, s_b0);
+    load_scales(min(s0 + 2, s1 - 1));
+    issue(min(s0 + 1, s1 - 1), s_b1);
+    int st = s0;
+    for (; st + 3 <= s1; st += 3) {
+      step(st, s_b0, s_b2);
+      step(st + 1, s_b1, s_b0);
+      step(st + 2, s_b2, s_b1);
+    }
+    if (st < s1) step(st, s_b0, s_b2);
+    if (st + 1 < s1) step(st + 1, s_b1, s_b0);
+  }
+
+  // The first four waves take rows 0 to 63, the others 64 to 127: each gives the
+  // other its sums of them, 8 KiB at a time.
+  f32x4_t mine[H::FN][H::FM];
+  auto region = [&](int i) {
+    uint8_t* buf = i < 3 ? s_b0 : i < 6 ? s_b1 : s_b2;
+    return reinterpret_cast<f32x4_t*>(buf + i % 3 * 8192) + lane;
+  };
+  wait_loads<0>();                                  // (the last stage asked for again is on its way to them)
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < T::FN; ++n)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        region(wave)[(n * 2 + m) * 64] = part ? acc[n][2 * q + m] : acc[n][4 + 2 * q + m];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < T::FN; ++n)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        mine[n][2 * q + m] = (part ? acc[n][4 + 2 * q + m] : acc[n][2 * q + m]) + region(wave ^ 4)[(n * 2 + m) * 64];
+  }
+  many_results<H, FMT, MODE>(a, mine, m0 + 64 * part, o0, 0, wn, r, g);
+}
+
+// Whether the rows are whole pieces and stages, and offsets small enough.
+inline bool ring_fits(const LinearLaunch& l) {
+  const int64_t most = (int64_t)1 << 22;
+  return l.x_type == kXBF16 && l.w.k % kStage == 0 && (l.transposed ? l.w.n : l.w.k) % kStage == 0 && l.w.k <= most &&
+         l.x_stride % 8 == 0 && l.x_stride <= most && (!l.gated || l.w.n / 2 * (l.w.k / 16) < (int64_t)1 << 31) && reinterpret_cast<uintptr_t>(l.x) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(l.w.codes) % 16 == 0;
+}
+
 template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
 hipError_t launch_many_t(const ManyArgs& a, hipStream_t s) {
   using T = ManyTile<FMT, XT, MODE, BM, BN, WM, WN>;
@@ -390,6 +574,12 @@ template <int FMT, int XT, int MODE>
 hipError_t launch_many_size(const ManyArgs& a, int size, hipStream_t s) {
   if (size == 0) return launch_many_t<FMT, XT, MODE, 64, 128, 1, 4>(a, s);
   constexpr int BM = many_size(XT, 1).bm;
+  if constexpr (XT == kXBF16) {
+    if (ring_fits(a.l)) {
+      hipLaunchKernelGGL((ring_kernel<FMT, MODE>), dim3((a.ntiles + 7) / 8 * 8, a.splits), dim3(512), 0, s, a);
+      return hipGetLastError();
+    }
+  }
   return launch_many_t<FMT, XT, MODE, BM, 256, 1, 4>(a, s);
 }
 

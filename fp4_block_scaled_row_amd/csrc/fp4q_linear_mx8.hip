@@ -36,19 +36,6 @@ constexpr int kGroup8 = 3;                          // stages that a load of sca
 
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x3_t __attribute__((ext_vector_type(3)));
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0,
-                                           (int)(bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF), 0x00020000);
-}
-
-// Until at most N loads are on their way, and every LDS access is done.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));     // (and no LDS access)
-}
-
 template <bool GATED>
 __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   // separate objects, so that reads of one are not ordered after loads into others
@@ -83,7 +70,7 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
       const int region = wave * kXLoads8 + i, row = region * 8 + (lane >> 3);
       const int chunk = (lane & 7) ^ ((row >> 1) & 7);
       const int64_t r = min(m0 + row, l.rows - 1) - m0;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(x, x_bytes), (lds_void_t*)(buf + region * 1024), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(x, x_bytes), (lds_void_t*)(buf + region * 1024), 16,
                                                (int)(r * K + (int64_t)st * kK8 + chunk * 16), 0, 0, 0);
     }
 #pragma unroll
@@ -91,7 +78,7 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
       const int region = wave * kWLoads8 + i, row = region * 16 + (lane >> 2);
       const int chunk = (lane & 3) ^ ((row >> 2) & 3);
       const int64_t base = w_base(region * 16);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.w.codes + base * kb, (l.w.n - base) * kb),
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(l.w.codes + base * kb, (l.w.n - base) * kb),
                                                (lds_void_t*)(buf + kXBytes8 + region * 1024), 16,
                                                (int)(w_row(row) * kb + (int64_t)st * (kK8 / 2) + chunk * 16), 0, 0, 0);
     }
@@ -102,7 +89,7 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   const int s_row = (wave & 3) * 64 + lane;
   const bool s_of_x = wave < 4;
   const int64_t s_base = s_of_x ? m0 : w_base((wave & 3) * 64);
-  const __amdgpu_buffer_rsrc_t scales = rsrc((s_of_x ? l.x_scales : l.w.scales) + s_base * ks,
+  const __amdgpu_buffer_rsrc_t scales = buffer_of((s_of_x ? l.x_scales : l.w.scales) + s_base * ks,
                                              ((s_of_x ? l.rows : l.w.n) - s_base) * ks);
   const int s_off = (int)((s_of_x ? min(m0 + s_row, l.rows - 1) - m0 : w_row(s_row)) * ks);
   u32x3_t s_next;
@@ -165,12 +152,13 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   };
   // Step st waits until only the next stage's loads are on their way.  The barrier
   // then tells that every wave has its part of stage st in LDS and is done with
-  // stage st - 1, whose buffer the refill takes.  Scales of stage st + 1 are written
-  // beside it, and after a group's last the next group is asked for, before the
-  // refill, so that waiting for it leaves the refill on its way.  There is no branch
-  // (past the last stage it is asked for again), so that the compiler's own counts
-  // of loads stay exact.
-  auto step = [&](int st, auto group_step, const uint8_t* cur, uint8_t* next, uint8_t* fill) {
+  // stage st - 1, whose buffer the refill takes.  The refill's scales are written
+  // before it (beside a stage that is on its way the write would wait for it), and
+  // after a group's last the next group is asked for, before the refill too, so that
+  // waiting for it leaves the refill on its way.  There is no branch (past the last
+  // stage it is asked for again), so that the compiler's own counts of loads stay
+  // exact.
+  auto step = [&](int st, auto group_step, const uint8_t* cur, uint8_t* fill) {
     constexpr int sg = decltype(group_step)::value;
     wait_loads<kStageLoads8>();
     __builtin_amdgcn_sched_barrier(0);
@@ -180,28 +168,30 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
     read(cur, 0);
     mma(std::integral_constant<int, 0>());
     read(cur, 1);
-    store_scales(next, (sg + 1) % kGroup8);
-    if (sg == 1) load_scales(st / kGroup8 + 1);
+    store_scales(fill, (sg + 2) % kGroup8);
+    if (sg == 0) load_scales(st / kGroup8 + 1);
     __builtin_amdgcn_sched_barrier(0);
     issue(min(st + 2, nstage - 1), fill);
     __builtin_amdgcn_sched_barrier(0);
     mma(std::integral_constant<int, 1>());
   };
   load_scales(0);
+  store_scales(s_b0, 0);
+  store_scales(s_b1, 1);
   issue(0, s_b0);
   issue(min(1, nstage - 1), s_b1);
-  store_scales(s_b0, 0);
   const std::integral_constant<int, 0> g0;
   const std::integral_constant<int, 1> g1;
   const std::integral_constant<int, 2> g2;
   int st = 0;
   for (; st + 3 <= nstage; st += 3) {
-    step(st, g0, s_b0, s_b1, s_b2);
-    step(st + 1, g1, s_b1, s_b2, s_b0);
-    step(st + 2, g2, s_b2, s_b0, s_b1);
+    step(st, g0, s_b0, s_b2);
+    step(st + 1, g1, s_b1, s_b0);
+    step(st + 2, g2, s_b2, s_b1);
   }
-  if (st < nstage) step(st, g0, s_b0, s_b1, s_b2);
-  if (st + 1 < nstage) step(st + 1, g1, s_b1, s_b2, s_b0);
+  if (st < nstage) step(st, g0, s_b0, s_b2);
+  if (st + 1 < nstage) step(st + 1, g1, s_b1, s_b0);
+  wait_loads<0>();                                  // (the last stage asked for again: its LDS may be another's next)
 
   auto put4 = [&](void* to, int64_t at, f32x4_t v, int count, int bf16) {
     if (bf16) {
