@@ -33,17 +33,29 @@ Plan plan(const LinearLaunch& l) {
   Plan p = {!l.transposed && l.rows <= (l.x_type == kXF32 ? 16 : 64), false, 1, 1};
   if (p.few) return p;
   const int cus = device_cu_count();
-  // Block-scaled products from a quarter as many tiles as CUs on (its offsets within
-  // 256 rows are 31-bit).  Measured, MXFP4, us, there / converted to bf16:
+  // Block-scaled products for bf16 results (the instruction drops more bits than an
+  // fp32 result should lose), from a quarter as many tiles as CUs on (its offsets
+  // within 256 rows are 31-bit).  Measured, MXFP4, us, there / converted to bf16:
   //   k, n        rows 256       512          1024         2048
   //   8192, 8192  88 /  69    90 / 106     92 / 163    114 / 253
   //   4096, 4096  45 /  34    45 /  43     51 /  58     53 /  87
   //   8192, 1024  79 /  29    79 /  33     90 /  43     91 /  69
-  p.mx8 = l.x_type == kXE4M3 && l.w.format == 0 && l.w.k > 0 && l.w.k % 128 == 0 && l.w.k <= 1 << 22 &&
+  p.mx8 = l.x_type == kXE4M3 && l.w.format == 0 && l.out_bf16 && (!l.products || l.products_bf16) && l.w.k > 0 && l.w.k % 128 == 0 && l.w.k <= 1 << 22 &&
           many_args(l, -1).ntiles >= cus / 4;
   if (p.mx8) return p;
-  const ManyArgs large = many_args(l, 1);
-  if (large.ntiles >= cus) return p;
+  const int tiles = many_args(l, 1).ntiles;
+  if (tiles >= cus && !ring_sizes(l)) return p;
+  if (ring_sizes(l)) {
+    // A tile a CU, in parts of 32 stages or more; a gradient's two a CU, in parts of
+    // 64 or more.
+    const int stages = many_args(l, 1).stages;
+    p.splits = (cus + tiles - 1) / tiles;
+    if (l.transposed) {
+      const int two = (2 * cus + tiles - 1) / tiles;
+      if (stages / two >= 64) p.splits = two;
+    }
+    if (p.splits == 1 || stages / p.splits >= 32) return p;
+  }
   p.size = 0;
   const ManyArgs small = many_args(l, 0);
   // parts of the contraction, of 8 stages at least, until every CU has two

@@ -82,18 +82,21 @@ __device__ __forceinline__ void many_multiply(const uint8_t* buf, f32x4_t (&acc)
     const int t = half < 0 ? i : half;
     u32x4_t wf[FN];
     if constexpr (T::kT) {
-      const uint8_t* c0 = bw + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * (T::TN / 2) + T::kColBytes * r;
+      // (hidden, as one addition to the buffer's address: more, and the compiler no
+      // longer tells which loads into LDS the reads have to wait for, and waits for all)
+      int c0 = T::kXBytes + (32 * t + 8 * g) * T::kWPitch + (4 * t + g) * 64 + wn * (T::TN / 2) + T::kColBytes * r;
+      asm volatile("" : "+v"(c0));
       const u32x2_t sb = *reinterpret_cast<const u32x2_t*>(
           bs + ((wn * T::TN + FN * r) / T::kBlock) * T::kSPitch + 32 * t + 8 * g);
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {     // rows i and i + 1 of this lane's 8
         uint32_t ca, cb;
         if constexpr (FN == 4) {
-          ca = *reinterpret_cast<const uint16_t*>(c0 + i * T::kWPitch);
-          cb = *reinterpret_cast<const uint16_t*>(c0 + (i + 1) * T::kWPitch);
+          ca = *reinterpret_cast<const uint16_t*>(buf + (c0 + i * T::kWPitch));
+          cb = *reinterpret_cast<const uint16_t*>(buf + (c0 + (i + 1) * T::kWPitch));
         } else {
-          ca = c0[i * T::kWPitch];
-          cb = c0[(i + 1) * T::kWPitch];
+          ca = buf[c0 + i * T::kWPitch];
+          cb = buf[c0 + (i + 1) * T::kWPitch];
         }
         const uint32_t sw = i < 4 ? sb.x : sb.y;
         const float sa = scale_operand<FMT>((sw >> (8 * (i & 3))) & 0xFFu);
@@ -368,11 +371,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
 // ----------------------------------------------------------------------------
 // The same tile for bf16 rows that are whole 16-byte pieces and stages.  x and
 // codes go straight into LDS, into a ring of three buffers, two stages ahead.
-// Eight waves: four side by side as above, and those twice, each four with one half
-// of a stage's contraction, so that every SIMD has two waves on one tile and still
-// no code is converted twice.  At the end the two fours exchange halves of their
-// rows' sums.  (Two workgroups of four waves a CU need twice the tiles: dx of 1024
-// rows, k and n 8192, took 207 us, or 151 in two parts with a join.)
+// NW = 4: waves as above, two workgroups on a CU.  NW = 8: four waves side by side
+// twice, each four with one half of a stage's contraction, so that every SIMD has
+// two waves on one tile and still no code is converted twice; at the end the two
+// fours exchange halves of their rows' sums.  Measured, k and n 8192, us, NVFP4 /
+// MXFP4 (at 1024 rows there is a tile a CU):
+//   rows   direction        many_kernel   NW = 4      NW = 8
+//   1024   forward          182 / 155     206 / 144   142 / 133
+//   2048   forward          282 / 244     282 / 231   271 / 254
+//   1024   gradient         196 / 178     207 / 188   168 / 157
+//   1024   in two parts                   151 / 141
+//   2048   gradient         272 / 248     242 / 211   331 / 311
+// so four waves where every CU has two workgroups.  (NVFP4 forward has not the
+// registers for that: its eight scales a lane spill.)
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base, int64_t bytes) {
@@ -385,11 +396,11 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
-template <int FMT, int MODE>
-__global__ __launch_bounds__(512) void ring_kernel(ManyArgs a) {
+template <int FMT, int MODE, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void ring_kernel(ManyArgs a) {
   constexpr int BM = 128, BN = 256;
   using T = ManyTile<FMT, kXBF16, MODE, BM, BN, 1, 4>;
-  using H = ManyTile<FMT, kXBF16, MODE, BM / 2, BN, 1, 4>;     // what a wave stores
+  constexpr int XL = 16 / NW, WL = 8 / NW;                      // a wave's loads of a stage
   // separate objects, so that reads of one are not ordered after loads into others
   __shared__ __align__(16) uint8_t s_b0[T::kBuf];
   __shared__ __align__(16) uint8_t s_b1[T::kBuf];
@@ -419,10 +430,10 @@ __global__ __launch_bounds__(512) void ring_kernel(ManyArgs a) {
   // the ends read the last one, columns past the end what lies there (zeros past
   // the plane's), and their results are not stored.
   const uint8_t* x = static_cast<const uint8_t*>(l.x) + m0 * l.x_stride * 2;
-  int x_off[2], w_off;
+  int x_off[4], w_off[2];                           // XL and WL of them
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {                     // 8 rows of x a load, 128 bytes each
-    const int row = (wave * 2 + i) * 8 + (lane >> 3);
+  for (int i = 0; i < XL; ++i) {                    // 8 rows of x a load, 128 bytes each
+    const int row = (wave * XL + i) * 8 + (lane >> 3);
     x_off[i] = (int)((min(m0 + row, l.rows - 1) - m0) * l.x_stride * 2) + x_chunk(row, lane & 7) * 16;
   }
   // row of the weight that local row i is (of the forward directions), from its side's first
@@ -432,117 +443,154 @@ __global__ __launch_bounds__(512) void ring_kernel(ManyArgs a) {
   };
   auto w_side = [&](int i) { return MODE == kGated && (i & 32) ? o0 + half : o0; };
   // 32 rows' 32 bytes a load, or 8 rows' 128
-  if constexpr (T::kT) w_off = (int)((wave * 8 + (lane >> 3)) * kb) + (lane & 7) * 16;
-  else w_off = (int)(w_row(wave * 32 + (lane >> 1)) * kb) + (lane & 1) * 16;
+#pragma unroll
+  for (int i = 0; i < WL; ++i) {
+    if constexpr (T::kT) w_off[i] = (int)(((wave * WL + i) * 8 + (lane >> 3)) * kb) + (lane & 7) * 16;
+    else w_off[i] = (int)(w_row((wave * WL + i) * 32 + (lane >> 1)) * kb) + (lane & 1) * 16;
+  }
   auto issue = [&](int st, uint8_t* buf) {
     const __amdgpu_buffer_rsrc_t xb = buffer_of(x + (int64_t)st * (kStage * 2), 0x7FFFFFFF);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void_t*)(buf + (wave * 2 + i) * 1024), 16, x_off[i], 0, 0, 0);
-    const int64_t at = T::kT ? (int64_t)st * kStage * kb + o0 / 2 : w_side(wave * 32) * kb + (int64_t)st * (kStage / 2);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(l.w.codes + at, l.w.n * kb - at),
-                                             (lds_void_t*)(buf + T::kXBytes + wave * (T::kT ? 1024 + 64 : 1024)), 16,
-                                             w_off, 0, 0, 0);
+    for (int i = 0; i < XL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void_t*)(buf + (wave * XL + i) * 1024), 16, x_off[i], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < WL; ++i) {
+      const int piece = wave * WL + i;
+      const int64_t at = T::kT ? (int64_t)st * kStage * kb + o0 / 2 : w_side(piece * 32) * kb + (int64_t)st * (kStage / 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(l.w.codes + at, l.w.n * kb - at),
+                                               (lds_void_t*)(buf + T::kXBytes + piece * (T::kT ? 1024 + 64 : 1024)), 16,
+                                               w_off[i], 0, 0, 0);
+    }
   };
-  // Scales go through a register: a row's two halves in two threads; transposed, an
-  // eighth of a row's blocks in each of eight, to the places of their blocks.
-  constexpr int kHave = T::kT ? BN / T::kBlock / 8 : kStage / T::kBlock / 2;    // 1 or 2 bytes
-  using scale_t = typename std::conditional<kHave == 1, uint8_t, uint16_t>::type;
+  // Scales go through a register: a thread has a row's, or a half of them, and
+  // transposed a fourth or an eighth, which it puts to the places of their blocks.
+  constexpr int kBlocks = T::kT ? BN / T::kBlock : kStage / T::kBlock;          // a row's in a stage
+  constexpr int kThreadsRow = T::kT ? NW : NW / 4;
+  constexpr int kHave = kBlocks / kThreadsRow;                                  // 1, 2 or 4 bytes
+  using scale_t = typename std::conditional<kHave == 1, uint8_t,
+                                            typename std::conditional<kHave == 2, uint16_t, uint32_t>::type>::type;
+  const int s_row = tid / kThreadsRow, s_col = tid % kThreadsRow * kHave;
   int s_off;                                        // from the tile's first scale (transposed: the stage's)
-  bool s_in = true;
   if constexpr (T::kT) {
-    const int col = (tid & 7) * kHave;
-    s_in = o0 / T::kBlock + col < srow;             // (K is a multiple of 64: both are there or not)
-    s_off = (tid >> 3) * (int)srow + col;
+    // (K is a multiple of 64: all are there or none, and then the row's first ones stand in)
+    s_off = s_row * (int)srow + (o0 / T::kBlock + s_col < srow ? s_col : 0);
   } else {
-    s_off = (int)((w_side(tid >> 1) - o0 + w_row(tid >> 1)) * srow) + (tid & 1) * kHave;
+    s_off = (int)((w_side(s_row) - o0 + w_row(s_row)) * srow) + s_col;
   }
-  uint32_t s_next;
   auto load_scales = [&](int st) {
     const uint8_t* p = l.w.scales + (T::kT ? (int64_t)st * kStage * srow + o0 / T::kBlock
                                            : o0 * srow + (int64_t)st * (kStage / T::kBlock));
-    s_next = 0u;
-    if (s_in) s_next = load_any<scale_t>(p + s_off);
+    return (uint32_t)load_any<scale_t>(p + s_off);
   };
-  auto store_scales = [&](uint8_t* buf) {
+  auto store_scales = [&](uint8_t* buf, uint32_t v) {
     uint8_t* bs = buf + T::kXBytes + T::kWBytes;
     if constexpr (T::kT) {
 #pragma unroll
-      for (int i = 0; i < kHave; ++i) bs[((tid & 7) * kHave + i) * T::kSPitch + (tid >> 3)] = (uint8_t)(s_next >> (8 * i));
+      for (int i = 0; i < kHave; ++i) bs[(s_col + i) * T::kSPitch + s_row] = (uint8_t)(v >> (8 * i));
     } else {
-      *reinterpret_cast<scale_t*>(bs + tid * kHave) = (scale_t)s_next;
+      *reinterpret_cast<scale_t*>(bs + tid * kHave) = (scale_t)v;
     }
   };
-  // As the block-scaled kernel's step: wait until only the next stage's loads are on
-  // their way, meet, ask for the stage after the next, which goes where the one
-  // before lay, and multiply.  Scales are written there before: beside a stage that
-  // is on its way the write would wait for it.  No branch, so that the compiler's
-  // counts stay exact.
-  auto step = [&](int st, const uint8_t* cur, uint8_t* fill) {
-    wait_loads<4>();
+  // As the block-scaled kernel's step: wait until only the loads of the step before
+  // are on their way, which are the next stage's, meet, ask for the stage after the
+  // next, which goes where the one before lay, and multiply.  Scales are written
+  // there before: beside a stage that is on its way the write would wait for it.
+  // They are asked for three steps ahead, each position of the ring's into a register
+  // of its own, and first in their step, so that nothing waits for them.  The order of
+  // loads is fixed, and there is no branch, so that all counts are exact; after the
+  // loop nobody takes the scales that are asked for, the compiler leaves those loads
+  // out, and a step has one less on its way.
+  auto step = [&](int st, const uint8_t* cur, uint8_t* fill, uint32_t& sc, auto looped) {
+    wait_loads<XL + WL + (decltype(looped)::value ? 1 : 0)>();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    store_scales(fill);
-    load_scales(min(st + 3, s1 - 1));
+    store_scales(fill, sc);
+    sc = load_scales(min(st + 5, s1 - 1));
+    __builtin_amdgcn_sched_barrier(0);
     issue(min(st + 2, s1 - 1), fill);
     __builtin_amdgcn_sched_barrier(0);
     // (the lane's part of the addresses is made anew each time: kept for three
     // buffers, it would take more registers than there are)
     int rr = r, gg = g;
     asm volatile("" : "+v"(rr), "+v"(gg));
-    many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, part);
+    if constexpr (NW == 8) {
+      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, part);
+    } else {
+      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, 0);
+      __builtin_amdgcn_sched_barrier(0);            // (or both halves' operands would be held at once)
+      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, 1);
+    }
   };
   if (s0 < s1) {
-    load_scales(s0);
-    store_scales(s_b0);
-    load_scales(min(s0 + 1, s1 - 1));
-    store_scales(s_b1);
+    store_scales(s_b0, load_scales(s0));
+    store_scales(s_b1, load_scales(min(s0 + 1, s1 - 1)));
+    uint32_t sc0 = load_scales(min(s0 + 2, s1 - 1)), sc1 = load_scales(min(s0 + 3, s1 - 1));
+    __builtin_amdgcn_sched_barrier(0);
     issue(s0, s_b0);
-    load_scales(min(s0 + 2, s1 - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    uint32_t sc2 = load_scales(min(s0 + 4, s1 - 1));
+    __builtin_amdgcn_sched_barrier(0);
     issue(min(s0 + 1, s1 - 1), s_b1);
+    const std::true_type looped;
+    const std::false_type last;
     int st = s0;
     for (; st + 3 <= s1; st += 3) {
-      step(st, s_b0, s_b2);
-      step(st + 1, s_b1, s_b0);
-      step(st + 2, s_b2, s_b1);
+      step(st, s_b0, s_b2, sc0, looped);
+      step(st + 1, s_b1, s_b0, sc1, looped);
+      step(st + 2, s_b2, s_b1, sc2, looped);
     }
-    if (st < s1) step(st, s_b0, s_b2);
-    if (st + 1 < s1) step(st + 1, s_b1, s_b0);
+    if (st < s1) step(st, s_b0, s_b2, sc0, last);
+    if (st + 1 < s1) step(st + 1, s_b1, s_b0, sc1, last);
   }
 
-  // The first four waves take rows 0 to 63, the others 64 to 127: each gives the
-  // other its sums of them, 8 KiB at a time.
-  f32x4_t mine[H::FN][H::FM];
-  auto region = [&](int i) {
-    uint8_t* buf = i < 3 ? s_b0 : i < 6 ? s_b1 : s_b2;
-    return reinterpret_cast<f32x4_t*>(buf + i % 3 * 8192) + lane;
-  };
-  wait_loads<0>();                                  // (the last stage asked for again is on its way to them)
+  wait_loads<0>();                                  // (the last stage, asked for again, is on its way to the ring)
+  if constexpr (NW == 4) {
+    many_results<T, FMT, MODE>(a, acc, m0, o0, 0, wn, r, g);
+  } else {
+    // The first four waves take rows 0 to 63, the others 64 to 127: each gives the
+    // other its sums of them, 8 KiB at a time.
+    using H = ManyTile<FMT, kXBF16, MODE, BM / 2, BN, 1, 4>;
+    f32x4_t mine[H::FN][H::FM];
+    auto region = [&](int i) {
+      uint8_t* buf = i < 3 ? s_b0 : i < 6 ? s_b1 : s_b2;
+      return reinterpret_cast<f32x4_t*>(buf + i % 3 * 8192) + lane;
+    };
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    __syncthreads();
+    for (int q = 0; q < 2; ++q) {
+      __syncthreads();
 #pragma unroll
-    for (int n = 0; n < T::FN; ++n)
+      for (int n = 0; n < T::FN; ++n)
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        region(wave)[(n * 2 + m) * 64] = part ? acc[n][2 * q + m] : acc[n][4 + 2 * q + m];
-    __syncthreads();
+        for (int m = 0; m < 2; ++m)
+          region(wave)[(n * 2 + m) * 64] = part ? acc[n][2 * q + m] : acc[n][4 + 2 * q + m];
+      __syncthreads();
 #pragma unroll
-    for (int n = 0; n < T::FN; ++n)
+      for (int n = 0; n < T::FN; ++n)
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        mine[n][2 * q + m] = (part ? acc[n][4 + 2 * q + m] : acc[n][2 * q + m]) + region(wave ^ 4)[(n * 2 + m) * 64];
+        for (int m = 0; m < 2; ++m)
+          mine[n][2 * q + m] = (part ? acc[n][4 + 2 * q + m] : acc[n][2 * q + m]) + region(wave ^ 4)[(n * 2 + m) * 64];
+    }
+    many_results<H, FMT, MODE>(a, mine, m0 + 64 * part, o0, 0, wn, r, g);
   }
-  many_results<H, FMT, MODE>(a, mine, m0 + 64 * part, o0, 0, wn, r, g);
 }
 
-// Whether the rows are whole pieces and stages, and offsets small enough.
+// Whether rows are whole stages and offsets small enough, and whether the pieces of
+// them are aligned.  (The plan asks the sizes alone: a workspace is asked for before
+// the call.)
+inline bool ring_sizes(const LinearLaunch& l) {
+  return l.x_type == kXBF16 && l.w.k > 0 && l.w.k % kStage == 0 && l.w.n % (l.transposed ? kStage : 1) == 0 &&
+         l.w.k <= 1 << 22 && (!l.gated || l.w.n / 2 * (l.w.k / 16) < (int64_t)1 << 31);
+}
 inline bool ring_fits(const LinearLaunch& l) {
-  const int64_t most = (int64_t)1 << 22;
-  return l.x_type == kXBF16 && l.w.k % kStage == 0 && (l.transposed ? l.w.n : l.w.k) % kStage == 0 && l.w.k <= most &&
-         l.x_stride % 8 == 0 && l.x_stride <= most && (!l.gated || l.w.n / 2 * (l.w.k / 16) < (int64_t)1 << 31) && reinterpret_cast<uintptr_t>(l.x) % 16 == 0 &&
+  return ring_sizes(l) && l.x_stride % 8 == 0 && l.x_stride <= 1 << 22 && reinterpret_cast<uintptr_t>(l.x) % 16 == 0 &&
          reinterpret_cast<uintptr_t>(l.w.codes) % 16 == 0;
+}
+
+template <int FMT, int MODE, int NW>
+hipError_t launch_ring(const ManyArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((ring_kernel<FMT, MODE, NW>), dim3((a.ntiles + 7) / 8 * 8, a.splits), dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
 }
 
 template <int FMT, int XT, int MODE, int BM, int BN, int WM, int WN>
@@ -576,8 +624,10 @@ hipError_t launch_many_size(const ManyArgs& a, int size, hipStream_t s) {
   constexpr int BM = many_size(XT, 1).bm;
   if constexpr (XT == kXBF16) {
     if (ring_fits(a.l)) {
-      hipLaunchKernelGGL((ring_kernel<FMT, MODE>), dim3((a.ntiles + 7) / 8 * 8, a.splits), dim3(512), 0, s, a);
-      return hipGetLastError();
+      if constexpr (FMT == 0 || MODE == kTransposed) {
+        if ((int64_t)a.ntiles * a.splits >= 2 * device_cu_count()) return launch_ring<FMT, MODE, 4>(a, s);
+      }
+      return launch_ring<FMT, MODE, 8>(a, s);
     }
   }
   return launch_many_t<FMT, XT, MODE, BM, 256, 1, 4>(a, s);

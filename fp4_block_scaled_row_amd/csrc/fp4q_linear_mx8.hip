@@ -126,9 +126,12 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   // read has to wait for only where the read's address is a step or two from the
   // buffer's (else it waits for all, which took 110 us for 106).
   auto read = [&](const uint8_t* buf, int kk) {
-    const int part = 2 * kk + (lane >> 5);          // this lane's 32 of the stage's k
-    int x0 = (64 * wx + (lane & 31)) * kK8 + ((2 * part) ^ ((lane >> 1) & 7)) * 16, x1 = x0 ^ 16;
-    int w0 = kXBytes8 + (128 * ww + (lane & 31)) * (kK8 / 2) + (part ^ ((lane >> 2) & 3)) * 16;
+    // Of the instruction's 64 a lane has 32: 4-bit ones, and the scales of both sides,
+    // 32 h to 32 h + 31 (h = lane / 32); 8-bit ones 16 h to 16 h + 15 in its first four
+    // registers, and those and 32 in the other four.
+    const int h = lane >> 5;
+    int x0 = (64 * wx + (lane & 31)) * kK8 + ((4 * kk + h) ^ ((lane >> 1) & 7)) * 16, x1 = x0 ^ 32;
+    int w0 = kXBytes8 + (128 * ww + (lane & 31)) * (kK8 / 2) + ((2 * kk + h) ^ ((lane >> 2) & 3)) * 16;
     asm volatile("" : "+v"(x0), "+v"(x1), "+v"(w0));
 #pragma unroll
     for (int u = 0; u < kSubX; ++u) {
@@ -178,7 +181,9 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   load_scales(0);
   store_scales(s_b0, 0);
   store_scales(s_b1, 1);
+  __builtin_amdgcn_sched_barrier(0);                // (the order of loads is what a count of them means)
   issue(0, s_b0);
+  __builtin_amdgcn_sched_barrier(0);
   issue(min(1, nstage - 1), s_b1);
   const std::integral_constant<int, 0> g0;
   const std::integral_constant<int, 1> g1;
