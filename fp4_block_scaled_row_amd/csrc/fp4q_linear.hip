@@ -43,18 +43,23 @@ Plan plan(const LinearLaunch& l) {
   p.mx8 = l.x_type == kXE4M3 && l.w.format == 0 && l.out_bf16 && (!l.products || l.products_bf16) && l.w.k > 0 && l.w.k % 128 == 0 && l.w.k <= 1 << 22 &&
           many_args(l, -1).ntiles >= cus / 4;
   if (p.mx8) return p;
-  const int tiles = many_args(l, 1).ntiles;
-  if (tiles >= cus && !ring_sizes(l)) return p;
-  if (ring_sizes(l)) {
-    // A tile a CU, in parts of 32 stages or more; a gradient's two a CU, in parts of
-    // 64 or more.
-    const int stages = many_args(l, 1).stages;
-    p.splits = (cus + tiles - 1) / tiles;
-    if (l.transposed) {
-      const int two = (2 * cus + tiles - 1) / tiles;
-      if (stages / two >= 64) p.splits = two;
-    }
-    if (p.splits == 1 || stages / p.splits >= 32) return p;
+  // Large tiles from one a CU on; whole stages also in parts of 32 stages or more
+  // that give each CU one, forward of 128 stages or more in all.  Measured, bf16,
+  // NVFP4, us, parts of large tiles / of small ones:
+  //   k, n              rows 256     512         1024        2048
+  //   8192, 8192        62 / 70      97 / 113
+  //   4096, 16384       63 / 59
+  //   4096, 4096                                 65 / 61
+  //   8192, 1024                                             62 / 70
+  //   gradient: 8192, 8192           107 / 133
+  //   k 4096, n 16384   58 / 75      90 / 139    151 / 261
+  //   4096, 4096                                 59 / 71
+  const ManyArgs large = many_args(l, 1);
+  const int parts = (cus + large.ntiles - 1) / large.ntiles;
+  if (parts == 1) return p;
+  if (ring_sizes(l) && large.stages / parts >= 32 && (l.transposed || large.stages >= 128)) {
+    p.splits = parts;
+    return p;
   }
   p.size = 0;
   const ManyArgs small = many_args(l, 0);

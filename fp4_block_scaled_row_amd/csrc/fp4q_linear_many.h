@@ -375,15 +375,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
 // twice, each four with one half of a stage's contraction, so that every SIMD has
 // two waves on one tile and still no code is converted twice; at the end the two
 // fours exchange halves of their rows' sums.  Measured, k and n 8192, us, NVFP4 /
-// MXFP4 (at 1024 rows there is a tile a CU):
-//   rows   direction        many_kernel   NW = 4      NW = 8
-//   1024   forward          182 / 155     206 / 144   142 / 133
-//   2048   forward          282 / 244     282 / 231   271 / 254
-//   1024   gradient         196 / 178     207 / 188   168 / 157
-//   1024   in two parts                   151 / 141
-//   2048   gradient         272 / 248     242 / 211   331 / 311
+// MXFP4 (at 1024 rows there is a tile a CU, at 2048 two):
+//   rows   direction    many_kernel   NW = 4      NW = 8
+//   1024   forward      182 / 155     206 / 144   138 / 129
+//   2048   forward      282 / 244     282 / 235   273 / 251
+//   1024   gradient     196 / 178     207 / 188   137 / 120
+//   2048   gradient     272 / 248     236 / 218   271 / 236
 // so four waves where every CU has two workgroups.  (NVFP4 forward has not the
-// registers for that: its eight scales a lane spill.)
+// registers for that: its eight scales a lane spill.)  The conversion bounds it: a
+// wave's 8 codes cost 4 conversions, 8 multiplications (NVFP4) and 4 joins of bf16
+// pairs for the 8 matrix instructions (64 of the matrix unit's clocks) that use them.
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* base, int64_t bytes) {

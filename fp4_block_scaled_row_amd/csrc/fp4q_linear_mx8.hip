@@ -5,20 +5,29 @@
 // the rate of bf16 and without any conversion.  k a multiple of 128.
 //
 // v_mfma_scale_f32_32x32x64_f8f6f4, weights as the left operand: lane l supplies
-// row (l mod 32) of either side for k = 32 (l / 32) .. + 31 (16 bytes of E2M1, 32
-// of E4M3) with that block's scale byte; result register i of lane l is weight
-// row 8 (i / 4) + 4 (l / 32) + i mod 4 for row l mod 32 of x: 4 consecutive
-// outputs of a row.
+// row l mod 32 of either side.  With h = l / 32 its 32 E2M1 codes (16 bytes), and
+// its scale byte of either side, are those of k = 32 h .. + 31; its 32 E4M3 codes
+// are those of 16 h .. + 15 and of 32 + 16 h .. + 15.  Result register i is weight
+// row 8 (i / 4) + 4 h + i mod 4 for row l mod 32 of x: 4 consecutive outputs of a
+// row.  The instruction adds eight neighbouring products at a time, lined up by the
+// largest exponent among them, and drops what lies below 2^-13 of that; sums of
+// eights are fp32's.  That is less than a bf16 result's rounding, to which alone
+// these kernels write; fp32 results take the bf16 instructions, whose sums are
+// fp32's throughout.
 //
 // A workgroup of 8 waves computes 256 rows of x by 256 of the weight, each wave 64
 // x 128: the side with the wider elements is read twice from LDS, the other four
 // times.  (128 x 128 a wave would read less and takes all 256 accumulator
-// registers, which the compiler spills around.)  A stage is 128 k: 32 KiB of x and 16
-// KiB of codes, loaded straight into LDS into a ring of three buffers, two stages
+// registers, which the compiler spills around.)  A stage is 128 k: 32 KiB of x and
+// 16 KiB of codes, loaded straight into LDS into a ring of three buffers, two stages
 // ahead.  Scales come 12 bytes a row (three stages) a load, a row a lane, and are
 // written beside the stage they belong to: loaded by the lanes that use them they
-// would cost the load unit as long as the products take.  LDS rows are 128 and 64 bytes, their 16-byte
-// chunks exchanged so that reads of one chunk of 16 rows meet all banks.
+// would cost the load unit as long as the products take.  LDS rows are 128 and 64
+// bytes, their 16-byte chunks exchanged so that reads of one chunk of 16 rows meet
+// all banks.
+//
+// 2048 rows, k and n 8192: 105 us, 2.6 PFLOP/s, where a library's product of E4M3
+// matrices of that size reaches 2.9 (converted to bf16: 253 us).
 #include <type_traits>
 
 #include "fp4q_linear_many.h"
