@@ -271,6 +271,7 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
 #pragma unroll
             for (int p = 0; p < P; ++p) acc[t][m] = mfma16(wf, xf[m][p], acc[t][m]);
         }
+        if constexpr (NT * MT >= 12) __builtin_amdgcn_sched_barrier(0);   // (registers: one step's operands at a time)
       }
   };
 
@@ -317,46 +318,61 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
     }
   }
 
-  // ---- the sums of a wave's tiles, to where x was
+  // ---- the sums of a wave's tiles, to where x was: four weight rows' of row m of x
+  // a 16-byte piece, 4 of a tile (number q), m exchanged by q so that neighbouring
+  // lanes' reads of 4 pieces of 4 rows meet all banks (as they lie, and read 4 bytes
+  // a lane, they took 2 of 26 us of 40 rows gated)
   __syncthreads();
-  float* s_sum = reinterpret_cast<float*>(s_x);      // [wave][tile][lane][4]
+  f32x4_t* s_sum = reinterpret_cast<f32x4_t*>(s_x);      // [wave][tile][q][m]
+  auto sum_at = [&](int w, int t, int mt, int q, int m) {
+    return ((w * NT + t) * MT + mt) * 64 + q * 16 + (m ^ (4 * q));
+  };
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      *reinterpret_cast<f32x4_t*>(s_sum + ((wave * NT * MT + t * MT + m) * 64 + lane) * 4) = acc[t][m];
+    for (int m = 0; m < MT; ++m) s_sum[sum_at(wave, t, m, g, r)] = acc[t][m];
   __syncthreads();
 
-  // element (row of x, weight row) of the joined sums
   const float tensor = FMT == 1 ? *l.w.g : 1.0f;
-  auto sum = [&](int t, int m, int n) {
-    float s = 0.0f;
+  auto sum = [&](int t, int m, int q) {
+    f32x4_t v = s_sum[sum_at(0, t, m >> 4, q, m & 15)];
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w)
-      s += s_sum[((w * NT * MT + t * MT + (m >> 4)) * 64 + (m & 15) + 16 * (n >> 2)) * 4 + (n & 3)];
-    return s * tensor;
+    for (int w = 1; w < kFewWaves; ++w) v += s_sum[sum_at(w, t, m >> 4, q, m & 15)];
+    return v * tensor;
   };
-  auto put = [&](void* to, int64_t at, float v, int bf16) {
-    if (bf16) static_cast<__bf16*>(to)[at] = (__bf16)v;
-    else static_cast<float*>(to)[at] = v;
-  };
-  constexpr int kCols = 16 * kSide;
-  for (int e = tid; e < rows * kCols; e += kFewThreads) {
-    const int m = e / kCols, nn = e % kCols;
-    const int64_t n = n0 + nn;
-    if (n >= half) continue;
-    float v = sum(nn >> 4, m, nn & 15);
-    if constexpr (GATED) {
-      const float u = sum(kSide + (nn >> 4), m, nn & 15);
-      if (l.products) {
-        put(l.products, m * l.w.n + n, v, l.products_bf16);
-        put(l.products, m * l.w.n + half + n, u, l.products_bf16);
-      }
-      v = v * sigmoid(v) * u;
-    } else if (l.bias) {
-      v += l.out_bf16 ? (float)static_cast<const __bf16*>(l.bias)[n] : static_cast<const float*>(l.bias)[n];
+  auto put = [&](void* to, int64_t at, f32x4_t v, int count, int bf16) {   // the first `count`, at most 4
+    if (bf16) {
+      __bf16* o = static_cast<__bf16*>(to) + at;
+      if (count >= 4) store_any(o, u32x2_t{pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)});
+      else for (int i = 0; i < count; ++i) o[i] = (__bf16)v[i];
+    } else {
+      float* o = static_cast<float*>(to) + at;
+      if (count >= 4) store_any(o, v);
+      else for (int i = 0; i < count; ++i) o[i] = v[i];
     }
-    put(l.out, m * half + n, v, l.out_bf16);
+  };
+  constexpr int kPieces16 = 4 * kSide;                   // of a row
+  for (int e = tid; e < rows * kPieces16; e += kFewThreads) {
+    const int m = e / kPieces16, q = e % kPieces16;
+    const int64_t n = n0 + 4 * q;
+    const int count = (int)min(half - n, (int64_t)4);
+    if (count <= 0) continue;
+    f32x4_t v = sum(q >> 2, m, q & 3);
+    if constexpr (GATED) {
+      const f32x4_t u = sum(kSide + (q >> 2), m, q & 3);
+      if (l.products) {
+        put(l.products, m * l.w.n + n, v, count, l.products_bf16);
+        put(l.products, m * l.w.n + half + n, u, count, l.products_bf16);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
+    } else if (l.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < count)
+          v[i] += l.out_bf16 ? (float)static_cast<const __bf16*>(l.bias)[n + i] : static_cast<const float*>(l.bias)[n + i];
+    }
+    put(l.out, m * half + n, v, count, l.out_bf16);
   }
 }
 
@@ -374,9 +390,33 @@ hipError_t launch_t(const LinearLaunch& l, int log_kp, hipStream_t s) {
   return hipGetLastError();
 }
 
+// 17 to 48 rows: two tiles a workgroup, or four or six, by the workgroups that CUs
+// take one after another (LDS holds one at a time), each as long as its tiles and one
+// and a half, for x.  Measured, MXFP4 (NVFP4), k 4096, us, 24 rows / 40 rows:
+//   n       two tiles                  four                       six
+//   4096     7.7 (8.9) /  9.7 (10.8)    9.4 (12.2) / 11.9 (14.8)  11.5 (17.1) / 18.3 (31.3)
+//   16384   14.0 (17.2) / 18.1 (20.9)  11.8 (14.0) / 13.7 (16.7)  14.3 (19.7) / 21.2 (36.2)
+//   20000 (gated, 40 rows): 25.4, 23.7, 21.1
+// Six with 33 rows and more want more registers than there are: MXFP4 with bf16
+// alone takes them (52 spilled).
+template <int FMT, int XT, int MT, bool GATED>
+hipError_t launch_nt(const LinearLaunch& l, hipStream_t s) {
+  constexpr bool kSix = MT == 2 || (FMT == 0 && XT == kXBF16);
+  const int64_t cus = device_cu_count();
+  auto cost = [&](int nt) {
+    const int64_t groups = (l.w.n + 16 * nt - 1) / (16 * nt);
+    return (groups + cus - 1) / cus * (3 + 2 * nt);
+  };
+  if constexpr (kSix) {
+    if (cost(6) < cost(4) && cost(6) < cost(2)) return launch_t<FMT, XT, MT, 6, 128, 1, GATED, false>(l, 0, s);
+  }
+  if (cost(4) < cost(2)) return launch_t<FMT, XT, MT, 4, 128, 1, GATED, false>(l, 0, s);
+  return launch_t<FMT, XT, MT, 2, 128, 1, GATED, false>(l, 0, s);
+}
+
 // Two tiles a workgroup, which share what is read of x (24 rows of k 8192 by n
-// 8192: 14.9 us; four tiles 23, one 21), one where two would leave CUs without
-// work; one chunk in flight (two: 15.9 us; the other waves' loads hide the rest).
+// 8192: 14.7 us; one tile 21), one where two would leave CUs without work; one chunk
+// in flight (two: 15.9 us; the other waves' loads hide the rest).
 template <int FMT, int XT, bool GATED>
 hipError_t launch_m(const LinearLaunch& l, hipStream_t s) {
   // all of x in LDS where 64 KiB hold it (and one tile its rows)
@@ -390,8 +430,8 @@ hipError_t launch_m(const LinearLaunch& l, hipStream_t s) {
   }
   if (l.rows <= 16) return launch_t<FMT, XT, 1, 2, 128, 1, GATED, false>(l, 0, s);
   if constexpr (XT != kXF32) {                 // (its three planes of 17 rows and more do not fit)
-    if (l.rows <= 32) return launch_t<FMT, XT, 2, 2, 128, 1, GATED, false>(l, 0, s);
-    if (l.rows <= 48) return launch_t<FMT, XT, 3, 2, 128, 1, GATED, false>(l, 0, s);
+    if (l.rows <= 32) return launch_nt<FMT, XT, 2, GATED>(l, s);
+    if (l.rows <= 48) return launch_nt<FMT, XT, 3, GATED>(l, s);
     return launch_t<FMT, XT, 4, 2, 128, 1, GATED, false>(l, 0, s);
   }
   return hipErrorInvalidValue;

@@ -191,3 +191,17 @@ def test_nothing_past_the_ends_and_again(fq, fmt, kind, rows):
         fq.fp4_linear(x, w, out=out)
         assert torch.equal(out, first)
     assert (space[:4096] == 7).all() and (space[4096 + rows * n:] == 7).all()
+
+
+# Few rows of wide weights: two, four and six tiles of the weight a workgroup, the last of them partly there.
+@pytest.mark.parametrize("fmt,kind", [("nvfp4", "bf16"), ("mxfp4", "bf16"), ("mxfp4", "mxfp8"), ("nvfp4", "mxfp8")])
+@pytest.mark.parametrize("rows", [17, 32, 33, 48])
+@pytest.mark.parametrize("n,k", [(8193, 160), (16401, 416), (20001, 96)])
+def test_few_rows_wide(fq, fmt, kind, rows, n, k):
+    check_linear(fq, fmt, kind, rows, n, k, rows + n, bias=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,f,k", [(24, 8200, 160), (40, 8201, 288), (24, 10001, 416), (48, 10007, 160)])
+def test_few_rows_wide_gated(fq, fmt, rows, f, k):
+    check_gated(fq, fmt, "bf16", rows, f, k, rows + f)
