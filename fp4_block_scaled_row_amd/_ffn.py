@@ -106,6 +106,17 @@ def _buffer(t, what, shape, dtype, device):
     return t
 
 
+def _apart(t, what, *others):
+    """Refuses a buffer t of the caller's that overlaps one of the others (2-D or dense tensors, or None)."""
+    lo, hi = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    for o in others:
+        if o is None or o.numel() == 0:
+            continue
+        span = (sum((n - 1) * s for n, s in zip(o.shape, o.stride())) + 1) * o.element_size()
+        if lo < o.data_ptr() + span and o.data_ptr() < hi:
+            raise ValueError("fp4q: %s must not overlap what the call reads or its other results" % what)
+
+
 def _activations(x, w, out_dtype):
     """x of a linear layer as LinearArgs fields, and the output's dtype."""
     if isinstance(x, Mx8Result):
@@ -154,9 +165,11 @@ def fp4_linear(x, w, *, bias=None, out_dtype=None, out=None):
     _weight(w)
     _, fields, dtype = _activations(x, w, out_dtype)
     code = _out_dtype(dtype)
-    out = _buffer(out, "out", (fields[2], w.n), dtype, w.device)
     if bias is not None:
         _buffer(bias, "bias", (w.n,), dtype, w.device)
+    if out is not None:
+        _apart(out, "out", *(x if isinstance(x, Mx8Result) else (x,)), bias, w.codes, w.scales, w.global_scale)
+    out = _buffer(out, "out", (fields[2], w.n), dtype, w.device)
     a = _lib.LinearArgs(*fields, code, None if bias is None else bias.data_ptr(), out.data_ptr(), None, code)
     _linear(w, a, _lib.FP4Q_LINEAR, _lib.load().fp4q_linear, "fp4q_linear")
     return out
@@ -168,6 +181,8 @@ def fp4_linear_backward(dy, w, *, out=None):
     gradient of a bias is dy.sum(0).)"""
     _weight(w)
     rows, stride, code = _rows(dy, "dy", w._index, w.n)
+    if out is not None:
+        _apart(out, "out", dy, w.codes, w.scales, w.global_scale)
     out = _buffer(out, "out", (rows, w.k), dy.dtype, w.device)
     a = _lib.LinearArgs(dy.data_ptr(), None, rows, stride, code, code, None, out.data_ptr(), None, code)
     _linear(w, a, _lib.FP4Q_LINEAR_BACKWARD, _lib.load().fp4q_linear_backward, "fp4q_linear_backward")
@@ -187,6 +202,8 @@ def fp4_gated(x, w, *, return_products=False, products_dtype=torch.float32, out_
         raise ValueError("fp4q: a gated weight has an even number of rows, got %d" % w.n)
     _, fields, dtype = _activations(x, w, out_dtype)
     code = _out_dtype(dtype)
+    if out is not None:
+        _apart(out, "out", *(x if isinstance(x, Mx8Result) else (x,)), w.codes, w.scales, w.global_scale)
     out = _buffer(out, "out", (fields[2], w.n // 2), dtype, w.device)
     products = None
     if return_products:
@@ -235,14 +252,16 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, quantize=None, return_rstd=F
     quantize="mxfp8" (d a multiple of 32) an Mx8Result, which fp4_linear and
     fp4_gated take and dequantize("mxfp8", ...) reads; summed is s (None without
     a residual: it is x); rstd, fp32 [rows], with return_rstd, for
-    rms_norm_backward.  out, summed: buffers to write; summed may be x or residual
-    itself, which updates a residual stream in place."""
+    rms_norm_backward.  out, summed: buffers to write; either may be a dense x or
+    residual itself (summed so updates a residual stream in place), and overlaps
+    nothing else."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
         raise ValueError("fp4q: x must be a 2-D GPU tensor")
     index, d, device = x.get_device(), x.shape[1], x.device
     rows, stride, code = _rows(x, "x", index, d)
     w_code = _vector(weight, "weight", d, index)
     r_stride = 0
+    given = out is not None or summed is not None
     if residual is not None:
         r_rows, r_stride, r_code = _rows(residual, "residual", index, d)
         if r_rows != rows or r_code != code:
@@ -263,6 +282,13 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, quantize=None, return_rstd=F
         y, codes, scales = None, out.codes.data_ptr(), out.scales.data_ptr()
     else:
         raise ValueError("fp4q: quantize is None or 'mxfp8', got %r" % (quantize,))
+    if given:
+        # a row is read before any of it is written: y and s may be written over the whole of x or residual
+        results = list(out) if quantize else [out]
+        for i, t in enumerate(results + ([] if summed is None else [summed])):
+            over = [o for o in (x, residual) if o is not None and not (o.is_contiguous() and o.data_ptr() == t.data_ptr()
+                                                                      and t.dtype == o.dtype)]
+            _apart(t, "out or summed", weight, *over, *results[i + 1:], *([summed] if i < len(results) else []))
     rstd = torch.empty(rows, dtype=torch.float32, device=device) if return_rstd else None
     a = _lib.RmsNormArgs(x.data_ptr(), None if residual is None else residual.data_ptr(), stride, r_stride,
                          weight.data_ptr(), y, None if summed is None else summed.data_ptr(),

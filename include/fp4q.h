@@ -393,7 +393,8 @@ fp4q_status fp4q_kv_attention(const fp4q_kv_cache *cache, const fp4q_kv_attentio
  * A weight [n][k] is the planes that fp4q_quantize_mxfp4 or
  * fp4q_quantize_nvfp4 (policies NV_MAX6 and FOUR_OVER_SIX) writes for it: codes
  * [n][k / 2], scales [n][k / block].  n and k: to 2^31 - 1; k a multiple of the
- * block.  Any n, any alignment.  FP4Q_IF4 is UNSUPPORTED. */
+ * block.  Any n, any alignment.  FP4Q_IF4 is UNSUPPORTED.  What a call of this
+ * group writes overlaps nothing that it reads, except where it is said. */
 typedef struct {
   int32_t format;              /* FP4Q_MXFP4 or FP4Q_NVFP4 */
   int64_t n, k;
@@ -424,7 +425,9 @@ size_t fp4q_linear_workspace_bytes(const fp4q_weight *weight, const fp4q_linear_
 /* out [rows][n] = x W^T + bias.  Weights and activations enter exactly, sums are
  * fp32 in an order that the shapes fix (a call gives the same bits each time),
  * the tensor scale and the bias are applied in fp32, and the result is rounded
- * once.  A NaN scale makes its terms NaN. */
+ * once.  A NaN scale makes its terms NaN.  With MXFP8 activations, MXFP4 weights
+ * and results in bf16 alone, sums of eight neighbouring products may lose what lies
+ * below 2^-13 of the largest of them. */
 fp4q_status fp4q_linear(const fp4q_weight *weight, const fp4q_linear_args *args, void *workspace,
                         size_t workspace_bytes, void *hip_stream);
 
@@ -459,7 +462,7 @@ typedef struct {
   const void *x, *residual;    /* [rows][stride] of dtype; residual may be NULL */
   int64_t x_stride, residual_stride;   /* elements, >= 0 */
   const void *weight;          /* [d] of weight_dtype */
-  void *y;                     /* [rows][d] of dtype, or NULL with codes */
+  void *y;                     /* [rows][d] of dtype (may be x or residual where those are dense), or NULL with codes */
   void *summed;                /* with residual: [rows][d] of dtype (may be x or residual where those are dense) */
   float *rstd;                 /* [rows] or NULL */
   uint8_t *codes, *scales;     /* MXFP8 output: [rows][d] E4M3, [rows][d / 32] E8M0; NULL with y */

@@ -401,3 +401,48 @@ def test_weights_of_the_quantizers(fq, policy):
     m = fq.quantize_mxfp4(w)
     want = fq.dequantize("mxfp4", m.codes, m.scales)
     assert torch.equal(fq.fp4_linear(eye, fq.fp4_weight(m)), want.t())
+
+
+def test_buffers_that_overlap(fq):
+    """A caller's buffer that lies in what the call reads is refused; the norm may write over whole dense rows."""
+    w = handle(fq, "mxfp4", weight(np.random.default_rng(3), "mxfp4", 64, 64))
+    space = torch.zeros(40, 64, dtype=torch.bfloat16, device="cuda")
+    x = space[:32]
+    for out in (x, space[8:]):
+        with pytest.raises(ValueError):
+            fq.fp4_linear(x, w, out=out)
+        with pytest.raises(ValueError):
+            fq.fp4_linear_backward(x, w, out=out)
+    with pytest.raises(ValueError):
+        fq.fp4_linear(x[:1], w, bias=space[33], out=space[33:34])
+    with pytest.raises(ValueError):
+        fq.fp4_gated(x, w, out=space.view(-1)[64:64 + 32 * 32].view(32, 32))
+    g = torch.ones(64, device="cuda")
+    with pytest.raises(ValueError):
+        fq.rms_norm(x, g, out=space[8:])
+    with pytest.raises(ValueError):
+        fq.rms_norm(x, g, residual=x.clone(), out=x, summed=x)
+    with pytest.raises(ValueError):
+        fq.rms_norm(x, g, residual=space[8:], summed=space[4:36])
+    with pytest.raises(ValueError):
+        fq.rms_norm(x, g, quantize="mxfp8", out=(x.view(torch.uint8).view(-1)[:2048].view(32, 64),
+                                                 torch.empty(32, 2, dtype=torch.uint8, device="cuda")))
+    a = torch.randn(300, 5000, device="cuda").bfloat16()
+    b, gain = torch.randn_like(a), torch.randn(5000, device="cuda")
+    want = fq.rms_norm(a, gain, residual=b)
+    a2, b2 = a.clone(), b.clone()
+    got = fq.rms_norm(a2, gain, residual=b2, out=a2, summed=b2)
+    torch.cuda.synchronize()
+    assert got.out.data_ptr() == a2.data_ptr() and torch.equal(a2, want.out) and torch.equal(b2, want.summed)
+
+
+@pytest.mark.parametrize("rows", [3, 70, 2090])
+def test_gradient_of_no_outputs(fq, rows):
+    """A weight without rows: zeros, by each kernel."""
+    for fmt, block in (("nvfp4", 16), ("mxfp4", 32)):
+        g = torch.ones(1, device="cuda") if fmt == "nvfp4" else None
+        none = fq.Fp4Weight(fmt, torch.zeros(0, 4128, dtype=torch.uint8, device="cuda"),
+                            torch.zeros(0, 8256 // block, dtype=torch.uint8, device="cuda"), g)
+        out = torch.full((rows, 8256), 5.0, dtype=torch.bfloat16, device="cuda")
+        fq.fp4_linear_backward(torch.zeros(rows, 0, dtype=torch.bfloat16, device="cuda"), none, out=out)
+        assert out.abs().max() == 0
