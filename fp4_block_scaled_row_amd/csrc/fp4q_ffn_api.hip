@@ -56,7 +56,8 @@ fp4q_status check_linear(const fp4q_weight* w, const fp4q_linear_args* a, int ki
     if (!a->x || !w->codes || !w->scales || (a->x_dtype == FP4Q_E4M3 && !a->x_scales)) return FP4Q_ERR_INVALID_ARG;
   }
   const size_t os = size_of(a->out_dtype);
-  if (!aligned(a->out, os) || !aligned(a->products, size_of(a->products_dtype)) || !aligned(a->bias, os) || !aligned(w->global_scale, 4))
+  if (!aligned(a->out, os) || !aligned(a->products, size_of(a->products_dtype)) || !aligned(a->bias, os) ||
+      !aligned(w->global_scale, 4))
     return FP4Q_ERR_UNSUPPORTED;
   if (a->x_dtype != FP4Q_E4M3 && !aligned(a->x, size_of(a->x_dtype))) return FP4Q_ERR_UNSUPPORTED;
   l->w.codes = w->codes;

@@ -40,7 +40,8 @@ Plan plan(const LinearLaunch& l) {
   //   8192, 8192  88 /  69    90 / 106     92 / 163    114 / 253
   //   4096, 4096  45 /  34    45 /  43     51 /  58     53 /  87
   //   8192, 1024  79 /  29    79 /  33     90 /  43     91 /  69
-  p.mx8 = l.x_type == kXE4M3 && l.w.format == 0 && l.out_bf16 && (!l.products || l.products_bf16) && l.w.k > 0 && l.w.k % 128 == 0 && l.w.k <= 1 << 22 &&
+  p.mx8 = l.x_type == kXE4M3 && l.w.format == 0 && l.out_bf16 && (!l.products || l.products_bf16) && l.w.k > 0 &&
+          l.w.k % 128 == 0 && l.w.k <= 1 << 22 &&
           many_args(l, -1).ntiles >= cus / 4;
   if (p.mx8) return p;
   // Large tiles from one a CU on; whole stages also in parts of 32 stages or more

@@ -52,7 +52,8 @@ __global__ __launch_bounds__(64 * kWaves8) void mx8_kernel(ManyArgs a) {
   __shared__ __align__(16) uint8_t s_b1[kBuf8];
   __shared__ __align__(16) uint8_t s_b2[kBuf8];
   const LinearLaunch& l = a.l;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // (one a wave: descriptors go by it)
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // (the same in all lanes: descriptors go by it)
   const int wx = wave >> 1, ww = wave & 1;          // this wave's quarter of x's rows, half of the weight's
 
   const int w = blockIdx.x, per = (a.ntiles + 7) / 8;

@@ -205,3 +205,37 @@ def test_few_rows_wide(fq, fmt, kind, rows, n, k):
 @pytest.mark.parametrize("rows,f,k", [(24, 8200, 160), (40, 8201, 288), (24, 10001, 416), (48, 10007, 160)])
 def test_few_rows_wide_gated(fq, fmt, rows, f, k):
     check_gated(fq, fmt, "bf16", rows, f, k, rows + f)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_parts_captured_and_on_two_streams(fq, fmt):
+    """Calls whose parts lie in memory of the call's own: replayed beside eager ones, and two at once."""
+    rng = np.random.default_rng(13)
+    n, k = 8200, 4160
+    w = handle(fq, fmt, weight(rng, fmt, n, k))
+    back = handle(fq, fmt, weight(rng, fmt, k, 8256))
+    xs = [activations(rng, fq, "bf16", 600, k)[0] for _ in range(4)]
+    want = [(fq.fp4_linear(x, w), fq.fp4_linear_backward(x, back)) for x in xs]
+    x = xs[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dx = fq.fp4_linear(x, w), fq.fp4_linear_backward(x, back)
+    for i in (1, 2, 3, 0):
+        x.copy_(xs[i])
+        graph.replay()
+        assert torch.equal(fq.fp4_linear(xs[i - 1], w), want[i - 1][0])      # (eager, while the graph's results wait)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i][0]) and torch.equal(dx, want[i][1])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for i in range(4):
+        for j, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                a = xs[(i + j) % 4]
+                got[j].append((fq.fp4_linear(a, w), fq.fp4_linear_backward(a, back)))
+    torch.cuda.synchronize()
+    for j in range(2):
+        for i in range(4):
+            y, dx = got[j][i]
+            assert torch.equal(y, want[(i + j) % 4][0]) and torch.equal(dx, want[(i + j) % 4][1])
