@@ -29,20 +29,23 @@ ManyArgs many_args(const LinearLaunch& l, int size) {
   return a;
 }
 
+bool multiple(const void* p, uintptr_t of) { return reinterpret_cast<uintptr_t>(p) % of == 0; }
+
 Plan plan(const LinearLaunch& l) {
   Plan p = {!l.transposed && l.rows <= (l.x_type == kXF32 ? 16 : 64), false, 1, 1};
   if (p.few) return p;
   const int cus = device_cu_count();
   // Block-scaled products for bf16 results (the instruction drops more bits than an
   // fp32 result should lose), from a quarter as many tiles as CUs on (its offsets
-  // within 256 rows are 31-bit).  Measured, MXFP4, us, there / converted to bf16:
+  // within 256 rows are 31-bit; its loads into LDS and of scales are aligned ones).
+  // Measured, MXFP4, us, there / converted to bf16:
   //   k, n        rows 256       512          1024         2048
   //   8192, 8192  88 /  69    90 / 106     92 / 163    114 / 253
   //   4096, 4096  45 /  34    45 /  43     51 /  58     53 /  87
   //   8192, 1024  79 /  29    79 /  33     90 /  43     91 /  69
   p.mx8 = l.x_type == kXE4M3 && l.w.format == 0 && l.out_bf16 && (!l.products || l.products_bf16) && l.w.k > 0 &&
-          l.w.k % 128 == 0 && l.w.k <= 1 << 22 &&
-          many_args(l, -1).ntiles >= cus / 4;
+          l.w.k % 128 == 0 && l.w.k <= 1 << 22 && multiple(l.x, 16) && multiple(l.w.codes, 16) &&
+          multiple(l.x_scales, 4) && multiple(l.w.scales, 4) && many_args(l, -1).ntiles >= cus / 4;
   if (p.mx8) return p;
   // Large tiles from one a CU on; whole stages also in parts of 32 stages or more
   // that give each CU one, forward of 128 stages or more in all.  Measured, bf16,

@@ -417,8 +417,9 @@ typedef struct {
 
 enum { FP4Q_LINEAR = 0, FP4Q_GATED = 1, FP4Q_LINEAR_BACKWARD = 2 };
 
-/* Bytes of device workspace that a call of this kind uses (0 for arguments it
- * would refuse; most calls use none), 16-byte aligned.  Its contents before and
+/* Bytes of device workspace that a call of this kind with these arguments,
+ * addresses among them, uses (0 for arguments it would refuse; most calls use
+ * none), 16-byte aligned.  Its contents before and
  * after a call mean nothing; calls that overlap on the GPU need one each. */
 size_t fp4q_linear_workspace_bytes(const fp4q_weight *weight, const fp4q_linear_args *args, int32_t kind);
 

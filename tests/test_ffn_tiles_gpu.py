@@ -239,3 +239,35 @@ def test_parts_captured_and_on_two_streams(fq, fmt):
         for i in range(4):
             y, dx = got[j][i]
             assert torch.equal(y, want[(i + j) % 4][0]) and torch.equal(dx, want[(i + j) % 4][1])
+
+
+@pytest.mark.parametrize("which,offset", [("codes", 1), ("codes", 8), ("scales", 1), ("scales", 2), ("x", 4), ("x", 3),
+                                          ("x_scales", 1), ("none", 0)])
+def test_planes_between_words(fq, which, offset):
+    """Planes of many rows that begin anywhere."""
+    rng = np.random.default_rng(14)
+    rows, n, k = 2049, 2050, 256
+    planes = weight(rng, "mxfp4", n, k)
+    x, xv, _ = activations(rng, fq, "mxfp8", rows, k)
+
+    def at(t, name):
+        space = torch.empty(t.numel() + 64, dtype=torch.uint8, device="cuda")
+        o = offset if name == which else 0
+        space[o:o + t.numel()] = t.reshape(-1)
+        return space[o:o + t.numel()].view(t.shape)
+
+    w = fq.Fp4Weight("mxfp4", at(torch.from_numpy(planes[0]).cuda(), "codes"),
+                     at(torch.from_numpy(planes[1]).cuda(), "scales"))
+    y = fq.fp4_linear(fq.Mx8Result(at(x.codes, "x"), at(x.scales, "x_scales")), w)
+    dy = rng.standard_normal((rows, n))
+    dt = torch.from_numpy(dy).bfloat16()
+    dx = fq.fp4_linear_backward(dt.cuda(), w)
+    z = fq.fp4_linear(torch.from_numpy(xv).bfloat16().cuda(), w)             # (MXFP8 values are exact in bf16)
+    torch.cuda.synchronize()
+    v = values("mxfp4", planes)
+    want, S = xv @ v.T, np.abs(xv) @ np.abs(v).T
+    check(y, want, block_scaled_bound(S, k) + 2.0 ** -8 * np.abs(want), "mxfp8")
+    check(z, want, sum_bound(S, k, 1) + 2.0 ** -8 * np.abs(want), "bf16")
+    d = dt.double().numpy()
+    want, S = d @ v, np.abs(d) @ np.abs(v)
+    check(dx, want, sum_bound(S, n, 1) + 2.0 ** -8 * np.abs(want), "gradient")
