@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "fp4q_ffn.h"
+#include "fp4q_ffn_sizes.h"
 
 namespace fp4q {
 
@@ -400,6 +401,7 @@ __device__ __forceinline__ void wait_loads() {
 template <int FMT, int MODE, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void ring_kernel(ManyArgs a) {
   constexpr int BM = 128, BN = 256;
+  static_assert(BN / 2 == kRingFactorRows, "what ring_scales_fit counts");
   using T = ManyTile<FMT, kXBF16, MODE, BM, BN, 1, 4>;
   constexpr int XL = 16 / NW, WL = 8 / NW;                      // a wave's loads of a stage
   // separate objects, so that reads of one are not ordered after loads into others
@@ -581,7 +583,7 @@ __global__ __launch_bounds__(64 * NW, 2) void ring_kernel(ManyArgs a) {
 // the call.)
 inline bool ring_sizes(const LinearLaunch& l) {
   return l.x_type == kXBF16 && l.w.k > 0 && l.w.k % kStage == 0 && l.w.n % (l.transposed ? kStage : 1) == 0 &&
-         l.w.k <= 1 << 22 && (!l.gated || l.w.n / 2 * (l.w.k / 16) < (int64_t)1 << 31);
+         l.w.k <= 1 << 22 && ring_scales_fit(l.gated, l.w.n, l.w.k);
 }
 inline bool ring_fits(const LinearLaunch& l) {
   return ring_sizes(l) && l.x_stride % 8 == 0 && l.x_stride <= 1 << 22 && reinterpret_cast<uintptr_t>(l.x) % 16 == 0 &&

@@ -1,0 +1,61 @@
+"""The bounds of the linear layers' 32-bit arithmetic (csrc/fp4q_ffn_sizes.h), compiled by themselves and held against
+the arithmetic of the kernels that rely on them, written again here."""
+import ctypes as C
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from fp4_block_scaled_row_amd import build
+
+SOURCE = r"""
+#include "fp4q_ffn_sizes.h"
+extern "C" int scales_fit(int gated, int64_t n, int64_t k) { return fp4q::ring_scales_fit(gated, n, k); }
+"""
+
+
+@pytest.fixture(scope="module")
+def sizes(tmp_path_factory):
+    at = tmp_path_factory.mktemp("sizes")
+    (at / "sizes.cpp").write_text(SOURCE)
+    cxx = shutil.which("g++") or build.hipcc()
+    r = subprocess.run([cxx, "-std=c++17", "-shared", "-fPIC", "-I" + build.CSRC, str(at / "sizes.cpp"), "-o",
+                        str(at / "sizes.so")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    lib = C.CDLL(str(at / "sizes.so"))
+    lib.scales_fit.argtypes = [C.c_int, C.c_int64, C.c_int64]
+    return lib
+
+
+def largest_scale_offset(n, k, block):
+    """The last byte that a thread of the gated ring kernel asks for, from the tile's first scale of the first factor:
+    local row 255 of the tile is row 127 of its factor, and a thread has 4 bytes at most."""
+    half, srow = n // 2, k // block
+    w_row = min(127, half - 1)
+    return (half + w_row) * srow + srow - 1
+
+
+@pytest.mark.parametrize("k", [64, 128, 4096, 16384, 1 << 20, 1 << 22])
+def test_gated_scale_offsets_stay_in_32_bits(sizes, k):
+    """At and around the largest weight that is taken; sizes well inside it are."""
+    edge = (1 << 31) // (k // 16)                  # half the rows at which the second factor's first scale is past 2^31
+    for half in {edge + d for d in range(-300, 300)} | {edge // 2, 1, 127, 128}:
+        if half < 1 or 2 * half >= 1 << 31:
+            continue
+        if sizes.scales_fit(1, 2 * half, k):
+            for block in (16, 32):
+                assert largest_scale_offset(2 * half, k, block) < 1 << 31, (half, k, block)
+        if half <= edge - 129:
+            assert sizes.scales_fit(1, 2 * half, k)
+
+
+@pytest.mark.parametrize("n,k", [(16777214, 4096), (2 * 2097151, 16384)])
+def test_gated_weights_just_below_2_31_scales_go_another_way(sizes, n, k):
+    """Second factors that begin below 2^31 and end past it."""
+    assert n // 2 * (k // 16) < 1 << 31 <= largest_scale_offset(n, k, 16)
+    assert not sizes.scales_fit(1, n, k)
+
+
+def test_other_directions_have_no_second_factor(sizes):
+    assert sizes.scales_fit(0, (1 << 31) - 1, 1 << 22)
