@@ -20,6 +20,7 @@
 // activation are applied in fp32, and outputs rounded once.
 #pragma once
 
+#include "fp4q_ffn_sizes.h"
 #include "fp4q_flat.h"
 
 namespace fp4q {
@@ -55,6 +56,8 @@ struct LinearLaunch {
   float* partials;             // parts of sums that several workgroups share (workspace)
 };
 
+// Whether one launch takes the call's tiles.
+bool linear_fits(const LinearLaunch& l);
 size_t linear_workspace(const LinearLaunch& l);
 hipError_t launch_linear(const LinearLaunch& l, hipStream_t s);
 hipError_t launch_linear_few(const LinearLaunch& l, hipStream_t s);
@@ -100,6 +103,9 @@ struct Dequant8Launch {
   void* out;
 };
 hipError_t launch_dequant8(const Dequant8Launch& l, hipStream_t s);
+
+// This workgroup's number in a grid of grid_x and grid_y.
+__device__ __forceinline__ int64_t group_number() { return (int64_t)blockIdx.y * kGridRow + blockIdx.x; }
 
 // ----------------------------------------------------------------------------
 // Loads of any alignment: rows need not begin on a vector's boundary.

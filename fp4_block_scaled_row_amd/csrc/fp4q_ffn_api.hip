@@ -49,7 +49,7 @@ fp4q_status check_linear(const fp4q_weight* w, const fp4q_linear_args* a, int ki
   l->out_bf16 = a->out_dtype == FP4Q_BF16;
   l->products_bf16 = a->products_dtype == FP4Q_BF16;
   if (a->rows == 0 || out == 0) return FP4Q_OK;
-  // (workgroups of the smallest tiles are counted in 31 bits)
+  // (tiles, the smallest too, are counted in 31 bits)
   if ((a->rows + 63) / 64 * ((out + 63) / 64) > INT_MAX / 8) return FP4Q_ERR_UNSUPPORTED;
   if (!a->out || (w->format == FP4Q_NVFP4 && !w->global_scale)) return FP4Q_ERR_INVALID_ARG;
   if (len > 0) {
@@ -69,7 +69,7 @@ fp4q_status check_linear(const fp4q_weight* w, const fp4q_linear_args* a, int ki
   l->bias = a->bias;
   l->out = a->out;
   l->products = a->products;
-  return FP4Q_OK;
+  return linear_fits(*l) ? FP4Q_OK : FP4Q_ERR_UNSUPPORTED;
 }
 
 bool nothing(const LinearLaunch& l) { return l.out == nullptr; }

@@ -15,4 +15,15 @@ inline bool ring_scales_fit(bool gated, int64_t n, int64_t k) {
   return !gated || (n / 2 + kRingFactorRows) * (k / 16) <= (int64_t)INT32_MAX;
 }
 
+// A launch takes fewer than 2^32 threads in a dimension of its grid, and workgroups
+// here have at most 1024.  More workgroups than kGridRow make rows of so many: number
+// y kGridRow + x; the last row's may be past the end.
+constexpr int64_t kGridRow = 1 << 21;
+inline unsigned grid_x(int64_t groups) { return (unsigned)(groups < kGridRow ? groups : kGridRow); }
+inline unsigned grid_y(int64_t groups) { return (unsigned)((groups + kGridRow - 1) / kGridRow); }
+
+// The kernels of many rows have a workgroup for each tile, of 512 threads at most, in
+// one dimension, their number rounded up to a multiple of 8.
+inline bool tiles_fit(int64_t tiles) { return (tiles + 7) / 8 * 8 * 512 < (int64_t)1 << 32; }
+
 }  // namespace fp4q

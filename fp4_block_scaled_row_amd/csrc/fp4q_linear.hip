@@ -129,7 +129,7 @@ template <bool BF16, bool PBF16>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradLaunch l) {
   constexpr int kElem = BF16 ? 2 : 4, kPElem = PBF16 ? 2 : 4;
   const int64_t per = (l.f + 7) / 8;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t at = group_number() * 256 + threadIdx.x;
   if (at >= l.rows * per) return;
   const int64_t row = at / per, col = (at - row * per) * 8;
   const uint8_t* dh = static_cast<const uint8_t*>(l.dh) + (row * l.dh_stride + col) * kElem;
@@ -198,6 +198,11 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradLaunch l) {
 
 }  // namespace
 
+bool linear_fits(const LinearLaunch& l) {
+  const Plan p = plan(l);
+  return p.few || tiles_fit(many_args(l, p.mx8 ? -1 : p.size).ntiles);
+}
+
 size_t linear_workspace(const LinearLaunch& l) {
   const Plan p = plan(l);
   if (p.splits <= 1) return 0;
@@ -222,8 +227,8 @@ hipError_t launch_linear(const LinearLaunch& l, hipStream_t s) {
 }
 
 hipError_t launch_gated_grad(const GatedGradLaunch& l, hipStream_t s) {
-  const int64_t threads = l.rows * ((l.f + 7) / 8);
-  const dim3 grid((unsigned)((threads + 255) / 256));
+  const int64_t groups = (l.rows * ((l.f + 7) / 8) + 255) / 256;
+  const dim3 grid(grid_x(groups), grid_y(groups));
   if (l.bf16 && l.products_bf16) hipLaunchKernelGGL((gated_grad_kernel<true, true>), grid, dim3(256), 0, s, l);
   else if (l.bf16) hipLaunchKernelGGL((gated_grad_kernel<true, false>), grid, dim3(256), 0, s, l);
   else if (l.products_bf16) hipLaunchKernelGGL((gated_grad_kernel<false, true>), grid, dim3(256), 0, s, l);

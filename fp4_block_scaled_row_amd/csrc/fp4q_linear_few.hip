@@ -140,7 +140,8 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, g = lane >> 4;
   const int64_t K = l.w.k, half = l.w.n / kHalves;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * kSide);
+  const int64_t n0 = group_number() * (16 * kSide);
+  if (n0 >= half) return;                        // (whole workgroups, behind the last)
   const int64_t srow = K / (FMT == 0 ? 32 : 16);
   const int rows = (int)l.rows;
 
@@ -385,7 +386,8 @@ hipError_t launch_t(const LinearLaunch& l, int log_kp, hipStream_t s) {
   const size_t lds = x + (size_t)kFewWaves * (kScratch<CH> + (WHOLE ? 0 : P * 16 * MT * (2 * CH + 16)));
   const size_t sums = (size_t)kFewWaves * NT * MT * 1024;
   const FewArgs a = {l, log_kp, (int)x};
-  hipLaunchKernelGGL((few_kernel<FMT, XT, MT, NT, CH, D, GATED, WHOLE>), dim3((unsigned)((n + per - 1) / per)),
+  const int64_t groups = (n + per - 1) / per;
+  hipLaunchKernelGGL((few_kernel<FMT, XT, MT, NT, CH, D, GATED, WHOLE>), dim3(grid_x(groups), grid_y(groups)),
                      dim3(kFewThreads), lds > sums ? lds : sums, s, a);
   return hipGetLastError();
 }

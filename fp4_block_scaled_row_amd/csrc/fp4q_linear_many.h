@@ -27,7 +27,6 @@
 #include <type_traits>
 
 #include "fp4q_ffn.h"
-#include "fp4q_ffn_sizes.h"
 
 namespace fp4q {
 

@@ -137,7 +137,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_kernel(NormLaunch l) {
   constexpr int kRows = T < 256 ? 256 / T : 1;
   __shared__ float s_sum[T / 64];
   const int t = threadIdx.x % T;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
+  const int64_t row = group_number() * kRows + threadIdx.x / T;
   if (row >= l.rows) return;                  // (whole waves; several rows a workgroup have no barrier)
   float v[NS][8];
   const void* x = at_row<BF16>(l.x, row, l.x_stride);
@@ -297,7 +297,8 @@ hipError_t launch_norm_t(const NormLaunch& l, hipStream_t s) {
 #define FP4Q_NORM(T, NS)                                                                                   \
   do {                                                                                                     \
     const int per = T < 256 ? 256 / T : 1;                                                                 \
-    hipLaunchKernelGGL((norm_kernel<BF16, WBF16, QUANT, T, NS>), dim3((unsigned)((l.rows + per - 1) / per)), \
+    const int64_t groups = (l.rows + per - 1) / per;                                                       \
+    hipLaunchKernelGGL((norm_kernel<BF16, WBF16, QUANT, T, NS>), dim3(grid_x(groups), grid_y(groups)),     \
                        dim3(T < 256 ? 256 : T), 0, s, l);                                                  \
     return hipGetLastError();                                                                              \
   } while (0)

@@ -392,8 +392,9 @@ fp4q_status fp4q_kv_attention(const fp4q_kv_cache *cache, const fp4q_kv_attentio
  *
  * A weight [n][k] is the planes that fp4q_quantize_mxfp4 or
  * fp4q_quantize_nvfp4 (policies NV_MAX6 and FOUR_OVER_SIX) writes for it: codes
- * [n][k / 2], scales [n][k / block].  n and k: to 2^31 - 1; k a multiple of the
- * block.  Any n, any alignment.  FP4Q_IF4 is UNSUPPORTED.  What a call of this
+ * [n][k / 2], scales [n][k / block].  n, k and rows: to 2^31 - 1; k a multiple of the
+ * block.  Any n, any alignment.  FP4Q_IF4 is UNSUPPORTED, and so are more
+ * than 2^23 - 8 tiles of results (64 to 256 rows by 128 to 256 columns) at once.  What a call of this
  * group writes overlaps nothing that it reads, except where it is said. */
 typedef struct {
   int32_t format;              /* FP4Q_MXFP4 or FP4Q_NVFP4 */
