@@ -44,7 +44,18 @@ __all__ = [
 ]
 
 MxResult = namedtuple("MxResult", "codes scales rotated counters")
-NvResult = namedtuple("NvResult", "codes scales global_scale choice_bits rotated counters")
+
+
+class NvResult(namedtuple("NvResult", "codes scales global_scale choice_bits rotated counters")):
+    """`policy`, beside the fields: the one that wrote the planes last (None for a
+    tuple that a caller made)."""
+    policy = None
+
+    def _replace(self, **fields):
+        other = super()._replace(**fields)
+        other.policy = self.policy
+        return other
+
 
 _ROUND = {"rne": _lib.FP4Q_ROUND_RNE, "stochastic": _lib.FP4Q_ROUND_STOCHASTIC, "sr": _lib.FP4Q_ROUND_STOCHASTIC}
 _ROT = {None: _lib.FP4Q_ROT_NONE, "none": _lib.FP4Q_ROT_NONE, "fwht_row": _lib.FP4Q_ROT_FWHT_ROW,
@@ -208,6 +219,8 @@ def quantize_nvfp4(x, *, policy="max6", rounding="rne", seed=0, rotation=None, g
                      _ptr(out.rotated), _ptr(out.counters))
     _lib.check(_lib.load().fp4q_quantize_nvfp4(a, _ptr(x), _ptr(global_amax), o, _ptr(workspace), ws_bytes,
                                                _stream()), "fp4q_quantize_nvfp4")
+    if isinstance(out, NvResult):
+        out.policy = policy
     return out
 
 

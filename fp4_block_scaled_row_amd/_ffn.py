@@ -66,8 +66,10 @@ class Fp4Weight:
 
 
 def fp4_weight(quantized):
-    """The Fp4Weight of a quantize_mxfp4 or quantize_nvfp4 result (not of policy
-    "if4", whose blocks of integers the products do not take)."""
+    """The Fp4Weight of a quantize_mxfp4 or quantize_nvfp4 result.  One of policy
+    "if4" is refused: the products do not take its blocks of integers."""
+    if getattr(quantized, "policy", None) == "if4":
+        raise ValueError("fp4q: a weight is in NVFP4 or MXFP4; IF4 blocks of integers are not")
     g = getattr(quantized, "global_scale", None)
     return Fp4Weight("mxfp4" if g is None else "nvfp4", quantized.codes, quantized.scales, g)
 
