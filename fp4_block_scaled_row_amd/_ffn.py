@@ -98,13 +98,15 @@ def _out_dtype(dtype):
     return code
 
 
-def _buffer(t, what, shape, dtype, device):
-    """A dense buffer of this shape and dtype: t after checks, or a new one."""
+def _buffer(t, what, shape, dtype, device, *others):
+    """A dense buffer of this shape and dtype: t after checks, apart from the others, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device \
             or not t.is_contiguous():
         raise ValueError("fp4q: %s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, shape, device))
+    if others:
+        _apart(t, what, *others)
     return t
 
 
@@ -169,9 +171,8 @@ def fp4_linear(x, w, *, bias=None, out_dtype=None, out=None):
     code = _out_dtype(dtype)
     if bias is not None:
         _buffer(bias, "bias", (w.n,), dtype, w.device)
-    if out is not None:
-        _apart(out, "out", *(x if isinstance(x, Mx8Result) else (x,)), bias, w.codes, w.scales, w.global_scale)
-    out = _buffer(out, "out", (fields[2], w.n), dtype, w.device)
+    out = _buffer(out, "out", (fields[2], w.n), dtype, w.device, *(x if isinstance(x, Mx8Result) else (x,)), bias,
+                  w.codes, w.scales, w.global_scale)
     a = _lib.LinearArgs(*fields, code, None if bias is None else bias.data_ptr(), out.data_ptr(), None, code)
     _linear(w, a, _lib.FP4Q_LINEAR, _lib.load().fp4q_linear, "fp4q_linear")
     return out
@@ -183,9 +184,7 @@ def fp4_linear_backward(dy, w, *, out=None):
     gradient of a bias is dy.sum(0).)"""
     _weight(w)
     rows, stride, code = _rows(dy, "dy", w._index, w.n)
-    if out is not None:
-        _apart(out, "out", dy, w.codes, w.scales, w.global_scale)
-    out = _buffer(out, "out", (rows, w.k), dy.dtype, w.device)
+    out = _buffer(out, "out", (rows, w.k), dy.dtype, w.device, dy, w.codes, w.scales, w.global_scale)
     a = _lib.LinearArgs(dy.data_ptr(), None, rows, stride, code, code, None, out.data_ptr(), None, code)
     _linear(w, a, _lib.FP4Q_LINEAR_BACKWARD, _lib.load().fp4q_linear_backward, "fp4q_linear_backward")
     return out
@@ -204,9 +203,8 @@ def fp4_gated(x, w, *, return_products=False, products_dtype=torch.float32, out_
         raise ValueError("fp4q: a gated weight has an even number of rows, got %d" % w.n)
     _, fields, dtype = _activations(x, w, out_dtype)
     code = _out_dtype(dtype)
-    if out is not None:
-        _apart(out, "out", *(x if isinstance(x, Mx8Result) else (x,)), w.codes, w.scales, w.global_scale)
-    out = _buffer(out, "out", (fields[2], w.n // 2), dtype, w.device)
+    out = _buffer(out, "out", (fields[2], w.n // 2), dtype, w.device, *(x if isinstance(x, Mx8Result) else (x,)),
+                  w.codes, w.scales, w.global_scale)
     products = None
     if return_products:
         products = torch.empty((fields[2], w.n), dtype=products_dtype, device=w.device)
@@ -278,6 +276,8 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, quantize=None, return_rstd=F
     elif quantize == "mxfp8":
         if d % 32:
             raise ValueError("fp4q: MXFP8 rows are multiples of 32, got %d" % d)
+        if out is not None and (not isinstance(out, tuple) or len(out) != 2):
+            raise ValueError("fp4q: out of an MXFP8 norm is an Mx8Result")
         c, s = (None, None) if out is None else out
         out = Mx8Result(_buffer(c, "out.codes", (rows, d), torch.uint8, device),
                         _buffer(s, "out.scales", (rows, d // 32), torch.uint8, device))
