@@ -16,8 +16,10 @@
 // conversions give NaN for scale byte 255, the E4M3 one for 0x7F).  bf16
 // activations are exact too.  An fp32 one is the sum of three bf16 pieces of 8
 // bits each, cut off rather than rounded, so that the sum is exact and no piece
-// passes the type's range.  Sums are fp32; the tensor scale, bias and
-// activation are applied in fp32, and outputs rounded once.
+// passes the type's range.  The tensor scale's power of two goes into the weights,
+// exactly, so that sums are of the results' size; what is left of it, in [1, 2),
+// multiplies the sums.  Those are fp32; bias and activation are applied in fp32, and
+// outputs rounded once.
 #pragma once
 
 #include "fp4q_ffn_sizes.h"
@@ -139,9 +141,25 @@ __device__ __forceinline__ float scale_operand(uint32_t byte) {
   else return e4m3_value_hw(byte & 0x7Fu);
 }
 
-// Eight codes of one block as bf16 pairs.
+// The tensor scale in two factors: a power of two that the conversions below
+// multiply into the elements, held to 2^-116 .. 2^115, with which the least of them
+// (2^-10) is normal in bf16 and the largest (2688) finite; and the rest, which is
+// exact.  A scalar load: it is one of none that the vector loads' counts mean.
+__device__ __forceinline__ float tensor_scale(const float* g) {
+  typedef const __attribute__((address_space(4))) float* constant_t;
+  return *(constant_t)reinterpret_cast<uintptr_t>(g);
+}
+__device__ __forceinline__ float tensor_power(float g) {
+  const uint32_t e = (as_u(g) >> 23) & 0xFFu;
+  return as_f(min(max(e, 11u), 242u) << 23);
+}
+__device__ __forceinline__ float tensor_rest(float g) {
+  return g * as_f((254u << 23) - as_u(tensor_power(g)));
+}
+
+// Eight codes of one block as bf16 pairs.  power: NVFP4, tensor_power.
 template <int FMT>
-__device__ __forceinline__ u32x4_t weights8(uint32_t codes, float s) {
+__device__ __forceinline__ u32x4_t weights8(uint32_t codes, float s, float power) {
   u32x4_t o;
   if constexpr (FMT == 0) {
     o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0));
@@ -149,11 +167,10 @@ __device__ __forceinline__ u32x4_t weights8(uint32_t codes, float s) {
     o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2));
     o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3));
   } else {
-    const float one = e8m0_operand(127u);
-    const float2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, one, 0);
-    const float2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, one, 1);
-    const float2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, one, 2);
-    const float2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, one, 3);
+    const float2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, power, 0);
+    const float2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, power, 1);
+    const float2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, power, 2);
+    const float2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, power, 3);
     o.x = high_halves(as_u(a.x * s), as_u(a.y * s));
     o.y = high_halves(as_u(b.x * s), as_u(b.y * s));
     o.z = high_halves(as_u(c.x * s), as_u(c.y * s));
@@ -165,7 +182,7 @@ __device__ __forceinline__ u32x4_t weights8(uint32_t codes, float s) {
 // N codes (2 or 4) of one row and N of the next, each row with its own scale: pair
 // j is column j's two values.
 template <int FMT, int N>
-__device__ __forceinline__ void weight_pairs(uint32_t ca, float sa, uint32_t cb, float sb, uint32_t (&o)[N]) {
+__device__ __forceinline__ void weight_pairs(uint32_t ca, float sa, uint32_t cb, float sb, float power, uint32_t (&o)[N]) {
   if constexpr (FMT == 0) {
     const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ca, sa, 0));
     const uint32_t b0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cb, sb, 0));
@@ -178,14 +195,13 @@ __device__ __forceinline__ void weight_pairs(uint32_t ca, float sa, uint32_t cb,
       o[3] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
     }
   } else {
-    const float one = e8m0_operand(127u);
-    const float2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ca, one, 0);
-    const float2_t b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cb, one, 0);
+    const float2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ca, power, 0);
+    const float2_t b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cb, power, 0);
     o[0] = high_halves(as_u(a0.x * sa), as_u(b0.x * sb));
     o[1] = high_halves(as_u(a0.y * sa), as_u(b0.y * sb));
     if constexpr (N == 4) {
-      const float2_t a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ca, one, 1);
-      const float2_t b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cb, one, 1);
+      const float2_t a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ca, power, 1);
+      const float2_t b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cb, power, 1);
       o[2] = high_halves(as_u(a1.x * sa), as_u(b1.x * sb));
       o[3] = high_halves(as_u(a1.y * sa), as_u(b1.y * sb));
     }

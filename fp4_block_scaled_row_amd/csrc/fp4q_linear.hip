@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void join_kernel(LinearLaunch l, int splits) {
   if (at >= l.rows * per) return;
   const int64_t row = at / per, col = (at - row * per) * 4;
   const int count = (int)min(out - col, (int64_t)4);
-  const float tensor = l.w.format == 1 ? *l.w.g : 1.0f;
+  const float tensor = l.w.format == 1 ? tensor_rest(tensor_scale(l.w.g)) : 1.0f;
   auto sum = [&](int64_t c, float (&v)[4]) {
     const float* p = l.partials + row * cols + c;
     for (int i = 0; i < 4; ++i) v[i] = 0.0f;

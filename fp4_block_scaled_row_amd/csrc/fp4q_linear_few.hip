@@ -144,6 +144,7 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
   if (n0 >= half) return;                        // (whole workgroups, behind the last)
   const int64_t srow = K / (FMT == 0 ? 32 : 16);
   const int rows = (int)l.rows;
+  const float gs = FMT == 1 ? tensor_scale(l.w.g) : 1.0f, power = tensor_power(gs);
 
   // ---- x in LDS: rows of `pitch` bytes (16 rows' pieces meet all banks), planes
   constexpr int kChunkPitch = 2 * CH + 16;
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const uint32_t s = FMT == 0 ? sv[t][i] : sv[t][i] >> (8 * (j >> 1));   // (of NV's two the first for 0 and 1)
-          const u32x4_t wf = weights8<FMT>(wv[t][i][j], scale_operand<FMT>(s & 0xFFu));
+          const u32x4_t wf = weights8<FMT>(wv[t][i][j], scale_operand<FMT>(s & 0xFFu), power);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -334,7 +335,7 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
     for (int m = 0; m < MT; ++m) s_sum[sum_at(wave, t, m, g, r)] = acc[t][m];
   __syncthreads();
 
-  const float tensor = FMT == 1 ? *l.w.g : 1.0f;
+  const float tensor = tensor_rest(gs);
   auto sum = [&](int t, int m, int q) {
     f32x4_t v = s_sum[sum_at(0, t, m >> 4, q, m & 15)];
 #pragma unroll

@@ -73,7 +73,7 @@ __device__ __forceinline__ int x_chunk(int row, int chunk) { return chunk ^ ((ro
 // (half: of its first or second 32 of the contraction alone, or both, -1.)
 template <class T, int FMT>
 __device__ __forceinline__ void many_multiply(const uint8_t* buf, f32x4_t (&acc)[T::FN][T::FM], int wm, int wn, int r,
-                                              int g, int half = -1) {
+                                              int g, float power, int half = -1) {
   constexpr int P = T::P, FM = T::FM, FN = T::FN, BM = T::TM * T::kWavesM;
   const uint8_t* bw = buf + T::kXBytes;
   const uint8_t* bs = bw + T::kWBytes;
@@ -102,7 +102,7 @@ __device__ __forceinline__ void many_multiply(const uint8_t* buf, f32x4_t (&acc)
         const float sa = scale_operand<FMT>((sw >> (8 * (i & 3))) & 0xFFu);
         const float sc = scale_operand<FMT>((sw >> (8 * (i & 3) + 8)) & 0xFFu);
         uint32_t o[FN];
-        weight_pairs<FMT, FN>(ca, sa, cb, sc, o);
+        weight_pairs<FMT, FN>(ca, sa, cb, sc, power, o);
 #pragma unroll
         for (int j = 0; j < FN; ++j) wf[j][i >> 1] = o[j];
       }
@@ -112,7 +112,7 @@ __device__ __forceinline__ void many_multiply(const uint8_t* buf, f32x4_t (&acc)
         const int row = wn * T::TN + 16 * n + r;
         const uint32_t c = *reinterpret_cast<const uint32_t*>(bw + row * T::kWPitch + 8 * g + 4 * t);
         const uint32_t s = bs[row * T::kSPitch + (FMT == 0 ? g >> 1 : g)];
-        wf[n] = weights8<FMT>(c, scale_operand<FMT>(s));
+        wf[n] = weights8<FMT>(c, scale_operand<FMT>(s), power);
       }
     }
     // this lane's 8 of the contraction: chunk 4 t + g where groups take runs of
@@ -157,7 +157,7 @@ __device__ __forceinline__ void many_results(const ManyArgs& a, const f32x4_t (&
       }
     }
   };
-  const float tensor = FMT == 1 ? *l.w.g : 1.0f;
+  const float tensor = FMT == 1 ? tensor_rest(tensor_scale(l.w.g)) : 1.0f;
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
     const int64_t row = m0 + wm * T::TM + 16 * m + r;
@@ -236,6 +236,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
   const int64_t K = l.w.k, srow = K / T::kBlock;
   const int64_t len = T::kT ? l.w.n : K;                // of the contraction
   const int s0 = blockIdx.y * a.per_split, s1 = min(a.stages, s0 + a.per_split);
+  const float power = FMT == 1 ? tensor_power(tensor_scale(l.w.g)) : 1.0f;
 
   // ---- loads of a stage: global memory to registers, registers to LDS
   uint32_t xr[T::kXPer][XT == kXF32 ? 8 : XT == kXBF16 ? 4 : 3];
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void many_kernel(ManyArgs a) {
         load_x((int64_t)(s + 1) * kStage);
         load_w((int64_t)(s + 1) * kStage);
       }
-      many_multiply<T, FMT>(s_buf[b], acc, wm, wn, r, g);
+      many_multiply<T, FMT>(s_buf[b], acc, wm, wn, r, g, power);
       if (s + 1 < s1) commit(s_buf[b ^ 1]);
       __syncthreads();
     }
@@ -421,6 +422,7 @@ __global__ __launch_bounds__(64 * NW, 2) void ring_kernel(ManyArgs a) {
   const int64_t o0 = (int64_t)(in_g / gsize) * (MODE == kGated ? BN / 2 : BN);
   const int64_t K = l.w.k, kb = K / 2, srow = K / T::kBlock;
   const int s0 = blockIdx.y * a.per_split, s1 = min(a.stages, s0 + a.per_split);
+  const float power = FMT == 1 ? tensor_power(tensor_scale(l.w.g)) : 1.0f;
 
   f32x4_t acc[T::FN][T::FM];
 #pragma unroll
@@ -517,11 +519,11 @@ __global__ __launch_bounds__(64 * NW, 2) void ring_kernel(ManyArgs a) {
     int rr = r, gg = g;
     asm volatile("" : "+v"(rr), "+v"(gg));
     if constexpr (NW == 8) {
-      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, part);
+      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, power, part);
     } else {
-      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, 0);
+      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, power, 0);
       __builtin_amdgcn_sched_barrier(0);            // (or both halves' operands would be held at once)
-      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, 1);
+      many_multiply<T, FMT>(cur, acc, 0, wn, rr, gg, power, 1);
     }
   };
   if (s0 < s1) {

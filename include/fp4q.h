@@ -426,8 +426,9 @@ size_t fp4q_linear_workspace_bytes(const fp4q_weight *weight, const fp4q_linear_
 
 /* out [rows][n] = x W^T + bias.  Weights and activations enter exactly, sums are
  * fp32 in an order that the shapes fix (a call gives the same bits each time),
- * the tensor scale and the bias are applied in fp32, and the result is rounded
- * once.  A NaN scale makes its terms NaN.  With MXFP8 activations, MXFP4 weights
+ * the tensor scale and the bias are applied in fp32 (the scale's power of two to the
+ * weights, exactly, so that sums pass fp32's range only where results do), and the
+ * result is rounded once.  A NaN scale makes its terms NaN.  With MXFP8 activations, MXFP4 weights
  * and results in bf16 alone, sums of eight neighbouring products may lose what lies
  * below 2^-13 of the largest of them. */
 fp4q_status fp4q_linear(const fp4q_weight *weight, const fp4q_linear_args *args, void *workspace,
