@@ -15,6 +15,9 @@ inline bool ring_scales_fit(bool gated, int64_t n, int64_t k) {
   return !gated || (n / 2 + kRingFactorRows) * (k / 16) <= (int64_t)INT32_MAX;
 }
 
+// The kernel of few rows has offsets of 32 bits into 8-bit rows, which are dense.
+inline bool few_eight_fits(int64_t rows, int64_t k) { return rows * k <= (int64_t)INT32_MAX; }
+
 // A launch takes fewer than 2^32 threads in a dimension of its grid, and workgroups
 // here have at most 1024.  More workgroups than kGridRow make rows of so many: number
 // y kGridRow + x; the last row's may be past the end.

@@ -32,7 +32,8 @@ ManyArgs many_args(const LinearLaunch& l, int size) {
 bool multiple(const void* p, uintptr_t of) { return reinterpret_cast<uintptr_t>(p) % of == 0; }
 
 Plan plan(const LinearLaunch& l) {
-  Plan p = {!l.transposed && l.rows <= (l.x_type == kXF32 ? 16 : 64), false, 1, 1};
+  Plan p = {!l.transposed && l.rows <= (l.x_type == kXF32 ? 16 : 64) && (l.x_type != kXE4M3 || few_eight_fits(l.rows, l.w.k)),
+            false, 1, 1};
   if (p.few) return p;
   const int cus = device_cu_count();
   // Block-scaled products for bf16 results (the instruction drops more bits than an

@@ -157,41 +157,68 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
   constexpr int kLoads = CH / 128, kLanes = CH / 32, kLane = Ring::kRowScales / 4;   // (scale bytes a lane)
   uint8_t* scratch = s_x + a.scratch + wave * (kScratch<CH> + P * XR * kChunkPitch);
   const int piece_at = lane % kLanes;
-  const uint8_t *wc[NT][kLoads], *ws[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    auto row = [&](int i) { return min(n0 + 16 * (t % kSide) + i, half - 1) + (t / kSide) * half; };
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      wc[t][i] = l.w.codes + row(lane / kLanes + i * (64 / kLanes)) * (K / 2) + 16 * piece_at;
-    ws[t] = l.w.scales + row(lane >> 2) * srow + (lane & 3) * kLane;
-  }
+  // Addresses, by the lane: a row's number times its bytes, in 64 bits (both factors have
+  // 32).  Where the sums take most registers, the lane is hidden from the compiler, so that
+  // addresses are made anew for each chunk (kept, they took up to 60 registers more than
+  // there are; 40 rows of k 4096 by two factors of 10000, MXFP4: 20.8 us, so 18.3).
+  constexpr bool kTight = NT * MT >= 12;
+  auto this_lane = [&] {
+    int ln = lane;
+    if constexpr (kTight) asm volatile("" : "+v"(ln));
+    return ln;
+  };
+  auto w_row = [&](int t, int i) {
+    return min((uint32_t)n0 + 16u * (t % kSide) + (uint32_t)i, (uint32_t)half - 1u) + (t / kSide) * (uint32_t)half;
+  };
+  auto codes_at = [&](int ln, int t, int i) {
+    return l.w.codes + (uint64_t)w_row(t, ln / kLanes + i * (64 / kLanes)) * (uint32_t)(K / 2) + 16 * (ln % kLanes);
+  };
+  auto scales_at = [&](int ln, int t) {
+    return l.w.scales + (uint64_t)w_row(t, ln >> 2) * (uint32_t)srow + (ln & 3) * kLane;
+  };
   // this lane's piece of a row of x, and the rows that it loads; rows past the last read it
   constexpr int kXLanes = CH / 8;
   const int x_piece = lane % kXLanes;
-  int64_t x_at[Ring::kXLoads > 0 ? Ring::kXLoads : 1];
-  auto x_row = [&](int i) { return min((int64_t)(i * (64 / kXLanes) + lane / kXLanes), l.rows - 1); };
+  auto x_row = [&](int ln, int i) { return (uint32_t)min(i * (64 / kXLanes) + ln / kXLanes, rows - 1); };
+  // (8-bit rows are dense and 2^31 elements at most in all: offsets of 32 bits, kept, and
+  // hidden where the compiler, which would keep addresses, has not the registers; 2 tiles
+  // of 32 rows are 5 % faster with them)
+  uint32_t x_at8[Ring::kXLoads > 0 ? Ring::kXLoads : 1];
+  if constexpr (XT == kXE4M3) {
 #pragma unroll
-  for (int i = 0; i < Ring::kXLoads; ++i) x_at[i] = x_row(i) * l.x_stride + 8 * x_piece;
-  auto x_scale = [&](int i, int64_t k) { return XT == kXE4M3 ? x_row(i) * (K / 32) + (k >> 5) : 0; };
+    for (int i = 0; i < Ring::kXLoads; ++i) x_at8[i] = x_row(lane, i) * (uint32_t)K + 8u * x_piece;
+  }
+  auto load_x = [&](int c, int ln, int i, XPiece<XT>& d) {
+    if constexpr (XT == kXE4M3) {
+      uint32_t at = x_at8[i];
+      if constexpr (NT * MT > 4) asm volatile("" : "+v"(at));
+      const u32x2_t v = load_any<u32x2_t>(static_cast<const uint8_t*>(l.x) + (int64_t)c * CH + at);
+      d.w[0] = v.x;
+      d.w[1] = v.y;
+      d.w[2] = (l.x_scales + (int64_t)c * (CH / 32))[at >> 5];
+    } else {
+      load_piece<XT>(l, (int64_t)(x_row(ln, i) * (uint64_t)l.x_stride) + 8 * (ln % kXLanes) + (int64_t)c * CH, 0, d);
+    }
+  };
 
   const int whole = (int)(K / CH), chunks = (int)((K + CH - 1) / CH);
   auto load = [&](int c, Ring& d) {           // a whole chunk
+    const int ln = this_lane();
 #pragma unroll
-    for (int i = 0; i < Ring::kXLoads; ++i)
-      load_piece<XT>(l, x_at[i] + (int64_t)c * CH, x_scale(i, (int64_t)c * CH + 8 * x_piece), d.x[i]);
+    for (int i = 0; i < Ring::kXLoads; ++i) load_x(c, ln, i, d.x[i]);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) d.c[t][i] = load_codes<CH>(wc[t][i] + (int64_t)c * (CH / 2));
-      d.s[t] = load_small<kLane>(ws[t] + (int64_t)c * kScales);
+      for (int i = 0; i < kLoads; ++i) d.c[t][i] = load_codes<CH>(codes_at(ln, t, i) + (int64_t)c * (CH / 2));
+      d.s[t] = load_small<kLane>(scales_at(ln, t) + (int64_t)c * kScales);
     }
   };
   auto load_end = [&](int c, Ring& d) {       // the chunk that the rows end in, zeros behind them
+    const int ln = this_lane();
 #pragma unroll
     for (int i = 0; i < Ring::kXLoads; ++i) {
       const int64_t k = (int64_t)c * CH + 8 * x_piece;             // (K is a multiple of 8)
-      if (k < K) load_piece<XT>(l, x_at[i] + (int64_t)c * CH, x_scale(i, k), d.x[i]);
+      if (k < K) load_x(c, ln, i, d.x[i]);
       else no_piece<XT>(d.x[i]);
     }
     const int64_t k0 = (int64_t)c * CH, v = K - k0 - 32 * piece_at;    // v: what this lane's 32 codes have of them
@@ -201,7 +228,7 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         d.c[t][i] = u32x4_t{0u, 0u, 0u, 0u};
-        const uint8_t* p = wc[t][i] + k0 / 2;
+        const uint8_t* p = codes_at(ln, t, i) + k0 / 2;
         if (v >= 32) {
           d.c[t][i] = load_any<u32x4_t>(p);
         } else if (v >= 16) {
@@ -213,7 +240,7 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(FewArgs a) {
       d.s[t] = 0u;
 #pragma unroll
       for (int i = 0; i < kLane; ++i)
-        if (i < have) d.s[t] |= (uint32_t)ws[t][(int64_t)c * kScales + i] << (8 * i);
+        if (i < have) d.s[t] |= (uint32_t)scales_at(ln, t)[(int64_t)c * kScales + i] << (8 * i);
     }
   };
   f32x4_t acc[NT][MT];
@@ -395,24 +422,23 @@ hipError_t launch_t(const LinearLaunch& l, int log_kp, hipStream_t s) {
 
 // 17 to 48 rows: two tiles a workgroup, or four or six, by the workgroups that CUs
 // take one after another (LDS holds one at a time), each as long as its tiles and one
-// and a half, for x.  Measured, MXFP4 (NVFP4), k 4096, us, 24 rows / 40 rows:
+// and a half, for x.  Measured, MXFP4 (NVFP4) with bf16, k 4096, us, 24 rows / 40 rows
+// (MXFP8 is 0 to 15 % slower, in the same order):
 //   n       two tiles                  four                       six
-//   4096     7.7 (8.9) /  9.7 (10.8)    9.4 (12.2) / 11.9 (14.8)  11.5 (17.1) / 18.3 (31.3)
-//   16384   14.0 (17.2) / 18.1 (20.9)  11.8 (14.0) / 13.7 (16.7)  14.3 (19.7) / 21.2 (36.2)
-//   20000 (gated, 40 rows): 25.4, 23.7, 21.1
-// Six with 33 rows and more want more registers than there are: MXFP4 with bf16
-// alone takes them (52 spilled).
+//   4096     7.5 (7.8) /  8.8 (9.4)     9.1 (10.1) / 12.5 (13.9)  12.6 (15.5) / 15.7 (18.2)
+//   16384   13.9 (15.6) / 17.7 (19.1)  10.7 (12.5) / 14.4 (16.2)  13.9 (17.3) / 17.0 (19.8)
+//   20000   18.5 (21.7) / 24.5 (26.8)  18.1 (20.9) / 23.8 (28.0)  14.3 (17.2) / 17.2 (19.9)
+//   28672   23.5 (28.4) / 31.7 (35.0)  18.9 (21.9) / 24.8 (28.8)  24.7 (31.4) / 30.3 (36.4)
+// (Six are the ones for widths that four would give a few CUs more turns: 16400 to
+// 24600 of 256 CUs.)
 template <int FMT, int XT, int MT, bool GATED>
 hipError_t launch_nt(const LinearLaunch& l, hipStream_t s) {
-  constexpr bool kSix = MT == 2 || (FMT == 0 && XT == kXBF16);
   const int64_t cus = device_cu_count();
   auto cost = [&](int nt) {
     const int64_t groups = (l.w.n + 16 * nt - 1) / (16 * nt);
     return (groups + cus - 1) / cus * (3 + 2 * nt);
   };
-  if constexpr (kSix) {
-    if (cost(6) < cost(4) && cost(6) < cost(2)) return launch_t<FMT, XT, MT, 6, 128, 1, GATED, false>(l, 0, s);
-  }
+  if (cost(6) < cost(4) && cost(6) < cost(2)) return launch_t<FMT, XT, MT, 6, 128, 1, GATED, false>(l, 0, s);
   if (cost(4) < cost(2)) return launch_t<FMT, XT, MT, 4, 128, 1, GATED, false>(l, 0, s);
   return launch_t<FMT, XT, MT, 2, 128, 1, GATED, false>(l, 0, s);
 }

@@ -17,6 +17,7 @@ extern "C" int scales_fit(int gated, int64_t n, int64_t k) { return fp4q::ring_s
 extern "C" unsigned grid_x(int64_t groups) { return fp4q::grid_x(groups); }
 extern "C" unsigned grid_y(int64_t groups) { return fp4q::grid_y(groups); }
 extern "C" int tiles_fit(int64_t tiles) { return fp4q::tiles_fit(tiles); }
+extern "C" int few_eight_fits(int64_t rows, int64_t k) { return fp4q::few_eight_fits(rows, k); }
 extern "C" int64_t grid_row() { return fp4q::kGridRow; }
 """
 
@@ -33,6 +34,7 @@ def sizes(tmp_path_factory):
     lib.scales_fit.argtypes = [C.c_int, C.c_int64, C.c_int64]
     for f in (lib.grid_x, lib.grid_y, lib.tiles_fit):
         f.argtypes = [C.c_int64]
+    lib.few_eight_fits.argtypes = [C.c_int64, C.c_int64]
     lib.grid_x.restype = lib.grid_y.restype = C.c_uint
     lib.grid_row.restype = C.c_int64
     return lib
@@ -95,3 +97,11 @@ def test_more_tiles_than_a_launch_takes_are_refused(lib, kind):
     call = (lib.fp4q_linear, lib.fp4q_gated, lib.fp4q_linear_backward)[kind]
     assert call(w, linear_args(rows=rows, x_stride=16), None, 0, None) == UNSUPPORTED
     assert lib.fp4q_linear_workspace_bytes(w, linear_args(rows=rows, x_stride=16), kind) == 0
+
+
+def test_eight_bit_rows_of_the_few_row_kernel(sizes):
+    """Its last element's offset stays below 2^31, and one row of any length is taken."""
+    for k in (32, 4096, 1 << 20, (1 << 25) - 32, 1 << 25, (1 << 31) - 32):
+        for rows in (1, 2, 16, 63, 64):
+            assert bool(sizes.few_eight_fits(rows, k)) == (rows * k < 1 << 31)
+    assert sizes.few_eight_fits(1, (1 << 31) - 32)
