@@ -47,8 +47,8 @@ __device__ __forceinline__ T load_wide(const uint8_t* p) {
 // Eight elements of a row from element c on, zeros past its end.  NT: not kept in
 // the caches.
 template <bool BF16, bool NT = false>
-__device__ __forceinline__ void load8(const void* row, int64_t c, int64_t d, float (&v)[8]) {
-  const uint8_t* p = static_cast<const uint8_t*>(row) + c * (BF16 ? 2 : 4);
+__device__ __forceinline__ void load8(const void* row, uint32_t c, uint32_t d, float (&v)[8]) {
+  const uint8_t* p = static_cast<const uint8_t*>(row) + c * (BF16 ? 2u : 4u);
   if (c + 8 <= d) {
     if constexpr (BF16) {
       const u32x4_t w = load_wide<u32x4_t, NT>(p);
@@ -75,8 +75,8 @@ __device__ __forceinline__ void load8(const void* row, int64_t c, int64_t d, flo
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void* row, int64_t c, int64_t d, const float (&v)[8]) {
-  uint8_t* p = static_cast<uint8_t*>(row) + c * (BF16 ? 2 : 4);
+__device__ __forceinline__ void store8(void* row, uint32_t c, uint32_t d, const float (&v)[8]) {
+  uint8_t* p = static_cast<uint8_t*>(row) + c * (BF16 ? 2u : 4u);
   if (c + 8 <= d) {
     if constexpr (BF16) {
       store_any(p, u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
@@ -189,14 +189,21 @@ __global__ __launch_bounds__(T, T <= 512 ? 4 : 1) void norm_grad_kernel(NormGrad
   __shared__ float s_sum[T / 64];
   const int t = threadIdx.x;
   float dw[NS][8], w[kHeld][8];
-  auto column = [&](int i) { return (int64_t)(i * T + t) * 8; };
+  const uint32_t d = (uint32_t)l.d;
+  // Hidden for each row where registers run out: else the compiler keeps all columns'
+  // comparisons with the row's end, and spilled (2048 rows of 32768, bf16: 263 us, so
+  // 163; 4096 of 8192, 57 and 54; shorter rows, which fit, are up to 15 % slower with it).
+  constexpr bool kHide = T == 512 || NS == 4;
+  int tt = t;
+  auto column = [&](int i) { return (uint32_t)(i * T + tt) * 8; };
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    if constexpr (!AGAIN) load8<WBF16>(l.w, column(i), l.d, w[i]);
+    if constexpr (!AGAIN) load8<WBF16>(l.w, column(i), d, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
   for (int64_t row = blockIdx.x; row < l.rows; row += gridDim.x) {
+    if constexpr (kHide) asm volatile("" : "+v"(tt));
     const void* dyr = at_row<BF16>(l.dy, row, l.dy_stride);
     const void* sr = at_row<BF16>(l.s, row, l.s_stride);
     const float rstd = l.rstd[row];
@@ -204,17 +211,17 @@ __global__ __launch_bounds__(T, T <= 512 ? 4 : 1) void norm_grad_kernel(NormGrad
     if constexpr (!AGAIN) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        load8<BF16>(dyr, column(i), l.d, g[i]);
-        load8<BF16>(sr, column(i), l.d, hat[i]);
+        load8<BF16>(dyr, column(i), d, g[i]);
+        load8<BF16>(sr, column(i), d, hat[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int h = AGAIN ? 0 : i;
       if constexpr (AGAIN) {
-        load8<BF16>(dyr, column(i), l.d, g[0]);
-        load8<BF16>(sr, column(i), l.d, hat[0]);
-        load8<WBF16>(l.w, column(i), l.d, w[0]);
+        load8<BF16>(dyr, column(i), d, g[0]);
+        load8<BF16>(sr, column(i), d, hat[0]);
+        load8<WBF16>(l.w, column(i), d, w[0]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -225,14 +232,15 @@ __global__ __launch_bounds__(T, T <= 512 ? 4 : 1) void norm_grad_kernel(NormGrad
       }
     }
     along = row_sum<T>(along, s_sum, true) / (float)l.d;
+    if constexpr (kHide && AGAIN) asm volatile("" : "+v"(tt));
     uint8_t* to = static_cast<uint8_t*>(l.dx) + row * l.d * (BF16 ? 2 : 4);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int h = AGAIN ? 0 : i;
       if constexpr (AGAIN) {
-        load8<BF16>(dyr, column(i), l.d, g[0]);
-        load8<BF16>(sr, column(i), l.d, hat[0]);
-        load8<WBF16>(l.w, column(i), l.d, w[0]);
+        load8<BF16>(dyr, column(i), d, g[0]);
+        load8<BF16>(sr, column(i), d, hat[0]);
+        load8<WBF16>(l.w, column(i), d, w[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           hat[0][j] *= rstd;
@@ -241,19 +249,19 @@ __global__ __launch_bounds__(T, T <= 512 ? 4 : 1) void norm_grad_kernel(NormGrad
       }
       float u[8];
       if (l.ds) {
-        load8<BF16>(at_row<BF16>(l.ds, row, l.ds_stride), column(i), l.d, u);
+        load8<BF16>(at_row<BF16>(l.ds, row, l.ds_stride), column(i), d, u);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[j] = fmaf(rstd, g[h][j] - hat[h][j] * along, u[j]);
-      store8<BF16>(to, column(i), l.d, u);
+      store8<BF16>(to, column(i), d, u);
     }
   }
   float* part = l.partials + (int64_t)blockIdx.x * l.d;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) store8<false>(part, column(i), l.d, dw[i]);
+  for (int i = 0; i < NS; ++i) store8<false>(part, column(i), d, dw[i]);
 }
 
 // dw = the sum of the parts: a workgroup 64 columns, its 16 waves every sixteenth

@@ -10,7 +10,7 @@ import pytest
 from fp4_block_scaled_row_amd import build
 
 SOURCES = ["fp4q_linear.hip", "fp4q_linear_few.hip", "fp4q_linear_many_mx.hip", "fp4q_linear_many_nv.hip",
-           "fp4q_linear_many_back_mx.hip", "fp4q_linear_many_back_nv.hip", "fp4q_linear_mx8.hip"]
+           "fp4q_linear_many_back_mx.hip", "fp4q_linear_many_back_nv.hip", "fp4q_linear_mx8.hip", "fp4q_norm.hip"]
 
 
 @pytest.fixture(scope="module")
