@@ -16,7 +16,8 @@
 // conversions give NaN for scale byte 255, the E4M3 one for 0x7F).  bf16
 // activations are exact too.  An fp32 one is the sum of three bf16 pieces of 8
 // bits each, cut off rather than rounded, so that the sum is exact and no piece
-// passes the type's range.  The tensor scale's power of two goes into the weights,
+// passes the type's range.  (From 2^-110 on: of smaller ones the last pieces fall
+// under bf16's least number, 2^-133, and less than that is lost of an element.)  The tensor scale's power of two goes into the weights,
 // exactly, so that sums are of the results' size; what is left of it, in [1, 2),
 // multiplies the sums.  Those are fp32; bias and activation are applied in fp32, and
 // outputs rounded once.
@@ -220,7 +221,8 @@ __device__ __forceinline__ u32x4_t e4m3_values8(u32x2_t codes, uint32_t scale) {
 }
 
 // The three bf16 pieces of eight fp32 values: the upper 16 bits of what is left
-// each time, which leaves nothing after three.  An infinity or NaN is its own
+// each time, which leaves nothing after three where the values' last bits are
+// 2^-133 or more, bf16's least number, and less than that elsewhere.  An infinity or NaN is its own
 // first piece (a NaN made quiet, so that the cut keeps it one) and leaves zeros.
 __device__ __forceinline__ void split8(const uint32_t v[8], u32x4_t out[3]) {
   uint32_t h[8], m[8], l[8];

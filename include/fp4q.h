@@ -424,7 +424,9 @@ enum { FP4Q_LINEAR = 0, FP4Q_GATED = 1, FP4Q_LINEAR_BACKWARD = 2 };
  * after a call mean nothing; calls that overlap on the GPU need one each. */
 size_t fp4q_linear_workspace_bytes(const fp4q_weight *weight, const fp4q_linear_args *args, int32_t kind);
 
-/* out [rows][n] = x W^T + bias.  Weights and activations enter exactly, sums are
+/* out [rows][n] = x W^T + bias.  Weights and activations enter exactly, down to
+ * bf16's least number: of fp32 elements below 2^-110 less than 2^-133 may be lost, and
+ * MXFP8 elements are what fp4q_dequantize gives in bf16.  Sums are
  * fp32 in an order that the shapes fix (a call gives the same bits each time),
  * the tensor scale and the bias are applied in fp32 (the scale's power of two to the
  * weights, exactly, so that sums pass fp32's range only where results do), and the

@@ -80,3 +80,44 @@ def test_tensor_scales_that_are_no_numbers(fq, rows, g):
     one = fq.fp4_linear(x, handle(fq, "nvfp4", (codes, scales, 1.0)), out_dtype=torch.float32)
     got = fq.fp4_linear(x, handle(fq, "nvfp4", (codes, scales, g)), out_dtype=torch.float32)
     assert torch.equal(torch.nan_to_num(got, nan=7.0), torch.nan_to_num(one * g, nan=7.0))
+
+
+# fp32 rows enter as three bf16 pieces, cut off.  From 2^-110 on the pieces sum to the row's elements; below, what lies
+# under bf16's least number, 2^-133, is lost: less than that of each element.
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows,n,k", [(4, 96, 320), (16, 64, 8192), (80, 96, 2112), (1030, 4200, 192)])
+@pytest.mark.parametrize("low", [-109, -118, -126, -140])
+def test_smallest_fp32_rows(fq, fmt, rows, n, k, low):
+    rng = np.random.default_rng(rows)
+    codes, scales, _ = weight(rng, fmt, n, k)
+    g = 1.3 * 2.0 ** 90 if fmt == "nvfp4" else None
+    if fmt == "mxfp4":
+        scales = (scales + 90).astype(np.uint8)
+    planes = codes, scales, g
+    # magnitudes of all bits, from 2^low to 2^(low + 1)
+    x = np.ldexp(rng.choice([-1.0, 1.0], (rows, k)) * rng.uniform(1, 2, (rows, k)), low).astype(np.float32)
+    dy = np.ldexp(rng.choice([-1.0, 1.0], (rows, n)) * rng.uniform(1, 2, (rows, n)), low).astype(np.float32)
+    h = handle(fq, fmt, planes)
+    y, dx = fq.fp4_linear(torch.from_numpy(x).cuda(), h), fq.fp4_linear_backward(torch.from_numpy(dy).cuda(), h)
+    torch.cuda.synchronize()
+    w = values(fmt, (codes, scales, 1.0 if fmt == "nvfp4" else None)) * (1.0 if g is None else float(np.float32(g)))
+    lost = 0.0 if low >= -110 else 2.0 ** -133
+    for got, v, a, terms in ((y, x.astype(np.float64), w.T, k), (dx, dy.astype(np.float64), w, n)):
+        want, S = v @ a, np.abs(v) @ np.abs(a)
+        check(got, want, sum_bound(S, terms, 3) + lost * np.abs(a).sum(0) + HALF[torch.float32] * np.abs(want))
+
+
+@pytest.mark.parametrize("rows", [3, 40, 70, 1030])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_smallest_mx_elements(fq, rows, kind):
+    """MXFP4 elements below bf16's normal range are exact: 2^-128 is the least."""
+    rng = np.random.default_rng(7)
+    n, k = 4200 if rows > 100 else 96, 192
+    codes, _, _ = weight(rng, "mxfp4", n, k)
+    scales = rng.integers(0, 3, (n, k // 32), dtype=np.uint8)
+    x, xv, pieces = activations(rng, fq, kind, rows, k)
+    y = fq.fp4_linear(powers(x, 100), handle(fq, "mxfp4", (codes, scales, None)), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    w, xv = values("mxfp4", (codes, scales, None)), np.ldexp(xv, 100)
+    want, S = xv @ w.T, np.abs(xv) @ np.abs(w).T
+    check(y, want, sum_bound(S, k, pieces) + HALF[torch.float32] * np.abs(want))
