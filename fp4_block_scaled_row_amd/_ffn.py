@@ -6,6 +6,16 @@ fp4q_rms_norm and their backward calls of include/fp4q.h).
 Activations are bf16, fp32, or MXFP8 (Mx8Result, as rms_norm writes it): E4M3
 codes with one power-of-two scale for each 32.  Weights and activations enter
 the products exactly, sums are fp32, results are rounded once.
+
+One exception: MXFP8 activations with MXFP4 weights, many rows and results in bf16
+alone go through the block-scaled matrix instructions, whose sums of eight
+neighbouring products may lose what lies below 2^-13 of the largest of them (over a
+whole output that is below bf16's rounding).  Who wants fp32 sums there asks for
+out_dtype=torch.float32.
+
+The same call on the same tensors gives the same bits each time.  Which kernel a
+call takes, and so the order of its sums, goes by shapes, types, x's row stride, the
+alignment of the planes, and whether products are asked for and in which type.
 """
 from collections import namedtuple
 
@@ -163,9 +173,9 @@ def fp4_linear(x, w, *, bias=None, out_dtype=None, out=None):
     """x W^T (+ bias): x [rows, k] bf16 or fp32 (any row stride), or an Mx8Result;
     w an Fp4Weight [n, k].
 
-    Returns [rows, n] in out_dtype: x's by default, bf16 for MXFP8.  bias: [n] of
-    that dtype, added before the one rounding.  Calls of a shape give the same bits
-    each time."""
+    Returns [rows, n] in out_dtype: x's by default, bf16 for MXFP8 (with an MXFP4
+    weight and many rows by sums of fewer bits, see this module; torch.float32 has
+    fp32 ones).  bias: [n] of that dtype, added before the one rounding."""
     _weight(w)
     _, fields, dtype = _activations(x, w, out_dtype)
     code = _out_dtype(dtype)
@@ -197,7 +207,9 @@ def fp4_gated(x, w, *, return_products=False, products_dtype=torch.float32, out_
     Returns [rows, f], or with return_products (out, products): products [rows,
     2 f], the two products side by side, which fp4_gated_backward takes: the fp32
     sums, or with products_dtype=torch.bfloat16 their rounding, which halves what a
-    training step keeps and moves the gradients by it (2^-8 of a product)."""
+    training step keeps and moves the gradients by it (2^-8 of a product).  With
+    MXFP8 x and an MXFP4 weight the call without products, or with bf16 ones, may
+    take sums of fewer bits than the one with fp32 products (see this module)."""
     _weight(w)
     if w.n % 2:
         raise ValueError("fp4q: a gated weight has an even number of rows, got %d" % w.n)

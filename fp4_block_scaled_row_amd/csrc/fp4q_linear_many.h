@@ -580,8 +580,8 @@ __global__ __launch_bounds__(64 * NW, 2) void ring_kernel(ManyArgs a) {
 }
 
 // Whether rows are whole stages and offsets small enough, and whether the pieces of
-// them are aligned.  (The plan asks the sizes alone: a workspace is asked for before
-// the call.)
+// them are aligned.  (Parts of the contraction go by the sizes alone, and rows whose
+// pieces lie between words then go through many_kernel in the same parts.)
 inline bool ring_sizes(const LinearLaunch& l) {
   return l.x_type == kXBF16 && l.w.k > 0 && l.w.k % kStage == 0 && l.w.n % (l.transposed ? kStage : 1) == 0 &&
          l.w.k <= 1 << 22 && ring_scales_fit(l.gated, l.w.n, l.w.k);

@@ -426,13 +426,22 @@ size_t fp4q_linear_workspace_bytes(const fp4q_weight *weight, const fp4q_linear_
 
 /* out [rows][n] = x W^T + bias.  Weights and activations enter exactly, down to
  * bf16's least number: of fp32 elements below 2^-110 less than 2^-133 may be lost, and
- * MXFP8 elements are what fp4q_dequantize gives in bf16.  Sums are
- * fp32 in an order that the shapes fix (a call gives the same bits each time),
- * the tensor scale and the bias are applied in fp32 (the scale's power of two to the
+ * MXFP8 elements are what fp4q_dequantize gives in bf16.  Sums are fp32; the
+ * tensor scale and the bias are applied in fp32 (the scale's power of two to the
  * weights, exactly, so that sums pass fp32's range only where results do), and the
- * result is rounded once.  A NaN scale makes its terms NaN.  With MXFP8 activations, MXFP4 weights
- * and results in bf16 alone, sums of eight neighbouring products may lose what lies
- * below 2^-13 of the largest of them. */
+ * result is rounded once.  A NaN scale makes its terms NaN.
+ *
+ * The same call on the same arguments gives the same bits each time.  The order of
+ * sums goes by the shapes, the types (of the results and products too), x's stride,
+ * whether the planes lie on the loads' alignment (x and codes on 16 bytes, scales on
+ * 4), and the card's number of compute units: calls that differ in one of these, as
+ * fp4q_gated with products and without them, may differ by the sums' rounding.
+ *
+ * One exception to fp32 sums: MXFP8 activations with MXFP4 weights, results (and
+ * products) in bf16 alone, of many rows and k a multiple of 128.  There sums of eight
+ * neighbouring products may lose what lies below 2^-13 of the largest of them, less
+ * than 7 2^-13 of the sum of the products' magnitudes in all.  With out_dtype FP4Q_F32
+ * sums are fp32 whatever the operands. */
 fp4q_status fp4q_linear(const fp4q_weight *weight, const fp4q_linear_args *args, void *workspace,
                         size_t workspace_bytes, void *hip_stream);
 
@@ -481,7 +490,8 @@ typedef struct {
  * with the scale 2^(floor(log2(largest)) - 8) (the OCP max rule for E4M3;
  * exponents clamp at -127, an all-zero block has 2^0), elements rounded to
  * nearest even, past 448 to 448; a block with an infinity or NaN gets the NaN
- * scale and zero codes. */
+ * scale and zero codes.  Squares are summed in fp32: a row whose sum of squares passes
+ * its range has r = 0, and one whose sum falls under it has that of eps alone. */
 fp4q_status fp4q_rms_norm(const fp4q_rms_norm_args *args, void *hip_stream);
 
 typedef struct {
@@ -501,7 +511,7 @@ size_t fp4q_rms_norm_backward_workspace_bytes(const fp4q_rms_norm_grad_args *arg
 
 /* With h = s r and g = dy weight: dx = r (g - h mean(g h)) + ds, the gradient of
  * s (and so of x and of residual), and dw = sum over rows of dy h, in an order
- * that the shapes fix.  fp32, rounded once. */
+ * that the shapes and the card's number of compute units fix.  fp32, rounded once. */
 fp4q_status fp4q_rms_norm_backward(const fp4q_rms_norm_grad_args *args, void *workspace, size_t workspace_bytes,
                                    void *hip_stream);
 
