@@ -230,7 +230,9 @@ def fp4_gated_backward(dh, products, w):
     """(dx, dproducts): the gradients of fp4_gated's x, [rows, k], and of its
     products, [rows, 2 f] (what adapters beside the weight need), from that of its
     result, dh [rows, f] bf16 or fp32, and the products that it returned.  Both in
-    dh's dtype; dx is that of the returned dproducts."""
+    dh's dtype; dx is that of the returned dproducts: with bf16 ones it has their
+    rounding and its own (2.3e-3 of it as a whole, where one is 1.7e-3).  Who wants
+    one rounding alone passes dh.float() and rounds dx."""
     _weight(w)
     if w.n % 2:
         raise ValueError("fp4q: a gated weight has an even number of rows, got %d" % w.n)
