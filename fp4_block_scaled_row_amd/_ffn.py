@@ -16,6 +16,20 @@ out_dtype=torch.float32.
 The same call on the same tensors gives the same bits each time.  Which kernel a
 call takes, and so the order of its sums, goes by shapes, types, x's row stride, the
 alignment of the planes, and whether products are asked for and in which type.
+
+As everywhere in this package, calls record no gradients: results require none,
+whatever the arguments do.  A training program joins a forward and a backward call in
+an autograd.Function of its own:
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            ctx.w = w
+            return fp4_linear(x, w)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return fp4_linear_backward(dy.contiguous(), ctx.w), None
 """
 from collections import namedtuple
 
@@ -190,8 +204,8 @@ def fp4_linear(x, w, *, bias=None, out_dtype=None, out=None):
 
 def fp4_linear_backward(dy, w, *, out=None):
     """dy W: the gradient of fp4_linear's x from that of its result, dy [rows, n]
-    bf16 or fp32.  Returns [rows, k] in dy's dtype.  (The weight is frozen; the
-    gradient of a bias is dy.sum(0).)"""
+    bf16 or fp32, rows contiguous.  Returns [rows, k] in dy's dtype.  (The weight is
+    frozen; the gradient of a bias is dy.sum(0).)"""
     _weight(w)
     rows, stride, code = _rows(dy, "dy", w._index, w.n)
     out = _buffer(out, "out", (rows, w.k), dy.dtype, w.device, dy, w.codes, w.scales, w.global_scale)
