@@ -145,7 +145,7 @@ __device__ __forceinline__ float scale_operand(uint32_t byte) {
 // The tensor scale in two factors: a power of two that the conversions below
 // multiply into the elements, held to 2^-116 .. 2^115, with which the least of them
 // (2^-10) is normal in bf16 and the largest (2688) finite; and the rest, which is
-// exact.  A scalar load: it is one of none that the vector loads' counts mean.
+// exact.  (A scalar load: the rings count the vector loads that are on their way.)
 __device__ __forceinline__ float tensor_scale(const float* g) {
   typedef const __attribute__((address_space(4))) float* constant_t;
   return *(constant_t)reinterpret_cast<uintptr_t>(g);
